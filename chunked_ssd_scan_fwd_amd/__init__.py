@@ -9,15 +9,22 @@ raises when it is used.
 
 Layouts (float32, contiguous):
     q, k [B,G,T,dk]   v, dy [B,H,T,dv]   log_alpha [B,H,T]   h0 [B,H,dk,dv]
+
+The operators of a linear-attention layer (packed prefill, one-token step,
+group norm, 8-bit state cache) are in ``layer``; they too take float32 states
+and log decays, and their activations may be bfloat16 or float16.
 """
 from __future__ import annotations
 
 import ctypes
 import os
 
+from . import layer
+from .layer import gn_bwd, gn_fwd, lin_prefill, lin_step, state_pack, state_unpack
+
 __all__ = ["fwd", "bwd", "library", "ShapeArg", "SsdError", "workspace_size",
            "workspace_layout", "KernelTimer", "CHUNK", "bwd_from_fwd", "WS_REGIONS", "fwd_noalloc",
-           "NOALLOC_WORKSPACE_BYTES"]
+           "NOALLOC_WORKSPACE_BYTES", "lin_prefill", "lin_step", "gn_fwd", "gn_bwd", "state_pack", "state_unpack"]
 
 CHUNK = 64
 WS_REGIONS = 4   # SSD_WS_REGIONS: decay weights, states, dstates, split partial sums
@@ -95,6 +102,7 @@ def library(path: str | None = None):
     lib.mamba_bwd.restype = ctypes.c_int
     lib.mamba_fwd_bwd.argtypes = [mp] + [vp] * 14 + [vp, sz, vp]
     lib.mamba_fwd_bwd.restype = ctypes.c_int
+    layer.declare(lib)
     if path is None:
         _lib = lib
     return lib

@@ -350,6 +350,151 @@ int mamba_fwd_bwd(const mamba_shape *shape,
                   float *y, float *dx, float *ddelta, float *dA, float *dB, float *dC, float *dDskip,
                   void *workspace, size_t workspace_bytes, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * Operators of a linear-attention layer: the scan above as a server runs it
+ * (a packed batch of prompts, then one token at a time, over a pool of
+ * states), the group norm that follows it in the layer, and an 8-bit cache
+ * of states.
+ *
+ * Types.  `dtype` is the element type of q, k, v, y (x, dy, gate, dx, dgate);
+ * states, log decays, weights, statistics and all sums are float32.  Outputs
+ * are rounded to `dtype` once.
+ *
+ * Ownership, asynchrony and status codes are those of ssd_fwd, with these
+ * differences: pointers need the alignment of their element type only (16
+ * bytes for workspaces; aligned rows are read 16 bytes at a time); the
+ * workspace is a caller's own and must not be shared by calls that may run
+ * at the same time, two captured graphs among them; index arrays are device
+ * memory and are read when the work runs, so they are checked by the kernels
+ * (each call says how) and no index outside its array is ever followed.
+ * Nothing is allocated and nothing waits, so every call can be captured into
+ * a graph.  Results are the same from run to run. */
+enum layer_dtype { LAYER_F32 = 0, LAYER_BF16 = 1, LAYER_F16 = 2 };
+
+/* T rows of q, k, v and y; N sequences; `slots` states in the pool. */
+typedef struct lin_shape {
+    int64_t T, N, G, H, dk, dv, slots;
+} lin_shape;
+
+/* Strides in elements between the rows (tokens) and between the heads or
+ * groups of a row; the last axis is dense.  A null pointer in place of the
+ * struct stands for dense [T,G,dk] and [T,H,dv]. */
+typedef struct lin_strides {
+    int64_t q_t, q_g, k_t, k_g, v_t, v_h, y_t, y_h;
+} lin_strides;
+
+/* Workspace bytes lin_prefill needs on the current device for `shape` and
+ * `max_seqlen`: 0 where no sequence is cut; (size_t)-1 for a shape that it
+ * refuses. */
+size_t lin_prefill_workspace_size(const lin_shape *shape, int64_t max_seqlen);
+
+/* The scan of a packed batch.  Sequence n is rows cu_seqlens[n] ..
+ * cu_seqlens[n+1]-1 (int32 [N+1], rising, within 0..T; values outside are
+ * clamped); rows of no sequence are not read, and their y is left as it was.
+ * For each sequence and head h, with g = h / (H/G),
+ *     S_t = exp(log_decay_t) S_{t-1} + k_t v_t^T,   y_t = S_t^T q_t,
+ * in chunks, from the state in slot slots[n] of `states` [slots][H][dk][dv]
+ * (from zero where carry[n] is 0); the state after the last row is written
+ * back to the slot.  A sequence of no rows leaves its slot as it was, or
+ * zero where carry[n] is 0.
+ *   log_decay     float32: [H], one for each head, when decay_stride is 0;
+ *                 else rows of H, decay_stride apart, one for each token.
+ *                 Finite, or -inf (the state is forgotten); positive values
+ *                 are growth, and overflow is the caller's risk.
+ *   slots         int32 [N]; NULL: sequence n has slot n (N <= slots).
+ *                 Negative: the sequence starts from zero and its state is
+ *                 not kept.  Not below `slots`, or the slot of an earlier
+ *                 sequence of the call: its y is NaN and no state is written.
+ *   carry         int32 [N]; NULL: every sequence continues its slot's state.
+ *   max_seqlen    an upper bound of the lengths, 0 if unknown (then T).  It
+ *                 only chooses how the work is split; a sequence that is
+ *                 longer all the same is still computed.
+ * Infinite and NaN values of a sequence's rows stay within that sequence,
+ * and reach rows up to 63 positions before their own.
+ * dk, dv in 1..256 (else SSD_ERR_UNSUPPORTED), G >= 1, H % G == 0,
+ * T < 2^31, N and slots < 2^24, row strides below 2^24 elements, and strides
+ * of y that let no two of its values overlap (else SSD_ERR_SHAPE). */
+int lin_prefill(const lin_shape *shape, int dtype, const lin_strides *strides,
+                const void *q, const void *k, const void *v,
+                const float *log_decay, int64_t decay_stride,
+                const int32_t *cu_seqlens, const int32_t *slots, const int32_t *carry,
+                int64_t max_seqlen, float *states, void *y,
+                void *workspace, size_t workspace_bytes, void *stream);
+
+/* One step of the same recurrence for each of N rows (T is not read): row n
+ * of q, k, v and y belongs to slot slots[n], whose state it updates in place.
+ * Rows of one slot take effect in their order.  A row whose slot is negative
+ * is padding: its y is left as it was.  Not below `slots`: its y is NaN.
+ * log_decay: [H], or rows of H for the N rows, as above. */
+int lin_step(const lin_shape *shape, int dtype, const lin_strides *strides,
+             const void *q, const void *k, const void *v,
+             const float *log_decay, int64_t decay_stride,
+             const int32_t *slots, float *states, void *y, void *stream);
+
+/* Group norm, channels last, with an activation.  x is N samples of L rows
+ * of C channels; the channels are cut into `groups` runs of C / groups, and
+ * the mean mu and the variance (over the L rows and the run's channels, the
+ * mean of squares of x - mu) are taken for each sample and run.  With
+ * rstd = 1 / sqrt(variance + eps) and z = (x - mu) rstd weight + bias:
+ *     y = act(z)            without a gate
+ *     y = z act(gate)       with one
+ * where act is SiLU, u / (1 + e^-u), or nothing.  L = 1 with a group for each
+ * head is the norm that follows the scan.  weight, bias: float32 [C] or NULL
+ * (1 and 0).  stats [N][groups][2] receives mu and rstd.
+ * Row n L + l of x, gate, dy starts ld_* elements after the row before it
+ * (0: C); y, dx and dgate are dense.  C % groups == 0; N L C < 2^40, C and
+ * the strides below 2^24, L < 2^31. */
+typedef struct gn_shape {
+    int64_t N, L, C, groups;
+} gn_shape;
+enum gn_act { GN_ACT_NONE = 0, GN_ACT_SILU = 1 };
+
+size_t gn_fwd_workspace_size(const gn_shape *shape);
+int gn_fwd(const gn_shape *shape, int dtype, int act, float eps,
+           const void *x, int64_t ld_x, const float *weight, const float *bias,
+           const void *gate, int64_t ld_gate, void *y, float *stats,
+           void *workspace, size_t workspace_bytes, void *stream);
+
+/* The gradients of sum(dy * y): dx, dgate (with a gate), dweight and dbias
+ * [C] (each NULL if not wanted, dx too).  `stats` is what gn_fwd wrote for
+ * the same x, groups and eps.  Sums over samples and rows are taken in a
+ * fixed order. */
+size_t gn_bwd_workspace_size(const gn_shape *shape);
+int gn_bwd(const gn_shape *shape, int dtype, int act,
+           const void *x, int64_t ld_x, const float *weight, const float *bias,
+           const void *gate, int64_t ld_gate, const float *stats,
+           const void *dy, int64_t ld_dy,
+           void *dx, float *dweight, float *dbias, void *dgate,
+           void *workspace, size_t workspace_bytes, void *stream);
+
+/* A cache of states in 8 bits.  A row of dv values is cut into blocks of
+ * STATE_CACHE_BLOCK (the last may be shorter); a block is held as e4m3
+ * numbers (1 sign, 4 exponent, 3 fraction bits, largest 448) times 2^(s-127),
+ * s its scale byte.  cache [entries][H][dk][dv] bytes, scales
+ * [entries][H][dk][ceil(dv/32)] bytes.
+ *
+ * state_pack writes the states in slots[i] to the entries entries[i], i < n,
+ * with the smallest power of two that keeps the block's values within 448
+ * (at least 2^-127, which an all-zero block has), each value rounded to
+ * nearest, ties to even: off by 2^-4 of itself at most, or by 2^-10 times the scale
+ * below 2^-6 times the scale.  A block that holds an infinity or a NaN gets
+ * scale byte 255 and reads back as NaN.
+ * state_unpack writes the entries entries[i] to the slots slots[i]; one entry
+ * may go to several slots.
+ * In both, NULL in place of an index array stands for 0, 1, 2, ...; a pair
+ * with a negative index, or whose destination does not exist, is skipped; a
+ * source that does not exist makes the destination NaN; of pairs with one
+ * destination the last counts.  The states and the cache must not overlap.
+ * 1 <= dk, dv <= 256; n, slots and entries < 2^24. */
+#define STATE_CACHE_BLOCK 32
+typedef struct state_cache_shape {
+    int64_t n, slots, entries, H, dk, dv;
+} state_cache_shape;
+int state_pack(const state_cache_shape *shape, const float *states, const int32_t *slots,
+               const int32_t *entries, uint8_t *cache, uint8_t *scales, void *stream);
+int state_unpack(const state_cache_shape *shape, const uint8_t *cache, const uint8_t *scales,
+                 const int32_t *entries, const int32_t *slots, float *states, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
