@@ -1,70 +1,641 @@
-// The scalar-decay scan of a packed batch over a pool of states.
+// The scalar-decay scan of a packed batch over a pool of states, in chunks.
+//
+// With b_t the sum of a chunk's log decays up to row t, b_L its last value and
+// S the state entering the chunk,
+//   Y  = (Q K^T o D) V + diag(e^b) Q S,   D_ij = e^{b_i - b_j} for j <= i, else 0
+//   S <- e^{b_L} S + K^T diag(e^{b_L - b}) V.
+//
+// A block walks the chunks of one segment of a sequence for one head and VT
+// columns of v, with S in its registers: q, k, v are read once and y is
+// written once, and no chunk's state goes to memory.  Each of the four waves
+// owns VT / 4 columns of S, of Y and of V and all dk rows of S, so S never
+// crosses waves; only the masked scores P = Q K^T o D do, through LDS.
+//
+// Sequences longer than the plan's segment are cut: one pass leaves the state
+// each segment makes from zero, a second pass joins them into the states that
+// enter the segments, a third walks the segments from those.
+//
+// bfloat16 inputs run on bf16 MFMA, float32 and float16 ones on fp32 MFMA (a
+// float16 P or S would overflow or vanish where float32 does not).
+#include <type_traits>
+
 #include "layer_device.h"
+#include "ssd_device.h"
 
 namespace layer {
+
+using ssd::block_sync;
+using ssd::kOOB;
+using ssd::rsrc_t;
+using ssd::make_rsrc;
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int PT = 256;   // threads of a block: 4 waves
 
 struct PrefillArgs {
     const void *q, *k, *v;
     const float *la;
     const int32_t *cu, *slots, *carry;
-    float *states;
+    float *states, *ends, *segdec;   // ends [id][H][dk][dv], segdec [id][H]
     void *y;
     int64_t la_t;
     lin_strides st;
     int T, N, G, H, dk, dv, nslots, tiles;
+    int seg;       // rows of a segment; 0: sequences are not cut
+    int ids;       // blocks' segment numbers, T / seg + N
+    bool vec_qk, vec_v, vec_y;
 };
 
-constexpr int PT = 256;
+// ---- fragments of the matrix products
+//
+// A fragment is the 8 values a lane holds of a 16 x 32 operand: its row (or
+// column) is lane % 16, and the 8 values lie along the summed axis.  Which 8
+// is free as long as both operands agree.
 
-// The recurrence step by step: 64 columns of a head's state, a quarter of
-// its rows in each wave.
-template <typename T>
-__global__ __launch_bounds__(PT) void k_lin_prefill(PrefillArgs a)
+template <typename L>
+struct Frag;
+template <>
+struct Frag<bf16> {
+    bf16x8 x;
+};
+template <>
+struct Frag<float> {
+    float x[8];
+};
+
+__device__ __forceinline__ f32x4 mma(const Frag<bf16> &a, const Frag<bf16> &b, f32x4 c)
 {
-    __shared__ float red[2][PT / 64][64];
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    const int tile = blockIdx.x % a.tiles, h = blockIdx.x / a.tiles % a.H, n = blockIdx.x / (a.tiles * a.H);
-    const int g = h / (a.H / a.G), col = tile * 64 + lane;
-    const bool on = col < a.dv;
-    const int begin = min(max(a.cu[n], 0), a.T), end = min(max(a.cu[n + 1], begin), a.T);
-    const int sl = index_of(a.slots, n);
-    bool bad = sl >= a.nslots;
-    if (a.slots && sl >= 0)
-        for (int j = 0; j < n && !bad; ++j) bad = a.slots[j] == sl;
-    T *y = static_cast<T *>(a.y) + h * a.st.y_h;
-    if (bad) {
-        for (int t = begin + wave; t < end; t += PT / 64)
-            if (on) y[t * a.st.y_t + col] = from_f<T>(__builtin_nanf(""));
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.x, b.x, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4 mma(const Frag<float> &a, const Frag<float> &b, f32x4 c)
+{
+#pragma unroll
+    for (int j = 0; j < 8; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.x[j], b.x[j], c, 0, 0, 0);
+    return c;
+}
+
+// 8 values in a row.
+__device__ __forceinline__ Frag<bf16> frag8(const bf16 *p) { return {*reinterpret_cast<const bf16x8 *>(p)}; }
+__device__ __forceinline__ Frag<float> frag8(const float *p)
+{
+    Frag<float> r;
+    *reinterpret_cast<f32x4 *>(r.x) = *reinterpret_cast<const f32x4 *>(p);
+    *reinterpret_cast<f32x4 *>(r.x + 4) = *reinterpret_cast<const f32x4 *>(p + 4);
+    return r;
+}
+// Values 0..3 and 16..19 of a row.
+__device__ __forceinline__ Frag<bf16> frag44(const bf16 *p)
+{
+    const bf16x4 a = *reinterpret_cast<const bf16x4 *>(p), b = *reinterpret_cast<const bf16x4 *>(p + 16);
+    return {__builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7)};
+}
+__device__ __forceinline__ Frag<float> frag44(const float *p)
+{
+    Frag<float> r;
+    *reinterpret_cast<f32x4 *>(r.x) = *reinterpret_cast<const f32x4 *>(p);
+    *reinterpret_cast<f32x4 *>(r.x + 4) = *reinterpret_cast<const f32x4 *>(p + 16);
+    return r;
+}
+// Column lane % 16 of rows 4g .. 4g+3 and 16+4g .. 16+4g+3 (g = lane / 16) of
+// the 32 x 16 tile at p, whose rows are ld apart.
+template <int LD>
+__device__ __forceinline__ Frag<bf16> frag_col(const bf16 *p, int lane)
+{
+    // ds_read_b64_tr_b16: the 16 lanes of a group name the 8-byte pieces of a
+    // 4 x 16 tile in order, and lane i of them receives its column i
+    const int i = lane & 15, g = lane >> 4;
+    typedef __attribute__((address_space(3))) s16x4 *lds_t;
+    const bf16 *a = p + (4 * g + (i >> 2)) * LD + (i & 3) * 4;
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_t)(a));
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_t)(a + 16 * LD));
+    return {__builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7))};
+}
+template <int LD>
+__device__ __forceinline__ Frag<float> frag_col(const float *p, int lane)
+{
+    Frag<float> r;
+    const float *a = p + (lane >> 4) * 4 * LD + (lane & 15);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        r.x[j] = a[j * LD];
+        r.x[4 + j] = a[(16 + j) * LD];
+    }
+    return r;
+}
+// Two accumulators (rows 4g..4g+3 of two 16-row tiles) as an operand.
+__device__ __forceinline__ void frag_acc(Frag<bf16> &r, f32x4 a, f32x4 b)
+{
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        r.x[j] = (bf16)a[j];
+        r.x[4 + j] = (bf16)b[j];
+    }
+}
+__device__ __forceinline__ void frag_acc(Frag<float> &r, f32x4 a, f32x4 b)
+{
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        r.x[j] = a[j];
+        r.x[4 + j] = b[j];
+    }
+}
+
+// ---- tiles of q, k and v: global memory to registers to LDS
+
+// A ROWS x COLS tile of elements E, PER pieces of 16 bytes to a thread.
+template <typename E, int ROWS, int COLS>
+struct Tile {
+    static constexpr int VE = 16 / (int)sizeof(E), PER = ROWS * COLS / (PT * VE);
+    static_assert(PER * PT * VE == ROWS * COLS, "whole pieces");
+    u32x4 buf[PER];
+
+    // Rows 0 .. rows-1 and columns 0 .. cols-1 of the matrix at `base`, whose
+    // rows are `ld` elements apart; 0 elsewhere.  At most 64 rows of strides
+    // below 2^24 elements (32 of 4-byte ones): offsets stay below 2^31.
+    __device__ __forceinline__ void load(const E *base, int64_t ld, int rows, int cols, bool vec, int tid)
+    {
+        const rsrc_t r = make_rsrc(base, rows > 0 ? ((rows - 1) * ld + cols) * (int64_t)sizeof(E) : 0);
+#pragma unroll
+        for (int u = 0; u < PER; ++u) {
+            const int e = (u * PT + tid) * VE, row = e / COLS, col = e % COLS;
+            const uint32_t off = (uint32_t)(row * (int)ld + col) * (uint32_t)sizeof(E);
+            if (vec) {
+                buf[u] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                                       r, row < rows && col < cols ? off : kOOB, 0, 0));
+            } else {
+                E x[VE];
+#pragma unroll
+                for (int i = 0; i < VE; ++i) {
+                    const uint32_t o = row < rows && col + i < cols ? off + i * (uint32_t)sizeof(E) : kOOB;
+                    if constexpr (sizeof(E) == 2)
+                        x[i] = __builtin_bit_cast(E, (short)__builtin_amdgcn_raw_buffer_load_b16(r, o, 0, 0));
+                    else
+                        x[i] = __builtin_bit_cast(E, __builtin_amdgcn_raw_buffer_load_b32(r, o, 0, 0));
+                }
+                __builtin_memcpy(&buf[u], x, 16);
+            }
+        }
+    }
+
+    template <int LD, typename L>
+    __device__ __forceinline__ void store(L *lds, int tid) const
+    {
+#pragma unroll
+        for (int u = 0; u < PER; ++u) {
+            const int e = (u * PT + tid) * VE, row = e / COLS, col = e % COLS;
+            L *to = lds + row * LD + col;
+            if constexpr (std::is_same<E, L>::value) {
+                *reinterpret_cast<u32x4 *>(to) = buf[u];
+            } else {
+                E x[VE];
+                __builtin_memcpy(x, &buf[u], 16);
+#pragma unroll
+                for (int i = 0; i < VE; i += 4)
+                    *reinterpret_cast<f32x4 *>(to + i) =
+                        f32x4{to_f(x[i]), to_f(x[i + 1]), to_f(x[i + 2]), to_f(x[i + 3])};
+            }
+        }
+    }
+};
+
+// ---- decays of a chunk
+
+// Sums of log decays grow over a chunk while their differences matter, so
+// they are formed in 64 bits and kept as a float and its remainder.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp_add64(double x)
+{
+    const unsigned long long u = __builtin_bit_cast(unsigned long long, x);
+    const unsigned lo = __builtin_amdgcn_update_dpp(0, (int)(u & 0xffffffffu), CTRL, ROWS, 0xf, true);
+    const unsigned hi = __builtin_amdgcn_update_dpp(0, (int)(u >> 32), CTRL, ROWS, 0xf, true);
+    return x + __builtin_bit_cast(double, (unsigned long long)hi << 32 | lo);
+}
+__device__ __forceinline__ double scan64(double x)
+{
+    x = dpp_add64<ssd::kRowShr + 1, 0xf>(x);
+    x = dpp_add64<ssd::kRowShr + 2, 0xf>(x);
+    x = dpp_add64<ssd::kRowShr + 4, 0xf>(x);
+    x = dpp_add64<ssd::kRowShr + 8, 0xf>(x);
+    x = dpp_add64<ssd::kRowBcast15, 0xa>(x);
+    return dpp_add64<ssd::kRowBcast31, 0xc>(x);
+}
+
+template <int C>
+struct Decays {
+    float hi[C], lo[C];   // b_t
+    float in[C];          // e^{b_t}
+    float out[C];         // e^{b_L - b_t}
+    float all;            // e^{b_L}
+    double sum;           // b_L
+};
+
+// One wave: the decays of a chunk whose log decay at row `lane` is la (0 past
+// the last row).
+template <int C>
+__device__ __forceinline__ void make_decays(Decays<C> &d, float la, int lane)
+{
+    const double b = scan64((double)clamp_decay(la));
+    const unsigned long long u = __builtin_bit_cast(unsigned long long, b);
+    const unsigned lo = __builtin_amdgcn_readlane((int)(u & 0xffffffffu), 63);
+    const unsigned hi = __builtin_amdgcn_readlane((int)(u >> 32), 63);
+    const double last = __builtin_bit_cast(double, (unsigned long long)hi << 32 | lo);
+    if (lane < C) {
+        const float h = (float)b;
+        d.hi[lane] = h;
+        d.lo[lane] = (float)(b - (double)h);
+        d.in[lane] = expf((float)b);
+        d.out[lane] = expf((float)(last - b));
+    }
+    if (lane == 0) {
+        d.all = expf((float)last);
+        d.sum = last;
+    }
+}
+
+// ---- where a block works
+
+struct Place {
+    int n, begin, rows;   // sequence, first row and number of rows of the segment
+    int segs, s;          // segments of the sequence, and which one this is
+    int slot;             // -1: no state is kept
+    bool bad;             // the slot does not exist, or an earlier sequence has it
+};
+
+// Sequence n's rows, clamped to the batch.
+__device__ __forceinline__ void rows_of(const PrefillArgs &a, int n, int &begin, int &end)
+{
+    begin = min(max(a.cu[n], 0), a.T);
+    end = min(max(a.cu[n + 1], begin), a.T);
+}
+
+// Segment number `id`.  Sequence n has the numbers from begin / seg + n on;
+// there are at least as many up to the next sequence's first as it has
+// segments, and the ones left over have none.  All 64 lanes look at
+// sequences, so a batch of 64 takes one load's latency.
+__device__ __forceinline__ bool find(const PrefillArgs &a, int id, Place &p)
+{
+    const int lane = threadIdx.x & 63;
+    int n = -1;
+    if (a.seg == 0) {
+        n = id;
+    } else {
+        for (int j0 = 0; j0 < a.N; j0 += 64) {
+            const int j = j0 + lane;
+            int b = 0, e = 0;
+            if (j < a.N) rows_of(a, j, b, e);
+            const int s = id - (b / a.seg + j);
+            const int len = e - b;
+            const unsigned long long m = __ballot(j < a.N && s >= 0 && (s == 0 || s * (int64_t)a.seg < len));
+            if (m != 0) n = j0 + __ffsll(m) - 1;   // see below: one at most
+        }
+        if (n < 0) return false;
+    }
+    int begin, end;
+    rows_of(a, n, begin, end);
+    p.n = n;
+    const int len = end - begin;
+    p.segs = a.seg == 0 ? 1 : max(1, (len + a.seg - 1) / a.seg);
+    p.s = a.seg == 0 ? 0 : id - (begin / a.seg + n);
+    p.begin = begin + p.s * a.seg;
+    p.rows = a.seg == 0 ? len : min(a.seg, end - p.begin);
+    return true;
+}
+
+// The slot of sequence n, and whether it cannot be used: it does not exist,
+// or an earlier sequence has it.
+__device__ __forceinline__ void slot_of(const PrefillArgs &a, int n, int &slot, bool &bad)
+{
+    slot = index_of(a.slots, n);
+    bad = slot >= a.nslots;
+    if (!a.slots || slot < 0 || bad) return;
+    for (int j0 = 0; j0 < n; j0 += 64) {
+        const int j = j0 + (int)(threadIdx.x & 63);
+        if (__ballot(j < n && a.slots[j < n ? j : 0] == slot) != 0) bad = true;
+    }
+}
+
+// One segment for one head and VT columns.  KP: dk rounded up; C: rows of a
+// chunk.  OUT: y and the last state, from the state that enters the segment.
+// Otherwise: the state that the segment makes from zero, and its decay.
+//
+// LDS rows are padded so that the reads below spread over the banks: a row of
+// Q and P 16 bytes off a multiple of 256 (rows read across lanes), a row of K
+// and V 32 bytes (4 x 16 tiles read for their columns).
+template <typename E, int KP, int VT, int C, bool OUT>
+__global__ __launch_bounds__(PT, 2) void k_lin_chunks(PrefillArgs a)
+{
+    typedef typename std::conditional<std::is_same<E, bf16>::value, bf16, float>::type L;
+    constexpr bool HALF = sizeof(L) == 2;
+    constexpr int PADR = 16 / (int)sizeof(L), PADC = HALF ? 16 : 4;
+    constexpr int LQ = KP + PADR, LK = KP + PADC, LV = VT + PADC, LP = C + PADR;
+    constexpr int MT = KP / 16, NT = VT / 64, TT = C / 16, KS = KP / 32, TS = C / 32;
+    __shared__ __align__(16) L qs[OUT ? C * LQ : 1], ks[C * LK], vs[C * LV], ps[OUT ? C * LP : 1];
+    __shared__ Decays<C> dec[2];
+
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int l16 = lane & 15, g4 = (lane >> 4) * 4;
+    const int tile = blockIdx.x % a.tiles, h = blockIdx.x / a.tiles % a.H, id = blockIdx.x / (a.tiles * a.H);
+    Place p;
+    if (!find(a, id, p)) return;
+    if (!OUT && p.s + 1 >= p.segs) return;   // nothing follows the last segment
+    slot_of(a, p.n, p.slot, p.bad);
+    const int g = h / (a.H / a.G), c0 = tile * VT, cols = min(VT, a.dv - c0);
+    E *y = static_cast<E *>(a.y) + p.begin * a.st.y_t + h * a.st.y_h + c0;
+    if (p.bad) {
+        if (OUT)
+            for (int64_t e = tid; e < (int64_t)p.rows * VT; e += PT)
+                if (e % VT < cols) y[e / VT * a.st.y_t + e % VT] = from_f<E>(__builtin_nanf(""));
         return;
     }
-    float *S = sl < 0 ? nullptr : a.states + ((int64_t)sl * a.H + h) * a.dk * a.dv + col;
-    const bool read = S && (!a.carry || a.carry[n] != 0);
-    const int per = (a.dk + 3) / 4, r0 = wave * per, r1 = min(r0 + per, a.dk);
-    float s[64];
+    const E *q = static_cast<const E *>(a.q) + p.begin * a.st.q_t + g * a.st.q_g;
+    const E *k = static_cast<const E *>(a.k) + p.begin * a.st.k_t + g * a.st.k_g;
+    const E *v = static_cast<const E *>(a.v) + p.begin * a.st.v_t + h * a.st.v_h + c0;
+    const float *la = a.la + (a.la_t ? p.begin * a.la_t : 0) + h;
+    const int64_t state = (int64_t)a.dk * a.dv;
+    float *pool = p.slot < 0 ? nullptr : a.states + ((int64_t)p.slot * a.H + h) * state;
+    float *ends = p.segs > 1 ? a.ends + ((int64_t)id * a.H + h) * state : nullptr;
+    const int w0 = wave * (VT / 4);   // this wave's columns of the tile
+
+    // S: rows 16 m + g4 + i, column w0 + 16 n + l16
+    f32x4 S[MT][NT];
+    {
+        const float *from = !OUT ? nullptr : p.segs > 1 ? ends : !a.carry || a.carry[p.n] != 0 ? pool : nullptr;
 #pragma unroll
-    for (int i = 0; i < 64; ++i) s[i] = read && on && r0 + i < r1 ? S[(int64_t)(r0 + i) * a.dv] : 0.f;
-    for (int t = begin; t < end; ++t) {
-        const T *q = static_cast<const T *>(a.q) + t * a.st.q_t + g * a.st.q_g;
-        const T *k = static_cast<const T *>(a.k) + t * a.st.k_t + g * a.st.k_g;
-        const float v = on ? to_f(static_cast<const T *>(a.v)[t * a.st.v_t + h * a.st.v_h + col]) : 0.f;
-        const float dec = expf(a.la[(a.la_t ? t * a.la_t : 0) + h]);
-        float o = 0.f;
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int i = 0; i < 64; ++i)
-            if (r0 + i < r1) {
-                s[i] = dec * s[i] + to_f(k[r0 + i]) * v;
-                o += to_f(q[r0 + i]) * s[i];
-            }
-        red[t & 1][wave][lane] = o;
-        __syncthreads();
-        if (wave == 0 && on)
-            y[t * a.st.y_t + col] = from_f<T>(red[t & 1][0][lane] + red[t & 1][1][lane] + red[t & 1][2][lane] +
-                                              red[t & 1][3][lane]);
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int row = 16 * m + g4 + i, col = w0 + 16 * n + l16;
+                    S[m][n][i] = from && row < a.dk && col < cols ? from[row * a.dv + c0 + col] : 0.f;
+                }
     }
-    if (S && on)
+
+    Tile<E, C, KP> tq, tk;
+    Tile<E, C, VT> tv;
+    const auto load = [&](int t0) {
+        const int rows = min(C, p.rows - t0);
+        if (OUT) tq.load(q + t0 * a.st.q_t, a.st.q_t, rows, a.dk, a.vec_qk, tid);
+        tk.load(k + t0 * a.st.k_t, a.st.k_t, rows, a.dk, a.vec_qk, tid);
+        tv.load(v + t0 * a.st.v_t, a.st.v_t, rows, cols, a.vec_v, tid);
+    };
+    const auto log_decay = [&](int t0) { return t0 + lane < p.rows && lane < C ? la[(t0 + lane) * a.la_t] : 0.f; };
+
+    // the scores above the diagonal that a 32-wide step over them reads stay 0
+    if (OUT && (wave & 1) == 0 && wave + 1 < TT)
+        for (int e = lane; e < 256; e += 64) ps[(16 * wave + e / 16) * LP + 16 * (wave + 1) + e % 16] = (L)0.f;
+
+    double total = 0.0;
+    if (p.rows > 0) {
+        load(0);
+        if (wave == 0) make_decays(dec[0], log_decay(0), lane);
+    }
+    for (int t0 = 0, c = 0; t0 < p.rows; t0 += C, ++c) {
+        const Decays<C> &d = dec[c & 1];
+        if (OUT) tq.template store<LQ>(qs, tid);
+        tk.template store<LK>(ks, tid);
+        tv.template store<LV>(vs, tid);
+        block_sync();
+        const bool more = t0 + C < p.rows;
+        if (more) load(t0 + C);
+        const bool decays = more && wave == (c + 1) % 4;
+        const float next_la = decays ? log_decay(t0 + C) : 0.f;
+
+        f32x4 Y[NT][TT];
+        if (OUT) {
+            // P: each wave one 16-row tile of queries, up to the diagonal.
+            // Formed as K Q^T, so that a lane holds 4 scores of one query.
+            if (wave < TT) {
+                Frag<L> fq[KS];
 #pragma unroll
-        for (int i = 0; i < 64; ++i)
-            if (r0 + i < r1) S[(int64_t)(r0 + i) * a.dv] = s[i];
+                for (int s = 0; s < KS; ++s) fq[s] = frag8(qs + (16 * wave + l16) * LQ + 32 * s + 2 * g4);
+                const int i = 16 * wave + l16;
+                const float bh = d.hi[i], bl = d.lo[i];
+                for (int jt = 0; jt <= wave; ++jt) {
+                    f32x4 x = {};
+#pragma unroll
+                    for (int s = 0; s < KS; ++s)
+                        x = mma(frag8(ks + (16 * jt + l16) * LK + 32 * s + 2 * g4), fq[s], x);
+                    const int j = 16 * jt + g4;
+                    L out[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        out[e] = j + e <= i ? (L)(x[e] * __expf((bh - d.hi[j + e]) + (bl - d.lo[j + e]))) : (L)0.f;
+                    __builtin_memcpy(__builtin_assume_aligned(ps + i * LP + j, 4 * sizeof(L)), out, sizeof(out));
+                }
+            }
+            // Y^T = diag(e^b) S^T Q^T, rows: columns of v, columns: queries
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int t = 0; t < TT; ++t) Y[n][t] = f32x4{};
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+                Frag<L> fs[NT];
+#pragma unroll
+                for (int n = 0; n < NT; ++n) frag_acc(fs[n], S[2 * s][n], S[2 * s + 1][n]);
+#pragma unroll
+                for (int t = 0; t < TT; ++t) {
+                    const Frag<L> fq = frag44(qs + (16 * t + l16) * LQ + 32 * s + g4);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) Y[n][t] = mma(fs[n], fq, Y[n][t]);
+                }
+            }
+#pragma unroll
+            for (int t = 0; t < TT; ++t) {
+                const float e = d.in[16 * t + l16];
+#pragma unroll
+                for (int n = 0; n < NT; ++n) Y[n][t] *= e;
+            }
+            block_sync();
+        }
+
+        const float all = d.all;
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) S[m][n] *= all;
+#pragma unroll
+        for (int s = 0; s < TS; ++s) {
+            Frag<L> fv[NT];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) fv[n] = frag_col<LV>(vs + 32 * s * LV + w0 + 16 * n, lane);
+            if (OUT) {
+#pragma unroll
+                for (int t = 2 * s; t < TT; ++t) {
+                    const Frag<L> fp = frag44(ps + (16 * t + l16) * LP + 32 * s + g4);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) Y[n][t] = mma(fv[n], fp, Y[n][t]);
+                }
+            }
+            // V's rows times e^{b_L - b}.  In bf16 as three parts, which hold
+            // all 24 bits: the state is a float32 result.
+            constexpr int PARTS = HALF ? 3 : 1;
+            Frag<L> fw[PARTS][NT];
+            const f32x4 wa = *reinterpret_cast<const f32x4 *>(d.out + 32 * s + g4);
+            const f32x4 wb = *reinterpret_cast<const f32x4 *>(d.out + 32 * s + 16 + g4);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    float x = (float)fv[n].x[e] * (e < 4 ? wa[e & 3] : wb[e & 3]);
+#pragma unroll
+                    for (int u = 0; u < PARTS; ++u) {
+                        fw[u][n].x[e] = (L)x;
+                        x -= (float)fw[u][n].x[e];
+                    }
+                }
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                const Frag<L> fk = frag_col<LK>(ks + 32 * s * LK + 16 * m, lane);
+#pragma unroll
+                for (int u = PARTS - 1; u >= 0; --u)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) S[m][n] = mma(fk, fw[u][n], S[m][n]);
+            }
+        }
+        if (OUT) {
+            const int rows = min(C, p.rows - t0);
+            E *yc = y + t0 * a.st.y_t;
+#pragma unroll
+            for (int t = 0; t < TT; ++t) {
+                const int row = 16 * t + l16;
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const int col = w0 + 16 * n + g4;
+                    if (row >= rows) continue;
+                    E out[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) out[e] = from_f<E>(Y[n][t][e]);
+                    E *to = yc + row * a.st.y_t + col;
+                    if (a.vec_y) {
+                        if (col < cols) *reinterpret_cast<Vec<E, 4> *>(to) = *reinterpret_cast<Vec<E, 4> *>(out);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (col + e < cols) to[e] = out[e];
+                    }
+                }
+            }
+        }
+        total += d.sum;
+        if (decays) make_decays(dec[(c + 1) & 1], next_la, lane);
+        block_sync();
+    }
+
+    float *to = OUT ? (p.s + 1 == p.segs ? pool : nullptr) : ends;
+    if (to) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int row = 16 * m + g4 + i, col = w0 + 16 * n + l16;
+                    if (row < a.dk && col < cols) to[row * a.dv + c0 + col] = S[m][n][i];
+                }
+    }
+    if (!OUT && tile == 0 && tid == 0) a.segdec[(int64_t)id * a.H + h] = expf((float)total);
+}
+
+// The state entering each segment of a sequence that was cut, in place of the
+// states that the segments make from zero: one thread for each element.
+__global__ __launch_bounds__(PT) void k_lin_carry(PrefillArgs a, int chunks)
+{
+    const int h = blockIdx.x / chunks % a.H, n = blockIdx.x / (chunks * a.H);
+    int begin, end;
+    rows_of(a, n, begin, end);
+    const int segs = (end - begin + a.seg - 1) / a.seg;
+    if (segs <= 1) return;
+    int slot;
+    bool bad;
+    slot_of(a, n, slot, bad);
+    const int64_t state = (int64_t)a.dk * a.dv;
+    const int64_t e = (int64_t)(blockIdx.x % chunks) * PT + threadIdx.x;
+    if (bad || e >= state) return;
+    float cur = slot >= 0 && (!a.carry || a.carry[n] != 0) ? a.states[((int64_t)slot * a.H + h) * state + e] : 0.f;
+    const int64_t id0 = begin / a.seg + n;
+    float *x = a.ends + (id0 * a.H + h) * state + e;
+    const float *dec = a.segdec + id0 * a.H + h;
+    const int64_t step = a.H * state;
+    constexpr int U = 8;
+    for (int s0 = 0; s0 < segs; s0 += U) {
+        float made[U], f[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const bool on = s0 + u + 1 < segs;   // the last segment made none
+            made[u] = on ? x[(s0 + u) * step] : 0.f;
+            f[u] = on ? dec[(int64_t)(s0 + u) * a.H] : 0.f;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (s0 + u < segs) {
+                x[(s0 + u) * step] = cur;
+                cur = f[u] * cur + made[u];
+            }
+    }
+}
+
+// ---- host side
+
+struct PrefillPlan {
+    int seg = 0, ids = 0;
+    size_t ends = 0, segdec = 0, total = 0;
+};
+
+static int col_tile(int64_t dk, int64_t dv) { return dk > 128 || dv <= 64 ? 64 : 128; }
+
+// Sequences are cut where whole ones would leave CUs idle: segments of a
+// length that makes about two blocks for each CU out of the batch's rows.
+static PrefillPlan plan_prefill(const lin_shape &s, int64_t max_seqlen, int cus)
+{
+    PrefillPlan P;
+    const int64_t longest = max_seqlen > 0 && max_seqlen < s.T ? max_seqlen : s.T;
+    const int64_t tiles = (s.dv + col_tile(s.dk, s.dv) - 1) / col_tile(s.dk, s.dv);
+    const int64_t blocks = 2 * int64_t(cus), work = s.T * s.H * tiles;
+    int64_t seg = (work + blocks - 1) / blocks;
+    seg = (seg + 63) / 64 * 64;
+    if (seg < 256) seg = 256;
+    P.ids = (int)s.N;
+    if (longest <= seg) return P;
+    P.seg = (int)seg;
+    P.ids = (int)(s.T / seg + s.N);
+    size_t o = 0;
+    P.ends = o;
+    o += (size_t)P.ids * s.H * s.dk * s.dv * sizeof(float);
+    o = (o + 255) / 256 * 256;
+    P.segdec = o;
+    o += (size_t)P.ids * s.H * sizeof(float);
+    P.total = (o + 255) / 256 * 256;
+    return P;
+}
+
+template <typename E, int KP, int VT, int C>
+static int run_prefill(PrefillArgs &a, hipStream_t st)
+{
+    const int64_t grid = (int64_t)a.ids * a.H * a.tiles;
+    if (a.seg > 0) {
+        k_lin_chunks<E, KP, VT, C, false><<<dim3((unsigned)grid), dim3(PT), 0, st>>>(a);
+        const int chunks = (a.dk * a.dv + PT - 1) / PT;
+        k_lin_carry<<<dim3((unsigned)((int64_t)a.N * a.H * chunks)), dim3(PT), 0, st>>>(a, chunks);
+    }
+    k_lin_chunks<E, KP, VT, C, true><<<dim3((unsigned)grid), dim3(PT), 0, st>>>(a);
+    return launch_status();
+}
+
+template <typename E>
+static int dispatch_prefill(PrefillArgs &a, hipStream_t st)
+{
+    // float tiles are twice as wide: half the rows to a chunk
+    constexpr int C = std::is_same<E, bf16>::value ? 64 : 32;
+    const bool wide = col_tile(a.dk, a.dv) == 128;
+    if (a.dk > 128) return run_prefill<E, 256, 64, 32>(a, st);
+    if (a.dk > 64) return wide ? run_prefill<E, 128, 128, C>(a, st) : run_prefill<E, 128, 64, C>(a, st);
+    return wide ? run_prefill<E, 64, 128, C>(a, st) : run_prefill<E, 64, 64, C>(a, st);
 }
 
 }  // namespace layer
@@ -74,7 +645,7 @@ using namespace layer;
 extern "C" size_t lin_prefill_workspace_size(const lin_shape *shape, int64_t max_seqlen)
 {
     if (check_lin(shape, false) != SSD_OK || max_seqlen < 0) return (size_t)-1;
-    return 0;
+    return plan_prefill(*shape, max_seqlen, ssd::device_cus()).total;
 }
 
 extern "C" int lin_prefill(const lin_shape *shape, int dtype, const lin_strides *strides, const void *q,
@@ -99,8 +670,10 @@ extern "C" int lin_prefill(const lin_shape *shape, int dtype, const lin_strides 
     if (misaligned(q, e) || misaligned(k, e) || misaligned(v, e) || misaligned(y, e) || misaligned(log_decay, 4) ||
         misaligned(slots, 4) || misaligned(states, 4) || misaligned(cu_seqlens, 4) || misaligned(carry, 4))
         return SSD_ERR_ALIGN;
-    (void)workspace;
-    (void)workspace_bytes;
+    const PrefillPlan P = plan_prefill(s, max_seqlen, ssd::device_cus());
+    if (workspace_bytes < P.total) return SSD_ERR_WORKSPACE;
+    if (P.total > 0 && !workspace) return SSD_ERR_NULL;
+    if (P.total > 0 && misaligned(workspace, 16)) return SSD_ERR_ALIGN;
     a.q = q;
     a.k = k;
     a.v = v;
@@ -111,6 +684,8 @@ extern "C" int lin_prefill(const lin_shape *shape, int dtype, const lin_strides 
     a.carry = carry;
     a.states = states;
     a.y = y;
+    a.ends = reinterpret_cast<float *>(static_cast<char *>(workspace) + P.ends);
+    a.segdec = reinterpret_cast<float *>(static_cast<char *>(workspace) + P.segdec);
     a.T = (int)s.T;
     a.N = (int)s.N;
     a.G = (int)s.G;
@@ -118,8 +693,20 @@ extern "C" int lin_prefill(const lin_shape *shape, int dtype, const lin_strides 
     a.dk = (int)s.dk;
     a.dv = (int)s.dv;
     a.nslots = (int)s.slots;
-    a.tiles = (a.dv + 63) / 64;
+    const int vt = col_tile(s.dk, s.dv);
+    a.tiles = (a.dv + vt - 1) / vt;
+    a.seg = P.seg;
+    a.ids = P.ids;
+    // 16 bytes at a time where every row of every head begins on 16 bytes and
+    // holds a whole number of them
+    const auto rows16 = [&](const void *ptr, int64_t row, int64_t head, int64_t d) {
+        return !misaligned(ptr, 16) && row * e % 16 == 0 && head * e % 16 == 0 && d * e % 16 == 0;
+    };
+    a.vec_qk = rows16(q, a.st.q_t, a.st.q_g, s.dk) && rows16(k, a.st.k_t, a.st.k_g, s.dk);
+    a.vec_v = rows16(v, a.st.v_t, a.st.v_h, s.dv);
+    a.vec_y = rows16(y, a.st.y_t, a.st.y_h, s.dv);
     hipStream_t st = static_cast<hipStream_t>(stream);
-    LAYER_DISPATCH(dtype, (k_lin_prefill<T><<<dim3((unsigned)((int64_t)a.N * a.H * a.tiles)), dim3(PT), 0, st>>>(a)));
-    return launch_status();
+    if (dtype == LAYER_BF16) return dispatch_prefill<bf16>(a, st);
+    if (dtype == LAYER_F16) return dispatch_prefill<f16>(a, st);
+    return dispatch_prefill<float>(a, st);
 }
