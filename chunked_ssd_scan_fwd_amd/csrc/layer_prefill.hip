@@ -7,9 +7,9 @@
 //
 // A block walks the chunks of one segment of a sequence for one head and VT
 // columns of v, with S in its registers: q, k, v are read once and y is
-// written once, and no chunk's state goes to memory.  Each of the four waves
-// owns VT / 4 columns of S, of Y and of V and all dk rows of S, so S never
-// crosses waves; only the masked scores P = Q K^T o D do, through LDS.
+// written once, and no chunk's state goes to memory.  Each wave owns 16
+// columns of S, of Y and of V and all dk rows of S, so S never crosses waves;
+// only the masked scores P = Q K^T o D do, through LDS.
 //
 // Sequences longer than the plan's segment are cut: one pass leaves the state
 // each segment makes from zero, a second pass joins them into the states that
@@ -30,11 +30,13 @@ using ssd::rsrc_t;
 using ssd::make_rsrc;
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int PT = 256;   // threads of a block: 4 waves
+constexpr int CT = 256;   // threads of a block of the carry pass
 
 struct PrefillArgs {
     const void *q, *k, *v;
@@ -47,7 +49,6 @@ struct PrefillArgs {
     int T, N, G, H, dk, dv, nslots, tiles;
     int seg;       // rows of a segment; 0: sequences are not cut
     int ids;       // blocks' segment numbers, T / seg + N
-    bool vec_qk, vec_v, vec_y;
 };
 
 // ---- fragments of the matrix products
@@ -87,38 +88,27 @@ __device__ __forceinline__ Frag<float> frag8(const float *p)
     *reinterpret_cast<f32x4 *>(r.x + 4) = *reinterpret_cast<const f32x4 *>(p + 4);
     return r;
 }
-// Values 0..3 and 16..19 of a row.
-__device__ __forceinline__ Frag<bf16> frag44(const bf16 *p)
-{
-    const bf16x4 a = *reinterpret_cast<const bf16x4 *>(p), b = *reinterpret_cast<const bf16x4 *>(p + 16);
-    return {__builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7)};
-}
-__device__ __forceinline__ Frag<float> frag44(const float *p)
-{
-    Frag<float> r;
-    *reinterpret_cast<f32x4 *>(r.x) = *reinterpret_cast<const f32x4 *>(p);
-    *reinterpret_cast<f32x4 *>(r.x + 4) = *reinterpret_cast<const f32x4 *>(p + 16);
-    return r;
-}
-// Column lane % 16 of rows 4g .. 4g+3 and 16+4g .. 16+4g+3 (g = lane / 16) of
-// the 32 x 16 tile at p, whose rows are ld apart.
-template <int LD>
-__device__ __forceinline__ Frag<bf16> frag_col(const bf16 *p, int lane)
+// One column of a tile in LDS whose rows are LD apart, at rows 4g .. 4g+3 and
+// 16+4g .. 16+4g+3 (g = lane / 16).  Lane i = lane % 16 takes column `col` + i,
+// or with SPLIT column `col` + 8 (i / 4) + i % 4.
+template <int LD, bool SPLIT>
+__device__ __forceinline__ Frag<bf16> frag_col(const bf16 *p, int col, int lane)
 {
     // ds_read_b64_tr_b16: the 16 lanes of a group name the 8-byte pieces of a
     // 4 x 16 tile in order, and lane i of them receives its column i
     const int i = lane & 15, g = lane >> 4;
     typedef __attribute__((address_space(3))) s16x4 *lds_t;
-    const bf16 *a = p + (4 * g + (i >> 2)) * LD + (i & 3) * 4;
+    const bf16 *a = p + (4 * g + (i >> 2)) * LD + col + (i & 3) * (SPLIT ? 8 : 4);
     const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_t)(a));
     const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_t)(a + 16 * LD));
     return {__builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7))};
 }
-template <int LD>
-__device__ __forceinline__ Frag<float> frag_col(const float *p, int lane)
+template <int LD, bool SPLIT>
+__device__ __forceinline__ Frag<float> frag_col(const float *p, int col, int lane)
 {
     Frag<float> r;
-    const float *a = p + (lane >> 4) * 4 * LD + (lane & 15);
+    const int i = lane & 15;
+    const float *a = p + (lane >> 4) * 4 * LD + col + (SPLIT ? 8 * (i >> 2) + (i & 3) : i);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         r.x[j] = a[j * LD];
@@ -126,14 +116,11 @@ __device__ __forceinline__ Frag<float> frag_col(const float *p, int lane)
     }
     return r;
 }
-// Two accumulators (rows 4g..4g+3 of two 16-row tiles) as an operand.
+// Two accumulators as an operand.
 __device__ __forceinline__ void frag_acc(Frag<bf16> &r, f32x4 a, f32x4 b)
 {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        r.x[j] = (bf16)a[j];
-        r.x[4 + j] = (bf16)b[j];
-    }
+    r.x = __builtin_shufflevector(__builtin_convertvector(a, bf16x4), __builtin_convertvector(b, bf16x4), 0, 1, 2, 3, 4,
+                                  5, 6, 7);
 }
 __device__ __forceinline__ void frag_acc(Frag<float> &r, f32x4 a, f32x4 b)
 {
@@ -144,33 +131,77 @@ __device__ __forceinline__ void frag_acc(Frag<float> &r, f32x4 a, f32x4 b)
     }
 }
 
+// V's rows times e^{b_L - b} (wa, wb: the fragment's first and last four
+// rows).  In bf16 as two parts: the state is a float32 result, and their sum
+// is off by 2^-18 of a product at most (states came out within 9e-7).
+template <typename L>
+struct Parts {
+    static constexpr int n = sizeof(L) == 2 ? 2 : 1;
+};
+__device__ __forceinline__ void weigh(Frag<bf16> (&fw)[2], const Frag<bf16> &fv, f32x4 wa, f32x4 wb)
+{
+    // pairs, so that two values are rounded by one instruction
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+        f32x2 x = {(float)fv.x[e], (float)fv.x[e + 1]};
+        x[0] *= e < 4 ? wa[e & 3] : wb[e & 3];
+        x[1] *= e < 4 ? wa[(e & 3) + 1] : wb[(e & 3) + 1];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const bf16x2 r = __builtin_convertvector(x, bf16x2);
+            fw[u].x[e] = r[0];
+            fw[u].x[e + 1] = r[1];
+            x[0] -= (float)r[0];
+            x[1] -= (float)r[1];
+        }
+    }
+}
+__device__ __forceinline__ void weigh(Frag<float> (&fw)[1], const Frag<float> &fv, f32x4 wa, f32x4 wb)
+{
+#pragma unroll
+    for (int e = 0; e < 8; ++e) fw[0].x[e] = fv.x[e] * (e < 4 ? wa[e & 3] : wb[e & 3]);
+}
+
+__device__ __forceinline__ void store4(bf16 *p, const float (&x)[4])
+{
+    *reinterpret_cast<bf16x4 *>(p) = __builtin_convertvector((f32x4{x[0], x[1], x[2], x[3]}), bf16x4);
+}
+__device__ __forceinline__ void store4(float *p, const float (&x)[4])
+{
+    *reinterpret_cast<f32x4 *>(p) = f32x4{x[0], x[1], x[2], x[3]};
+}
+
 // ---- tiles of q, k and v: global memory to registers to LDS
 
-// A ROWS x COLS tile of elements E, PER pieces of 16 bytes to a thread.
-template <typename E, int ROWS, int COLS>
+// A ROWS x COLS tile of elements E, PER pieces of 16 bytes to each of PT threads.
+template <typename E, int ROWS, int COLS, int PT>
 struct Tile {
-    static constexpr int VE = 16 / (int)sizeof(E), PER = ROWS * COLS / (PT * VE);
-    static_assert(PER * PT * VE == ROWS * COLS, "whole pieces");
+    static constexpr int VE = 16 / (int)sizeof(E), PIECES = ROWS * COLS / VE, PER = (PIECES + PT - 1) / PT;
     u32x4 buf[PER];
+
+    // Whether piece u of a thread exists.
+    static __device__ __forceinline__ bool has(int u, int tid) { return PIECES % PT == 0 || u * PT + tid < PIECES; }
 
     // Rows 0 .. rows-1 and columns 0 .. cols-1 of the matrix at `base`, whose
     // rows are `ld` elements apart; 0 elsewhere.  At most 64 rows of strides
     // below 2^24 elements (32 of 4-byte ones): offsets stay below 2^31.
-    __device__ __forceinline__ void load(const E *base, int64_t ld, int rows, int cols, bool vec, int tid)
+    template <bool VEC>
+    __device__ __forceinline__ void load(const E *base, int64_t ld, int rows, int cols, int tid)
     {
         const rsrc_t r = make_rsrc(base, rows > 0 ? ((rows - 1) * ld + cols) * (int64_t)sizeof(E) : 0);
 #pragma unroll
         for (int u = 0; u < PER; ++u) {
             const int e = (u * PT + tid) * VE, row = e / COLS, col = e % COLS;
             const uint32_t off = (uint32_t)(row * (int)ld + col) * (uint32_t)sizeof(E);
-            if (vec) {
+            if constexpr (VEC) {
                 buf[u] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                                       r, row < rows && col < cols ? off : kOOB, 0, 0));
+                                                       r, has(u, tid) && row < rows && col < cols ? off : kOOB, 0, 0));
             } else {
                 E x[VE];
 #pragma unroll
                 for (int i = 0; i < VE; ++i) {
-                    const uint32_t o = row < rows && col + i < cols ? off + i * (uint32_t)sizeof(E) : kOOB;
+                    const uint32_t o =
+                        has(u, tid) && row < rows && col + i < cols ? off + i * (uint32_t)sizeof(E) : kOOB;
                     if constexpr (sizeof(E) == 2)
                         x[i] = __builtin_bit_cast(E, (short)__builtin_amdgcn_raw_buffer_load_b16(r, o, 0, 0));
                     else
@@ -186,6 +217,7 @@ struct Tile {
     {
 #pragma unroll
         for (int u = 0; u < PER; ++u) {
+            if (!has(u, tid)) continue;
             const int e = (u * PT + tid) * VE, row = e / COLS, col = e % COLS;
             L *to = lds + row * LD + col;
             if constexpr (std::is_same<E, L>::value) {
@@ -247,11 +279,11 @@ __device__ __forceinline__ void make_decays(Decays<C> &d, float la, int lane)
         const float h = (float)b;
         d.hi[lane] = h;
         d.lo[lane] = (float)(b - (double)h);
-        d.in[lane] = expf((float)b);
-        d.out[lane] = expf((float)(last - b));
+        d.in[lane] = __expf((float)b);
+        d.out[lane] = __expf((float)(last - b));
     }
     if (lane == 0) {
-        d.all = expf((float)last);
+        d.all = __expf((float)last);
         d.sum = last;
     }
 }
@@ -322,21 +354,40 @@ __device__ __forceinline__ void slot_of(const PrefillArgs &a, int n, int &slot, 
 // chunk.  OUT: y and the last state, from the state that enters the segment.
 // Otherwise: the state that the segment makes from zero, and its decay.
 //
-// LDS rows are padded so that the reads below spread over the banks: a row of
-// Q and P 16 bytes off a multiple of 256 (rows read across lanes), a row of K
-// and V 32 bytes (4 x 16 tiles read for their columns).
+// The block's first four waves hold S and make Y, 16 NT columns each; the
+// other four fetch the next chunks, write them to LDS and form the next
+// chunk's scores, so that neither waits for the other's loads.  Matrix and
+// vector instructions of a SIMD's waves did not overlap in time, so what
+// counts for the first four is instructions: Q, K and P, which every one of
+// them reads, are read once for NT column tiles.
+//
+// Every operand is read from LDS 16 bytes at a time, or transposed; pairs of
+// 8-byte reads ran at a quarter of that rate.  So that S can meet Q as it
+// comes out of its accumulators, a lane's 8 rows of S (two accumulators) are
+// 8 rows of S that follow one another, and P is stored in the order in which
+// the transposed reads of V give its rows.  Rows of 2-byte values are padded
+// by 32 bytes: 16-byte reads of 16 rows then moved 252 bytes a clock, and 128
+// with 16 bytes.
 template <typename E, int KP, int VT, int C, bool OUT>
-__global__ __launch_bounds__(PT, 2) void k_lin_chunks(PrefillArgs a)
-{
+struct ChunkLds {
     typedef typename std::conditional<std::is_same<E, bf16>::value, bf16, float>::type L;
-    constexpr bool HALF = sizeof(L) == 2;
-    constexpr int PADR = 16 / (int)sizeof(L), PADC = HALF ? 16 : 4;
-    constexpr int LQ = KP + PADR, LK = KP + PADC, LV = VT + PADC, LP = C + PADR;
-    constexpr int MT = KP / 16, NT = VT / 64, TT = C / 16, KS = KP / 32, TS = C / 32;
-    __shared__ __align__(16) L qs[OUT ? C * LQ : 1], ks[C * LK], vs[C * LV], ps[OUT ? C * LP : 1];
-    __shared__ Decays<C> dec[2];
+    static constexpr int PAD = sizeof(L) == 2 ? 16 : 4;
+    static constexpr int LK = KP + PAD, LV = VT + PAD, LP = C + PAD;
+    L q[2][OUT ? C * LK : 8], k[2][C * LK], v[2][C * LV], p[2][OUT ? C * LP : 8];
+    Decays<C> dec[3];
+};
 
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+template <typename E, int KP, int VT, int C, bool OUT, bool VEC>
+__global__ __launch_bounds__(512, 2) void k_lin_chunks(PrefillArgs a)
+{
+    typedef ChunkLds<E, KP, VT, C, OUT> Lds;
+    typedef typename Lds::L L;
+    constexpr int LK = Lds::LK, LV = Lds::LV, LP = Lds::LP;
+    constexpr int NT = VT / 64, MT = KP / 16, TT = C / 16, KS = KP / 32, TS = C / 32, PARTS = Parts<L>::n;
+    constexpr int PT = 256;   // threads that fetch
+    __shared__ __align__(16) Lds lds;
+
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int l16 = lane & 15, g4 = (lane >> 4) * 4;
     const int tile = blockIdx.x % a.tiles, h = blockIdx.x / a.tiles % a.H, id = blockIdx.x / (a.tiles * a.H);
     Place p;
@@ -347,87 +398,138 @@ __global__ __launch_bounds__(PT, 2) void k_lin_chunks(PrefillArgs a)
     E *y = static_cast<E *>(a.y) + p.begin * a.st.y_t + h * a.st.y_h + c0;
     if (p.bad) {
         if (OUT)
-            for (int64_t e = tid; e < (int64_t)p.rows * VT; e += PT)
+            for (int64_t e = threadIdx.x; e < (int64_t)p.rows * VT; e += 512)
                 if (e % VT < cols) y[e / VT * a.st.y_t + e % VT] = from_f<E>(__builtin_nanf(""));
         return;
     }
-    const E *q = static_cast<const E *>(a.q) + p.begin * a.st.q_t + g * a.st.q_g;
-    const E *k = static_cast<const E *>(a.k) + p.begin * a.st.k_t + g * a.st.k_g;
-    const E *v = static_cast<const E *>(a.v) + p.begin * a.st.v_t + h * a.st.v_h + c0;
-    const float *la = a.la + (a.la_t ? p.begin * a.la_t : 0) + h;
+    const int chunks = (p.rows + C - 1) / C;
+
+    if (wave >= 4) {
+        // ---- fetches and scores
+        const int tid = threadIdx.x - 256, w = wave - 4;
+        const E *q = static_cast<const E *>(a.q) + p.begin * a.st.q_t + g * a.st.q_g;
+        const E *k = static_cast<const E *>(a.k) + p.begin * a.st.k_t + g * a.st.k_g;
+        const E *v = static_cast<const E *>(a.v) + p.begin * a.st.v_t + h * a.st.v_h + c0;
+        const float *la = a.la + (a.la_t ? p.begin * a.la_t : 0) + h;
+        Tile<E, C, KP, PT> tq, tk;
+        Tile<E, C, VT, PT> tv;
+        const auto load = [&](int c) {
+            const int t0 = c * C, rows = p.rows - t0;
+            if (OUT) tq.template load<VEC>(q + t0 * a.st.q_t, a.st.q_t, min(C, rows), a.dk, tid);
+            tk.template load<VEC>(k + t0 * a.st.k_t, a.st.k_t, min(C, rows), a.dk, tid);
+            tv.template load<VEC>(v + t0 * a.st.v_t, a.st.v_t, min(C, rows), cols, tid);
+        };
+        const auto log_decay = [&](int c) {
+            const int t = c * C + lane;
+            return lane < C && t < p.rows ? la[t * a.la_t] : 0.f;
+        };
+        const auto store = [&](int c) {
+            const int b = c & 1;
+            if (OUT) tq.template store<LK>(lds.q[b], tid);
+            tk.template store<LK>(lds.k[b], tid);
+            tv.template store<LV>(lds.v[b], tid);
+        };
+        // P: the 16 x 16 tiles on and below the diagonal, dealt to the four
+        // waves.  Formed as K Q^T, so that a lane holds 4 scores of one query.
+        const auto scores = [&](int c) {
+            const int b = c & 1;
+            const L *qs = lds.q[b], *ks = lds.k[b];
+            const Decays<C> &d = lds.dec[c % 3];
+            constexpr int TILES = TT * (TT + 1) / 2;
+            const auto product = [&](int u) {
+                const int it = TT == 2 ? (u > 0) : (u > 0) + (u > 2) + (u > 5), jt = u - it * (it + 1) / 2;
+                f32x4 x = {};
+#pragma unroll
+                for (int s = 0; s < KS; ++s)
+                    x = mma(frag8(ks + (16 * jt + l16) * LK + 32 * s + 2 * g4),
+                            frag8(qs + (16 * it + l16) * LK + 32 * s + 2 * g4), x);
+                return x;
+            };
+            const auto masked = [&](int u, f32x4 x) {
+                const int it = TT == 2 ? (u > 0) : (u > 0) + (u > 2) + (u > 5), jt = u - it * (it + 1) / 2;
+                const int i = 16 * it + l16, j = 16 * jt + g4;
+                const float bh = d.hi[i], bl = d.lo[i];
+                const f32x4 jh = *reinterpret_cast<const f32x4 *>(d.hi + j);
+                const f32x4 jl = *reinterpret_cast<const f32x4 *>(d.lo + j);
+                float out[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    out[e] = x[e] * __expf((bh - jh[e]) + (bl - jl[e]));
+                    if (j + e > i) out[e] = 0.f;
+                }
+                store4(lds.p[b] + i * LP + 32 * (jt / 2) + 2 * g4 + 4 * (jt % 2), out);
+            };
+            if (TILES >= 8) {   // two at a time, so that one's reads run beside the other's products
+                const f32x4 x0 = product(w), x1 = product(w + 4);
+                masked(w, x0);
+                masked(w + 4, x1);
+            }
+            const int u = TILES >= 8 ? w + 8 : w;
+            if (u < TILES) masked(u, product(u));
+        };
+        // the scores above the diagonal that a 32-wide step over them reads stay 0
+        if (OUT && w < TT && w % 2 == 0)
+            for (int e = lane; e < 512; e += 64)
+                lds.p[e / 256][(16 * w + e / 16 % 16) * LP + 16 * w + 8 * (e / 4 % 4) + 4 + e % 4] = (L)0.f;
+        // Without conditions: a chunk past the last one loads nothing and
+        // leaves zeros in a buffer that is not read.  (With them the compiler
+        // copied the tiles' registers and waited for the loads to do so.)
+        load(0);
+        if (w == 3) make_decays(lds.dec[0], log_decay(0), lane);
+        store(0);
+        load(1);
+        block_sync();
+        if (OUT) scores(0);
+        if (w == 3) make_decays(lds.dec[1], log_decay(1), lane);
+        if (OUT) block_sync();
+        for (int c = 0; c < chunks; ++c) {
+            const float la2 = log_decay(c + 2);
+            store(c + 1);
+            load(c + 2);
+            if (OUT) block_sync();
+            if (OUT && c + 1 < chunks) scores(c + 1);
+            if (w == 3) make_decays(lds.dec[(c + 2) % 3], la2, lane);
+            block_sync();
+        }
+        return;
+    }
+
+    // ---- states and outputs
     const int64_t state = (int64_t)a.dk * a.dv;
     float *pool = p.slot < 0 ? nullptr : a.states + ((int64_t)p.slot * a.H + h) * state;
     float *ends = p.segs > 1 ? a.ends + ((int64_t)id * a.H + h) * state : nullptr;
-    const int w0 = wave * (VT / 4);   // this wave's columns of the tile
+    const int w0 = 16 * NT * wave;   // this wave's columns of the tile
 
-    // S: rows 16 m + g4 + i, column w0 + 16 n + l16
+    // S: value i of accumulator m, n is row 32 (m / 2) + 2 g4 + 4 (m % 2) + i,
+    // column w0 + l16 or, of two column tiles, w0 + 8 (l16 / 4) + 4 n + l16 % 4:
+    // then a lane's values of Y are 8 columns that follow one another.
+    // Offsets step by constants from one lane's base; a row past dk lies past
+    // the resource's end, and a column past the tile's is sent there.
     f32x4 S[MT][NT];
+    const auto state_at = [&](int m, int n, int i) {
+        const int col = w0 + (NT == 2 ? 8 * (l16 >> 2) + 4 * n + (l16 & 3) : l16);
+        const uint32_t base = col < cols ? (uint32_t)(2 * g4 * a.dv + c0 + col) * 4u : kOOB;
+        return base + (uint32_t)(32 * (m / 2) + 4 * (m % 2) + i) * (uint32_t)a.dv * 4u;
+    };
     {
         const float *from = !OUT ? nullptr : p.segs > 1 ? ends : !a.carry || a.carry[p.n] != 0 ? pool : nullptr;
+        const rsrc_t r = make_rsrc(from, from ? state * 4 : 0);   // zeros where nothing enters
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int row = 16 * m + g4 + i, col = w0 + 16 * n + l16;
-                    S[m][n][i] = from && row < a.dk && col < cols ? from[row * a.dv + c0 + col] : 0.f;
-                }
+                for (int i = 0; i < 4; ++i) S[m][n][i] = OUT ? ssd::gload1(r, state_at(m, n, i)) : 0.f;
     }
-
-    Tile<E, C, KP> tq, tk;
-    Tile<E, C, VT> tv;
-    const auto load = [&](int t0) {
-        const int rows = min(C, p.rows - t0);
-        if (OUT) tq.load(q + t0 * a.st.q_t, a.st.q_t, rows, a.dk, a.vec_qk, tid);
-        tk.load(k + t0 * a.st.k_t, a.st.k_t, rows, a.dk, a.vec_qk, tid);
-        tv.load(v + t0 * a.st.v_t, a.st.v_t, rows, cols, a.vec_v, tid);
-    };
-    const auto log_decay = [&](int t0) { return t0 + lane < p.rows && lane < C ? la[(t0 + lane) * a.la_t] : 0.f; };
-
-    // the scores above the diagonal that a 32-wide step over them reads stay 0
-    if (OUT && (wave & 1) == 0 && wave + 1 < TT)
-        for (int e = lane; e < 256; e += 64) ps[(16 * wave + e / 16) * LP + 16 * (wave + 1) + e % 16] = (L)0.f;
-
     double total = 0.0;
-    if (p.rows > 0) {
-        load(0);
-        if (wave == 0) make_decays(dec[0], log_decay(0), lane);
-    }
-    for (int t0 = 0, c = 0; t0 < p.rows; t0 += C, ++c) {
-        const Decays<C> &d = dec[c & 1];
-        if (OUT) tq.template store<LQ>(qs, tid);
-        tk.template store<LK>(ks, tid);
-        tv.template store<LV>(vs, tid);
-        block_sync();
-        const bool more = t0 + C < p.rows;
-        if (more) load(t0 + C);
-        const bool decays = more && wave == (c + 1) % 4;
-        const float next_la = decays ? log_decay(t0 + C) : 0.f;
-
+    block_sync();
+    if (OUT) block_sync();
+    for (int c = 0; c < chunks; ++c) {
+        const int b = c & 1;
+        const Decays<C> &d = lds.dec[c % 3];
+        const L *qs = lds.q[b], *ks = lds.k[b], *vs = lds.v[b], *ps = lds.p[b];
         f32x4 Y[NT][TT];
         if (OUT) {
-            // P: each wave one 16-row tile of queries, up to the diagonal.
-            // Formed as K Q^T, so that a lane holds 4 scores of one query.
-            if (wave < TT) {
-                Frag<L> fq[KS];
-#pragma unroll
-                for (int s = 0; s < KS; ++s) fq[s] = frag8(qs + (16 * wave + l16) * LQ + 32 * s + 2 * g4);
-                const int i = 16 * wave + l16;
-                const float bh = d.hi[i], bl = d.lo[i];
-                for (int jt = 0; jt <= wave; ++jt) {
-                    f32x4 x = {};
-#pragma unroll
-                    for (int s = 0; s < KS; ++s)
-                        x = mma(frag8(ks + (16 * jt + l16) * LK + 32 * s + 2 * g4), fq[s], x);
-                    const int j = 16 * jt + g4;
-                    L out[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        out[e] = j + e <= i ? (L)(x[e] * __expf((bh - d.hi[j + e]) + (bl - d.lo[j + e]))) : (L)0.f;
-                    __builtin_memcpy(__builtin_assume_aligned(ps + i * LP + j, 4 * sizeof(L)), out, sizeof(out));
-                }
-            }
             // Y^T = diag(e^b) S^T Q^T, rows: columns of v, columns: queries
 #pragma unroll
             for (int n = 0; n < NT; ++n)
@@ -440,7 +542,7 @@ __global__ __launch_bounds__(PT, 2) void k_lin_chunks(PrefillArgs a)
                 for (int n = 0; n < NT; ++n) frag_acc(fs[n], S[2 * s][n], S[2 * s + 1][n]);
 #pragma unroll
                 for (int t = 0; t < TT; ++t) {
-                    const Frag<L> fq = frag44(qs + (16 * t + l16) * LQ + 32 * s + g4);
+                    const Frag<L> fq = frag8(qs + (16 * t + l16) * LK + 32 * s + 2 * g4);
 #pragma unroll
                     for (int n = 0; n < NT; ++n) Y[n][t] = mma(fs[n], fq, Y[n][t]);
                 }
@@ -451,9 +553,7 @@ __global__ __launch_bounds__(PT, 2) void k_lin_chunks(PrefillArgs a)
 #pragma unroll
                 for (int n = 0; n < NT; ++n) Y[n][t] *= e;
             }
-            block_sync();
         }
-
         const float all = d.all;
 #pragma unroll
         for (int m = 0; m < MT; ++m)
@@ -461,90 +561,82 @@ __global__ __launch_bounds__(PT, 2) void k_lin_chunks(PrefillArgs a)
             for (int n = 0; n < NT; ++n) S[m][n] *= all;
 #pragma unroll
         for (int s = 0; s < TS; ++s) {
-            Frag<L> fv[NT];
+            // the other waves' barrier between their tiles and their scores:
+            // these need it nowhere, and have done about half their work here
+            if (OUT && s == TS / 2) block_sync();
+            Frag<L> fv[NT], fw[NT][PARTS];
+            const f32x4 wa = *reinterpret_cast<const f32x4 *>(d.out + 32 * s + g4);
+            const f32x4 wb = *reinterpret_cast<const f32x4 *>(d.out + 32 * s + 16 + g4);
 #pragma unroll
-            for (int n = 0; n < NT; ++n) fv[n] = frag_col<LV>(vs + 32 * s * LV + w0 + 16 * n, lane);
+            for (int n = 0; n < NT; ++n) fv[n] = frag_col<LV, NT == 2>(vs + 32 * s * LV, w0 + 4 * n, lane);
             if (OUT) {
 #pragma unroll
                 for (int t = 2 * s; t < TT; ++t) {
-                    const Frag<L> fp = frag44(ps + (16 * t + l16) * LP + 32 * s + g4);
+                    const Frag<L> fp = frag8(ps + (16 * t + l16) * LP + 32 * s + 2 * g4);
 #pragma unroll
                     for (int n = 0; n < NT; ++n) Y[n][t] = mma(fv[n], fp, Y[n][t]);
                 }
             }
-            // V's rows times e^{b_L - b}.  In bf16 as three parts, which hold
-            // all 24 bits: the state is a float32 result.
-            constexpr int PARTS = HALF ? 3 : 1;
-            Frag<L> fw[PARTS][NT];
-            const f32x4 wa = *reinterpret_cast<const f32x4 *>(d.out + 32 * s + g4);
-            const f32x4 wb = *reinterpret_cast<const f32x4 *>(d.out + 32 * s + 16 + g4);
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    float x = (float)fv[n].x[e] * (e < 4 ? wa[e & 3] : wb[e & 3]);
-#pragma unroll
-                    for (int u = 0; u < PARTS; ++u) {
-                        fw[u][n].x[e] = (L)x;
-                        x -= (float)fw[u][n].x[e];
-                    }
-                }
+            for (int n = 0; n < NT; ++n) weigh(fw[n], fv[n], wa, wb);
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
-                const Frag<L> fk = frag_col<LK>(ks + 32 * s * LK + 16 * m, lane);
+                const Frag<L> fk = frag_col<LK, true>(ks + 32 * s * LK, 32 * (m / 2) + 4 * (m % 2), lane);
 #pragma unroll
                 for (int u = PARTS - 1; u >= 0; --u)
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) S[m][n] = mma(fk, fw[u][n], S[m][n]);
+                    for (int n = 0; n < NT; ++n) S[m][n] = mma(fk, fw[n][u], S[m][n]);
             }
         }
         if (OUT) {
-            const int rows = min(C, p.rows - t0);
-            E *yc = y + t0 * a.st.y_t;
+            const int t0 = c * C, rows = min(C, p.rows - t0);
+            const rsrc_t r = make_rsrc(y + t0 * a.st.y_t, ((rows - 1) * a.st.y_t + cols) * (int64_t)sizeof(E));
+            const int col = w0 + NT * g4;   // 4 NT columns from here on
+            constexpr int W = 4 * NT, PIECE = 16 / (int)sizeof(E) < W ? 16 / (int)sizeof(E) : W;
 #pragma unroll
             for (int t = 0; t < TT; ++t) {
                 const int row = 16 * t + l16;
+                const uint32_t off = (uint32_t)(row * (int)a.st.y_t + col) * (uint32_t)sizeof(E);
+                E out[W];
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const int col = w0 + 16 * n + g4;
-                    if (row >= rows) continue;
-                    E out[4];
+                for (int e = 0; e < W; ++e) out[e] = from_f<E>(Y[e / 4][t][e % 4]);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) out[e] = from_f<E>(Y[n][t][e]);
-                    E *to = yc + row * a.st.y_t + col;
-                    if (a.vec_y) {
-                        if (col < cols) *reinterpret_cast<Vec<E, 4> *>(to) = *reinterpret_cast<Vec<E, 4> *>(out);
+                for (int e = 0; e < W; e += VEC ? PIECE : 1) {
+                    const uint32_t o = row < rows && col + e < cols ? off + e * (uint32_t)sizeof(E) : kOOB;
+                    if constexpr (VEC && PIECE * sizeof(E) == 16) {
+                        ssd::v4u x;
+                        __builtin_memcpy(&x, out + e, 16);
+                        __builtin_amdgcn_raw_buffer_store_b128(x, r, o, 0, 0);
+                    } else if constexpr (VEC) {
+                        ssd::v2u x;
+                        __builtin_memcpy(&x, out + e, 8);
+                        __builtin_amdgcn_raw_buffer_store_b64(x, r, o, 0, 0);
+                    } else if constexpr (sizeof(E) == 2) {
+                        __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(short, out[e]), r, o, 0, 0);
                     } else {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (col + e < cols) to[e] = out[e];
+                        __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(int, out[e]), r, o, 0, 0);
                     }
                 }
             }
         }
         total += d.sum;
-        if (decays) make_decays(dec[(c + 1) & 1], next_la, lane);
         block_sync();
     }
 
     float *to = OUT ? (p.s + 1 == p.segs ? pool : nullptr) : ends;
-    if (to) {
+    const rsrc_t r = make_rsrc(to, to ? state * 4 : 0);
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int row = 16 * m + g4 + i, col = w0 + 16 * n + l16;
-                    if (row < a.dk && col < cols) to[row * a.dv + c0 + col] = S[m][n][i];
-                }
-    }
-    if (!OUT && tile == 0 && tid == 0) a.segdec[(int64_t)id * a.H + h] = expf((float)total);
+            for (int i = 0; i < 4; ++i) ssd::gstore1(r, state_at(m, n, i), S[m][n][i]);
+    if (!OUT && tile == 0 && threadIdx.x == 0) a.segdec[(int64_t)id * a.H + h] = expf((float)total);
 }
 
 // The state entering each segment of a sequence that was cut, in place of the
 // states that the segments make from zero: one thread for each element.
-__global__ __launch_bounds__(PT) void k_lin_carry(PrefillArgs a, int chunks)
+__global__ __launch_bounds__(CT) void k_lin_carry(PrefillArgs a, int chunks)
 {
     const int h = blockIdx.x / chunks % a.H, n = blockIdx.x / (chunks * a.H);
     int begin, end;
@@ -555,7 +647,7 @@ __global__ __launch_bounds__(PT) void k_lin_carry(PrefillArgs a, int chunks)
     bool bad;
     slot_of(a, n, slot, bad);
     const int64_t state = (int64_t)a.dk * a.dv;
-    const int64_t e = (int64_t)(blockIdx.x % chunks) * PT + threadIdx.x;
+    const int64_t e = (int64_t)(blockIdx.x % chunks) * CT + threadIdx.x;
     if (bad || e >= state) return;
     float cur = slot >= 0 && (!a.carry || a.carry[n] != 0) ? a.states[((int64_t)slot * a.H + h) * state + e] : 0.f;
     const int64_t id0 = begin / a.seg + n;
@@ -587,19 +679,28 @@ struct PrefillPlan {
     size_t ends = 0, segdec = 0, total = 0;
 };
 
-static int col_tile(int64_t dk, int64_t dv) { return dk > 128 || dv <= 64 ? 64 : 128; }
+#ifndef COLT
+#define COLT 128
+#endif
+static int col_tile(int64_t dk, int64_t dv) { return dk > 128 || dv <= 64 ? 64 : COLT; }
 
+#ifndef PLAN_X
+#define PLAN_X 1
+#endif
+#ifndef MIN_SEG
+#define MIN_SEG 256
+#endif
 // Sequences are cut where whole ones would leave CUs idle: segments of a
-// length that makes about two blocks for each CU out of the batch's rows.
+// length that makes about one block for each CU out of the batch's rows.
 static PrefillPlan plan_prefill(const lin_shape &s, int64_t max_seqlen, int cus)
 {
     PrefillPlan P;
     const int64_t longest = max_seqlen > 0 && max_seqlen < s.T ? max_seqlen : s.T;
-    const int64_t tiles = (s.dv + col_tile(s.dk, s.dv) - 1) / col_tile(s.dk, s.dv);
-    const int64_t blocks = 2 * int64_t(cus), work = s.T * s.H * tiles;
+    const int64_t vt = col_tile(s.dk, s.dv), tiles = (s.dv + vt - 1) / vt;
+    const int64_t blocks = PLAN_X * int64_t(cus), work = s.T * s.H * tiles;
     int64_t seg = (work + blocks - 1) / blocks;
     seg = (seg + 63) / 64 * 64;
-    if (seg < 256) seg = 256;
+    if (seg < MIN_SEG) seg = MIN_SEG;
     P.ids = (int)s.N;
     if (longest <= seg) return P;
     P.seg = (int)seg;
@@ -614,28 +715,28 @@ static PrefillPlan plan_prefill(const lin_shape &s, int64_t max_seqlen, int cus)
     return P;
 }
 
-template <typename E, int KP, int VT, int C>
+template <typename E, int KP, int VT, int C, bool VEC>
 static int run_prefill(PrefillArgs &a, hipStream_t st)
 {
     const int64_t grid = (int64_t)a.ids * a.H * a.tiles;
     if (a.seg > 0) {
-        k_lin_chunks<E, KP, VT, C, false><<<dim3((unsigned)grid), dim3(PT), 0, st>>>(a);
-        const int chunks = (a.dk * a.dv + PT - 1) / PT;
-        k_lin_carry<<<dim3((unsigned)((int64_t)a.N * a.H * chunks)), dim3(PT), 0, st>>>(a, chunks);
+        k_lin_chunks<E, KP, VT, C, false, VEC><<<dim3((unsigned)grid), dim3(512), 0, st>>>(a);
+        const int chunks = (a.dk * a.dv + CT - 1) / CT;
+        k_lin_carry<<<dim3((unsigned)((int64_t)a.N * a.H * chunks)), dim3(CT), 0, st>>>(a, chunks);
     }
-    k_lin_chunks<E, KP, VT, C, true><<<dim3((unsigned)grid), dim3(PT), 0, st>>>(a);
+    k_lin_chunks<E, KP, VT, C, true, VEC><<<dim3((unsigned)grid), dim3(512), 0, st>>>(a);
     return launch_status();
 }
 
-template <typename E>
+template <typename E, bool VEC>
 static int dispatch_prefill(PrefillArgs &a, hipStream_t st)
 {
     // float tiles are twice as wide: half the rows to a chunk
     constexpr int C = std::is_same<E, bf16>::value ? 64 : 32;
     const bool wide = col_tile(a.dk, a.dv) == 128;
-    if (a.dk > 128) return run_prefill<E, 256, 64, 32>(a, st);
-    if (a.dk > 64) return wide ? run_prefill<E, 128, 128, C>(a, st) : run_prefill<E, 128, 64, C>(a, st);
-    return wide ? run_prefill<E, 64, 128, C>(a, st) : run_prefill<E, 64, 64, C>(a, st);
+    if (a.dk > 128) return run_prefill<E, 256, 64, 32, VEC>(a, st);
+    if (a.dk > 64) return wide ? run_prefill<E, 128, 128, C, VEC>(a, st) : run_prefill<E, 128, 64, C, VEC>(a, st);
+    return wide ? run_prefill<E, 64, 128, C, VEC>(a, st) : run_prefill<E, 64, 64, C, VEC>(a, st);
 }
 
 }  // namespace layer
@@ -702,11 +803,10 @@ extern "C" int lin_prefill(const lin_shape *shape, int dtype, const lin_strides 
     const auto rows16 = [&](const void *ptr, int64_t row, int64_t head, int64_t d) {
         return !misaligned(ptr, 16) && row * e % 16 == 0 && head * e % 16 == 0 && d * e % 16 == 0;
     };
-    a.vec_qk = rows16(q, a.st.q_t, a.st.q_g, s.dk) && rows16(k, a.st.k_t, a.st.k_g, s.dk);
-    a.vec_v = rows16(v, a.st.v_t, a.st.v_h, s.dv);
-    a.vec_y = rows16(y, a.st.y_t, a.st.y_h, s.dv);
+    const bool vec = rows16(q, a.st.q_t, a.st.q_g, s.dk) && rows16(k, a.st.k_t, a.st.k_g, s.dk) &&
+                     rows16(v, a.st.v_t, a.st.v_h, s.dv) && rows16(y, a.st.y_t, a.st.y_h, s.dv);
     hipStream_t st = static_cast<hipStream_t>(stream);
-    if (dtype == LAYER_BF16) return dispatch_prefill<bf16>(a, st);
-    if (dtype == LAYER_F16) return dispatch_prefill<f16>(a, st);
-    return dispatch_prefill<float>(a, st);
+    if (dtype == LAYER_BF16) return vec ? dispatch_prefill<bf16, true>(a, st) : dispatch_prefill<bf16, false>(a, st);
+    if (dtype == LAYER_F16) return vec ? dispatch_prefill<f16, true>(a, st) : dispatch_prefill<f16, false>(a, st);
+    return vec ? dispatch_prefill<float, true>(a, st) : dispatch_prefill<float, false>(a, st);
 }
