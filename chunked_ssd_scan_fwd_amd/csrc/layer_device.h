@@ -36,11 +36,11 @@ __device__ __forceinline__ int index_of(const int32_t *ids, int i) { return ids 
 inline int launch_status() { return hipGetLastError() == hipSuccess ? SSD_OK : SSD_ERR_DEVICE; }
 
 // Runs BODY with T the element type that `dtype` names.
-#define LAYER_DISPATCH(DTYPE, BODY)                                \
+#define LAYER_DISPATCH(DTYPE, ...)                                 \
     do {                                                           \
-        if ((DTYPE) == LAYER_BF16) { using T = layer::bf16; BODY; } \
-        else if ((DTYPE) == LAYER_F16) { using T = layer::f16; BODY; } \
-        else { using T = float; BODY; }                            \
+        if ((DTYPE) == LAYER_BF16) { using T = layer::bf16; __VA_ARGS__; } \
+        else if ((DTYPE) == LAYER_F16) { using T = layer::f16; __VA_ARGS__; } \
+        else { using T = float; __VA_ARGS__; }                            \
     } while (0)
 
 }  // namespace layer

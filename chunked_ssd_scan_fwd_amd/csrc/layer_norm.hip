@@ -7,71 +7,170 @@
 //   dx = rstd (d - mean(d) - xh mean(d xh)),
 //   dgate = dy z act'(gate),  dweight = sum dz xh,  dbias = sum dz.
 // act is SiLU: act(u) = u s, act'(u) = s (1 + u (1 - s)), s = 1 / (1 + e^-u).
+//
+// Memory bounds all of it.  Two ways through the data:
+//
+// * A sample's run of M values that fits the registers of its threads (up to
+//   64 lanes of a wave, or one block) is read once: k_gn_fwd_held and
+//   k_gn_bwd_held.  The threads of a block keep their channels from sample to
+//   sample, so the backward sums dweight and dbias in registers.
+// * Longer runs are cut into parts of rows.  k_gn_sums reads them once for
+//   each channel's sums over a part, k_gn_mid joins these for each run, and
+//   k_gn_apply reads the data again.
+//
+// k_gn_wsum adds up the parts of dweight and dbias in a fixed order.
 #include "layer_device.h"
+#include "ssd_internal.h"
 
 namespace layer {
 
-constexpr int GT = 256;   // threads of a block
+constexpr int GT = 512;   // threads of a block
+constexpr int HELD = 4;   // most pieces of a run that a thread holds
 
 struct GnArgs {
     const void *x, *gate, *dy;
     const float *w, *b;
     void *y, *dx, *dgate;
-    float *stats, *dw, *db, *part;
-    int64_t N, ldx, ldg, ldy, nparts;
+    float *stats, *dw, *db;
+    float *part;        // held: [nparts][2][C]; cut: [N][nparts][2][C]
+    float *mean;        // cut, backward: [N][groups][2], mean(d) and mean(d xh)
+    int64_t N, ldx, ldg, ldy;
+    int64_t nparts, per;   // cut: parts of a sample, rows of a part
     int L, C, groups, cg;
     float eps;
+    bool silu;
+    // held: 2^lw threads to a run; gs runs of one sample side by side in a
+    // block (of sets blocks for all of them), rpb samples; a run's rows have
+    // ppr pieces, the run has `pieces`
+    int lw, gs, rpb, sets, ppr, pieces;
 };
 
-__device__ __forceinline__ float sigmoid(float u) { return 1.f / (1.f + expf(-u)); }
-
-// Sum over the block, in every thread.
-__device__ __forceinline__ float block_sum(float x, float *red)
+struct Act {
+    float f, df;   // act(u) and act'(u)
+};
+__device__ __forceinline__ Act act(float u, bool silu)
 {
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) x += __shfl_xor(x, d);
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = x;
-    __syncthreads();
-    float s = 0.f;
-#pragma unroll
-    for (int w = 0; w < GT / 64; ++w) s += red[w];
-    return s;
+    if (!silu) return {u, 1.f};
+    const float s = __builtin_amdgcn_rcpf(1.f + __expf(-u));
+    return {u * s, s * (1.f + u * (1.f - s))};
 }
 
-// One block for a sample's run of channels.
-template <typename T>
-__global__ __launch_bounds__(GT) void k_gn_fwd(GnArgs a, bool silu)
+template <typename T, int VE>
+__device__ __forceinline__ Vec<T, VE> load(const T *p, bool on)
 {
-    __shared__ float red[GT / 64];
-    const int64_t n = blockIdx.x / a.groups;
-    const int c0 = (int)(blockIdx.x % a.groups) * a.cg;
-    const int64_t M = (int64_t)a.L * a.cg;
-    const T *x = static_cast<const T *>(a.x) + n * a.L * a.ldx + c0;
-    const auto each = [&](auto f) {
-        for (int64_t e = threadIdx.x; e < M; e += GT) f(e / a.cg, (int)(e % a.cg));
-    };
-    float s = 0.f;
-    each([&](int64_t l, int c) { s += to_f(x[l * a.ldx + c]); });
-    const float mu = block_sum(s, red) / (float)M;
-    s = 0.f;
-    each([&](int64_t l, int c) {
-        const float d = to_f(x[l * a.ldx + c]) - mu;
-        s += d * d;
-    });
-    const float rstd = 1.f / sqrtf(block_sum(s, red) / (float)M + a.eps);
-    if (threadIdx.x == 0) {
-        a.stats[2 * blockIdx.x] = mu;
-        a.stats[2 * blockIdx.x + 1] = rstd;
+    Vec<T, VE> r = {};
+    if (on) r = *reinterpret_cast<const Vec<T, VE> *>(p);
+    return r;
+}
+// weight or bias of VE channels
+template <int VE>
+__device__ __forceinline__ void channels(float (&to)[VE], const float *p, float none, bool on)
+{
+#pragma unroll
+    for (int i = 0; i < VE; ++i) to[i] = p && on ? p[i] : none;
+}
+
+// Sum over a run's 2^lw threads, in each of them: up to a wave's lanes, or the
+// whole block (then every thread of the block calls it).
+__device__ __forceinline__ void run_sum(float &a, float &b, int lw, float (&red)[2][GT / 64])
+{
+    const int lanes = lw > 6 ? 6 : lw;
+    for (int d = 1; d < 1 << lanes; d *= 2) {
+        a += __shfl_xor(a, d);
+        b += __shfl_xor(b, d);
     }
-    T *y = static_cast<T *>(a.y) + n * a.L * a.C + c0;
-    const T *gate = a.gate ? static_cast<const T *>(a.gate) + n * a.L * a.ldg + c0 : nullptr;
-    each([&](int64_t l, int c) {
-        const float z = (to_f(x[l * a.ldx + c]) - mu) * rstd * (a.w ? a.w[c0 + c] : 1.f) + (a.b ? a.b[c0 + c] : 0.f);
-        const float u = gate ? to_f(gate[l * a.ldg + c]) : z;
-        const float act = silu ? u * sigmoid(u) : u;
-        y[l * a.C + c] = from_f<T>(gate ? z * act : act);
-    });
+    if (lw <= 6) return;
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) {
+        red[0][threadIdx.x >> 6] = a;
+        red[1][threadIdx.x >> 6] = b;
+    }
+    __syncthreads();
+    a = b = 0.f;
+#pragma unroll
+    for (int w = 0; w < GT / 64; ++w) {
+        a += red[0][w];
+        b += red[1][w];
+    }
+}
+
+// Where a thread of the held kernels works: run `run` of every rpb-th sample
+// from `first` on, piece k at row l[k] and channel c[k] of the sample.
+template <int VE, int K>
+struct Held {
+    int run, first, c[K], l[K];
+    bool on[K];
+    __device__ __forceinline__ explicit Held(const GnArgs &a)
+    {
+        const int set = blockIdx.x % a.sets, slot = threadIdx.x >> a.lw, j = threadIdx.x & ((1 << a.lw) - 1);
+        const int rs = slot / a.gs, g = set * a.gs + slot % a.gs;
+        const bool live = rs < a.rpb && g < a.groups;
+        run = live ? g : -1;
+        first = blockIdx.x / a.sets * a.rpb + rs;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int p = j + (k << a.lw);
+            on[k] = live && p < a.pieces;
+            l[k] = p / a.ppr;
+            c[k] = g * a.cg + p % a.ppr * VE;
+        }
+    }
+};
+
+template <typename T, int VE, int K>
+__global__ __launch_bounds__(GT) void k_gn_fwd_held(GnArgs a)
+{
+    __shared__ float red[2][GT / 64];
+    const Held<VE, K> h(a);
+    if (h.run < 0) return;   // a run's threads leave together
+    const int64_t step = (int64_t)(gridDim.x / a.sets) * a.rpb;
+    const float inv = 1.f / ((float)a.L * (float)a.cg);
+    const bool first = (threadIdx.x & ((1 << a.lw) - 1)) == 0;
+    for (int64_t n = h.first; n < a.N; n += step) {
+        Vec<T, VE> x[K], gt[K];
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int64_t row = n * a.L + h.l[k];
+            x[k] = load<T, VE>(static_cast<const T *>(a.x) + row * a.ldx + h.c[k], h.on[k]);
+            if (a.gate) gt[k] = load<T, VE>(static_cast<const T *>(a.gate) + row * a.ldg + h.c[k], h.on[k]);
+        }
+        float s = 0.f, none = 0.f;
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int i = 0; i < VE; ++i) s += to_f(x[k].v[i]);   // absent ones are 0
+        run_sum(s, none, a.lw, red);
+        const float mu = s * inv;
+        float q = 0.f;
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int i = 0; i < VE; ++i) {
+                const float d = to_f(x[k].v[i]) - mu;
+                q += h.on[k] ? d * d : 0.f;
+            }
+        run_sum(q, none, a.lw, red);
+        const float rstd = 1.f / sqrtf(q * inv + a.eps);
+        if (first) {
+            float *st = a.stats + 2 * (n * a.groups + h.run);
+            st[0] = mu;
+            st[1] = rstd;
+        }
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            if (!h.on[k]) continue;
+            float w[VE], b[VE];
+            channels<VE>(w, a.w ? a.w + h.c[k] : nullptr, 1.f, true);
+            channels<VE>(b, a.b ? a.b + h.c[k] : nullptr, 0.f, true);
+            Vec<T, VE> y;
+#pragma unroll
+            for (int i = 0; i < VE; ++i) {
+                const float z = (to_f(x[k].v[i]) - mu) * rstd * w[i] + b[i];
+                y.v[i] = from_f<T>(a.gate ? z * act(to_f(gt[k].v[i]), a.silu).f : act(z, a.silu).f);
+            }
+            *reinterpret_cast<Vec<T, VE> *>(static_cast<T *>(a.y) + (n * a.L + h.l[k]) * a.C + h.c[k]) = y;
+        }
+    }
 }
 
 struct GnGrad {
@@ -84,88 +183,338 @@ __device__ __forceinline__ GnGrad gn_grad(float x, float mu, float rstd, float w
 {
     GnGrad r;
     r.xh = (x - mu) * rstd;
-    const float z = r.xh * w + b, u = gated ? gate : z;
-    const float s = silu ? sigmoid(u) : 1.f;
-    const float d = silu ? s * (1.f + u * (1.f - s)) : 1.f;
-    r.dz = gated ? dy * (u * s) : dy * d;
-    r.dgate = dy * z * d;
+    const float z = r.xh * w + b;
+    const Act t = act(gated ? gate : z, silu);
+    r.dz = dy * (gated ? t.f : t.df);
+    r.dgate = dy * z * t.df;
     return r;
 }
 
-template <typename T>
-__global__ __launch_bounds__(GT) void k_gn_bwd(GnArgs a, bool silu)
+// Adds up what the threads of a block hold of dweight or dbias, in a fixed
+// order, into the block's row of `part`: `held` lists it by thread slot and
+// piece; a channel's values are those of its run's rows and of the block's
+// samples.  As many threads take a channel as there are for all.
+template <int VE, int K>
+__device__ __forceinline__ void held_part(const GnArgs &a, const float (&v)[K][VE], float *held, float *sub, float *to)
 {
-    __shared__ float red[GT / 64];
+    const int W = 1 << a.lw;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int i = 0; i < VE; ++i) held[((threadIdx.x >> a.lw) * K * W + k * W + (threadIdx.x & (W - 1))) * VE + i] = v[k][i];
+    __syncthreads();
+    const int set = blockIdx.x % a.sets, cb = min(a.gs, a.groups - set * a.gs) * a.cg;   // the block's channels
+    int ns = 1;
+    while (ns * 2 * cb <= GT) ns *= 2;
+    const int terms = a.rpb * a.L;
+    for (int c0 = 0; c0 < cb; c0 += GT / ns) {
+        const int c = c0 + (int)threadIdx.x / ns, s = threadIdx.x % ns;
+        float t = 0.f;
+        if (c < cb) {
+            const int g = c / a.cg, ch = c % a.cg;
+            for (int e = s; e < terms; e += ns) {
+                const int rs = e / a.L, l = e % a.L;
+                t += held[((rs * a.gs + g) * K * W + l * a.ppr + ch / VE) * VE + ch % VE];
+            }
+        }
+        sub[threadIdx.x] = t;
+        __syncthreads();
+        if (s == 0 && c < cb) {
+            for (int i = 1; i < ns; ++i) t += sub[threadIdx.x + i];
+            to[set * a.gs * a.cg + c] = t;
+        }
+        __syncthreads();
+    }
+}
+
+template <typename T, int VE, int K>
+__global__ __launch_bounds__(GT) void k_gn_bwd_held(GnArgs a)
+{
+    __shared__ float red[2][GT / 64], held[GT * VE * K], sub[GT];
+    const Held<VE, K> h(a);
+    const int64_t step = (int64_t)(gridDim.x / a.sets) * a.rpb;
+    const float inv = 1.f / ((float)a.L * (float)a.cg);
+    float aw[K][VE] = {}, ab[K][VE] = {}, w[K][VE], b[K][VE];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        channels<VE>(w[k], a.w ? a.w + h.c[k] : nullptr, 1.f, h.on[k]);
+        channels<VE>(b[k], a.b ? a.b + h.c[k] : nullptr, 0.f, h.on[k]);
+    }
+    if (h.run >= 0)
+        for (int64_t n = h.first; n < a.N; n += step) {
+            Vec<T, VE> x[K], gt[K], dy[K];
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                const int64_t row = n * a.L + h.l[k];
+                x[k] = load<T, VE>(static_cast<const T *>(a.x) + row * a.ldx + h.c[k], h.on[k]);
+                dy[k] = load<T, VE>(static_cast<const T *>(a.dy) + row * a.ldy + h.c[k], h.on[k]);
+                if (a.gate) gt[k] = load<T, VE>(static_cast<const T *>(a.gate) + row * a.ldg + h.c[k], h.on[k]);
+            }
+            const float *st = a.stats + 2 * (n * a.groups + h.run);
+            const float mu = st[0], rstd = st[1];
+            float xh[K][VE], d[K][VE], s1 = 0.f, s2 = 0.f;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                Vec<T, VE> dg;
+#pragma unroll
+                for (int i = 0; i < VE; ++i) {
+                    const GnGrad r = gn_grad(to_f(x[k].v[i]), mu, rstd, w[k][i], b[k][i], a.gate != nullptr,
+                                             a.gate ? to_f(gt[k].v[i]) : 0.f, to_f(dy[k].v[i]), a.silu);
+                    const float dz = h.on[k] ? r.dz : 0.f;
+                    xh[k][i] = h.on[k] ? r.xh : 0.f;
+                    d[k][i] = dz * w[k][i];
+                    s1 += d[k][i];
+                    s2 += d[k][i] * xh[k][i];
+                    aw[k][i] += dz * xh[k][i];
+                    ab[k][i] += dz;
+                    dg.v[i] = from_f<T>(r.dgate);
+                }
+                if (a.dgate && h.on[k])
+                    *reinterpret_cast<Vec<T, VE> *>(static_cast<T *>(a.dgate) + (n * a.L + h.l[k]) * a.C + h.c[k]) = dg;
+            }
+            if (!a.dx) continue;
+            run_sum(s1, s2, a.lw, red);
+            const float m1 = s1 * inv, m2 = s2 * inv;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                if (!h.on[k]) continue;
+                Vec<T, VE> dx;
+#pragma unroll
+                for (int i = 0; i < VE; ++i) dx.v[i] = from_f<T>(rstd * (d[k][i] - m1 - xh[k][i] * m2));
+                *reinterpret_cast<Vec<T, VE> *>(static_cast<T *>(a.dx) + (n * a.L + h.l[k]) * a.C + h.c[k]) = dx;
+            }
+        }
+    if (!a.part) return;
+    float *part = a.part + 2 * (int64_t)(blockIdx.x / a.sets) * a.C;
+    held_part<VE, K>(a, aw, held, sub, part);
+    held_part<VE, K>(a, ab, held, sub, part + a.C);
+}
+
+// ---- runs that are cut into parts of rows
+//
+// A block takes a part of a sample: cp threads side by side on a row's
+// pieces (of tiles of GT of them), GT / cp rows at a time.
+
+template <int VE>
+struct Cut {
+    int64_t n, part;
+    int c, r0, rp, l0, l1;   // channel, first row, rows at a time; the part's rows
+    bool on;
+    __device__ __forceinline__ explicit Cut(const GnArgs &a)
+    {
+        const int cp = min(a.C / VE, GT), tiles = (a.C / VE + GT - 1) / GT;
+        const int tile = blockIdx.x % tiles;
+        part = blockIdx.x / tiles % a.nparts;
+        n = blockIdx.x / tiles / a.nparts;
+        rp = GT / cp;
+        c = (tile * GT + (int)threadIdx.x % cp) * VE;
+        r0 = threadIdx.x / cp;
+        on = r0 < rp && c < a.C;
+        l0 = (int)(part * a.per);
+        l1 = (int)min((part + 1) * a.per, (int64_t)a.L);
+    }
+};
+
+// A part's sums for each channel.  Forward: mean and sum of squares about it,
+// formed from differences to the thread's first value, so that a mean far
+// from zero costs no accuracy.  Backward: sums of dz and dz xh.
+template <typename T, int VE, bool BWD>
+__global__ __launch_bounds__(GT) void k_gn_sums(GnArgs a)
+{
+    __shared__ float red[2][GT * VE], cnt[GT];
+    const Cut<VE> p(a);
+    float s[2][VE] = {}, x0[VE] = {}, w[VE], b[VE], mu[VE], rstd[VE];
+    int rows = 0;
+    if (p.on) {
+        if (BWD) {
+            channels<VE>(w, a.w ? a.w + p.c : nullptr, 1.f, true);
+            channels<VE>(b, a.b ? a.b + p.c : nullptr, 0.f, true);
+#pragma unroll
+            for (int i = 0; i < VE; ++i) {
+                const float *st = a.stats + 2 * (p.n * a.groups + (p.c + i) / a.cg);
+                mu[i] = st[0];
+                rstd[i] = st[1];
+            }
+        }
+#pragma unroll 4
+        for (int l = p.l0 + p.r0; l < p.l1; l += p.rp) {
+            const int64_t row = p.n * a.L + l;
+            const Vec<T, VE> x = load<T, VE>(static_cast<const T *>(a.x) + row * a.ldx + p.c, true);
+            Vec<T, VE> dy = {}, gt = {};
+            if (BWD) {
+                dy = load<T, VE>(static_cast<const T *>(a.dy) + row * a.ldy + p.c, true);
+                if (a.gate) gt = load<T, VE>(static_cast<const T *>(a.gate) + row * a.ldg + p.c, true);
+            }
+#pragma unroll
+            for (int i = 0; i < VE; ++i) {
+                if (BWD) {
+                    const GnGrad r = gn_grad(to_f(x.v[i]), mu[i], rstd[i], w[i], b[i], a.gate != nullptr,
+                                             to_f(gt.v[i]), to_f(dy.v[i]), a.silu);
+                    s[0][i] += r.dz * r.xh;
+                    s[1][i] += r.dz;
+                } else {
+                    if (rows == 0) x0[i] = to_f(x.v[i]);
+                    const float d = to_f(x.v[i]) - x0[i];
+                    s[0][i] += d;
+                    s[1][i] += d * d;
+                }
+            }
+            ++rows;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < VE; ++i) {
+        if (!BWD && rows > 0) {
+            const float m = s[0][i] / (float)rows;
+            s[1][i] = fmaxf(s[1][i] - m * s[0][i], 0.f) + 0.f * s[1][i];   // and a NaN stays one
+            s[0][i] = x0[i] + m;
+        }
+        red[0][threadIdx.x * VE + i] = s[0][i];
+        red[1][threadIdx.x * VE + i] = s[1][i];
+    }
+    cnt[threadIdx.x] = (float)rows;
+    __syncthreads();
+    if (p.on && p.r0 == 0) {
+        const int cp = min(a.C / VE, GT);
+        float *to = a.part + (p.n * a.nparts + p.part) * 2 * a.C + p.c;
+#pragma unroll
+        for (int i = 0; i < VE; ++i) {
+            float u = 0.f, v = 0.f;
+            if (BWD) {
+                for (int r = 0; r < p.rp; ++r) {
+                    u += red[0][(threadIdx.x + r * cp) * VE + i];
+                    v += red[1][(threadIdx.x + r * cp) * VE + i];
+                }
+            } else {
+                const float base = red[0][threadIdx.x * VE + i];   // the part has a row, and this thread the first
+                float n = 0.f;
+                for (int r = 0; r < p.rp; ++r) {
+                    const float k = cnt[threadIdx.x + r * cp];
+                    if (k > 0.f) u += k * (red[0][(threadIdx.x + r * cp) * VE + i] - base);
+                    n += k;
+                }
+                u = base + u / n;
+                for (int r = 0; r < p.rp; ++r) {
+                    const float k = cnt[threadIdx.x + r * cp];
+                    const float d = red[0][(threadIdx.x + r * cp) * VE + i] - u;
+                    if (k > 0.f) v += red[1][(threadIdx.x + r * cp) * VE + i] + k * d * d;
+                }
+            }
+            to[i] = u;
+            to[a.C + i] = v;
+        }
+    }
+}
+
+// Joins a run's parts and channels: forward, its statistics; backward,
+// mean(d) and mean(d xh).  One block for each run.
+template <bool BWD>
+__global__ __launch_bounds__(GT) void k_gn_mid(GnArgs a)
+{
+    __shared__ float red[2][GT / 64];
     const int64_t n = blockIdx.x / a.groups;
     const int c0 = (int)(blockIdx.x % a.groups) * a.cg;
-    const int64_t M = (int64_t)a.L * a.cg;
-    const T *x = static_cast<const T *>(a.x) + n * a.L * a.ldx + c0;
-    const T *dy = static_cast<const T *>(a.dy) + n * a.L * a.ldy + c0;
-    const T *gate = a.gate ? static_cast<const T *>(a.gate) + n * a.L * a.ldg + c0 : nullptr;
-    const float mu = a.stats[2 * blockIdx.x], rstd = a.stats[2 * blockIdx.x + 1];
-    const auto each = [&](auto f) {
-        for (int64_t e = threadIdx.x; e < M; e += GT) {
-            const int64_t l = e / a.cg;
+    const float *part = a.part + n * a.nparts * 2 * a.C + c0;
+    const int64_t items = a.nparts * a.cg;
+    const float inv = 1.f / ((float)a.L * (float)a.cg);
+    float s = 0.f, t = 0.f;
+    if (BWD) {
+        for (int64_t e = threadIdx.x; e < items; e += GT) {
             const int c = (int)(e % a.cg);
+            const float *p = part + e / a.cg * 2 * a.C + c;
             const float w = a.w ? a.w[c0 + c] : 1.f;
-            f(l, c, w, gn_grad(to_f(x[l * a.ldx + c]), mu, rstd, w, a.b ? a.b[c0 + c] : 0.f, gate != nullptr,
-                               gate ? to_f(gate[l * a.ldg + c]) : 0.f, to_f(dy[l * a.ldy + c]), silu));
+            t += p[0] * w;
+            s += p[a.C] * w;
         }
-    };
-    float s1 = 0.f, s2 = 0.f;
-    each([&](int64_t, int, float w, const GnGrad &r) {
-        s1 += r.dz * w;
-        s2 += r.dz * w * r.xh;
-    });
-    const float m1 = block_sum(s1, red) / (float)M, m2 = block_sum(s2, red) / (float)M;
-    T *dx = a.dx ? static_cast<T *>(a.dx) + n * a.L * a.C + c0 : nullptr;
-    T *dg = a.dgate ? static_cast<T *>(a.dgate) + n * a.L * a.C + c0 : nullptr;
-    each([&](int64_t l, int c, float w, const GnGrad &r) {
-        if (dx) dx[l * a.C + c] = from_f<T>(rstd * (r.dz * w - m1 - r.xh * m2));
-        if (dg) dg[l * a.C + c] = from_f<T>(r.dgate);
-    });
-}
-
-// Partial sums of dweight and dbias: 64 channels, every nparts-th row.
-template <typename T>
-__global__ __launch_bounds__(GT) void k_gn_wpart(GnArgs a, bool silu)
-{
-    __shared__ float red[2][GT];
-    const int c = blockIdx.x * 64 + (threadIdx.x & 63);
-    float sw = 0.f, sb = 0.f;
-    if (c < a.C) {
-        const float w = a.w ? a.w[c] : 1.f, b = a.b ? a.b[c] : 0.f;
-        for (int64_t r = (int64_t)blockIdx.y * 4 + (threadIdx.x >> 6); r < a.N * a.L; r += 4 * a.nparts) {
-            const float *st = a.stats + 2 * (r / a.L * a.groups + c / a.cg);
-            const GnGrad t =
-                gn_grad(to_f(static_cast<const T *>(a.x)[r * a.ldx + c]), st[0], st[1], w, b, a.gate != nullptr,
-                        a.gate ? to_f(static_cast<const T *>(a.gate)[r * a.ldg + c]) : 0.f,
-                        to_f(static_cast<const T *>(a.dy)[r * a.ldy + c]), silu);
-            sw += t.dz * t.xh;
-            sb += t.dz;
+        run_sum(s, t, 9, red);
+        s *= inv;
+        t *= inv;
+    } else {
+        const auto rows = [&](int64_t k) { return (float)(min((k + 1) * a.per, (int64_t)a.L) - k * a.per); };
+        const float base = part[0];
+        float none = 0.f;
+        for (int64_t e = threadIdx.x; e < items; e += GT) {
+            const int64_t k = e / a.cg;
+            s += rows(k) * (part[k * 2 * a.C + e % a.cg] - base);
         }
+        run_sum(s, none, 9, red);
+        s = base + s * inv;
+        for (int64_t e = threadIdx.x; e < items; e += GT) {
+            const int64_t k = e / a.cg;
+            const float *p = part + k * 2 * a.C + e % a.cg;
+            const float d = p[0] - s;
+            t += p[a.C] + rows(k) * d * d;
+        }
+        run_sum(t, none, 9, red);
+        t = 1.f / sqrtf(t * inv + a.eps);
     }
-    red[0][threadIdx.x] = sw;
-    red[1][threadIdx.x] = sb;
-    __syncthreads();
-    if (threadIdx.x < 64 && c < a.C) {
-        for (int k = 1; k < 4; ++k) {
-            sw += red[0][threadIdx.x + 64 * k];
-            sb += red[1][threadIdx.x + 64 * k];
-        }
-        a.part[(2 * (int64_t)blockIdx.y) * a.C + c] = sw;
-        a.part[(2 * (int64_t)blockIdx.y + 1) * a.C + c] = sb;
+    if (threadIdx.x == 0) {
+        float *to = (BWD ? a.mean : a.stats) + 2 * (int64_t)blockIdx.x;
+        to[0] = s;
+        to[1] = t;
     }
 }
 
-__global__ __launch_bounds__(GT) void k_gn_wsum(GnArgs a)
+template <typename T, int VE, bool BWD>
+__global__ __launch_bounds__(GT) void k_gn_apply(GnArgs a)
 {
-    const int64_t e = (int64_t)blockIdx.x * GT + threadIdx.x;
-    if (e >= 2 * (int64_t)a.C) return;
+    const Cut<VE> p(a);
+    if (!p.on) return;
+    float w[VE], b[VE], mu[VE], rstd[VE], m1[VE], m2[VE];
+    channels<VE>(w, a.w ? a.w + p.c : nullptr, 1.f, true);
+    channels<VE>(b, a.b ? a.b + p.c : nullptr, 0.f, true);
+#pragma unroll
+    for (int i = 0; i < VE; ++i) {
+        const int64_t run = 2 * (p.n * a.groups + (p.c + i) / a.cg);
+        mu[i] = a.stats[run];
+        rstd[i] = a.stats[run + 1];
+        m1[i] = BWD ? a.mean[run] : 0.f;
+        m2[i] = BWD ? a.mean[run + 1] : 0.f;
+    }
+#pragma unroll 2
+    for (int l = p.l0 + p.r0; l < p.l1; l += p.rp) {
+        const int64_t row = p.n * a.L + l;
+        const Vec<T, VE> x = load<T, VE>(static_cast<const T *>(a.x) + row * a.ldx + p.c, true);
+        Vec<T, VE> gt = {}, dy = {}, y, dg;
+        if (a.gate) gt = load<T, VE>(static_cast<const T *>(a.gate) + row * a.ldg + p.c, true);
+        if (BWD) dy = load<T, VE>(static_cast<const T *>(a.dy) + row * a.ldy + p.c, true);
+#pragma unroll
+        for (int i = 0; i < VE; ++i) {
+            if (BWD) {
+                const GnGrad r = gn_grad(to_f(x.v[i]), mu[i], rstd[i], w[i], b[i], a.gate != nullptr, to_f(gt.v[i]),
+                                         to_f(dy.v[i]), a.silu);
+                y.v[i] = from_f<T>(rstd[i] * (r.dz * w[i] - m1[i] - r.xh * m2[i]));
+                dg.v[i] = from_f<T>(r.dgate);
+            } else {
+                const float z = (to_f(x.v[i]) - mu[i]) * rstd[i] * w[i] + b[i];
+                y.v[i] = from_f<T>(a.gate ? z * act(to_f(gt.v[i]), a.silu).f : act(z, a.silu).f);
+            }
+        }
+        T *to = static_cast<T *>(BWD ? a.dx : a.y);
+        if (to) *reinterpret_cast<Vec<T, VE> *>(to + row * a.C + p.c) = y;
+        if (BWD && a.dgate) *reinterpret_cast<Vec<T, VE> *>(static_cast<T *>(a.dgate) + row * a.C + p.c) = dg;
+    }
+}
+
+// dweight and dbias: sums of `rows` rows of 2 C partial sums, in a fixed
+// order; 32 columns to a block, 16 threads to a column.
+__global__ __launch_bounds__(GT) void k_gn_wsum(GnArgs a, int64_t rows)
+{
+    __shared__ float red[GT];
+    const int64_t e = (int64_t)blockIdx.x * 32 + (threadIdx.x & 31);
     float s = 0.f;
-    for (int64_t p = 0; p < a.nparts; ++p) s += a.part[2 * p * a.C + e];
-    float *to = e < a.C ? a.dw : a.db;
-    if (to) to[e < a.C ? e : e - a.C] = s;
+    if (e < 2 * (int64_t)a.C) {
+#pragma unroll 8
+        for (int64_t p = threadIdx.x >> 5; p < rows; p += GT / 32) s += a.part[2 * p * a.C + e];
+    }
+    red[threadIdx.x] = s;
+    __syncthreads();
+    if (threadIdx.x < 32 && e < 2 * (int64_t)a.C) {
+        for (int k = 1; k < GT / 32; ++k) s += red[threadIdx.x + 32 * k];
+        float *to = e < a.C ? a.dw : a.db;
+        if (to) to[e < a.C ? e : e - a.C] = s;
+    }
 }
 
 // Statistics of samples without rows.
@@ -175,10 +524,98 @@ __global__ void k_gn_zero(float *p, int64_t n)
     if (i < n) p[i] = 0.f;
 }
 
-static int64_t wparts(const gn_shape &s)
+// ---- host side
+
+struct GnPlan {
+    bool held = false;
+    int ve = 1, k = 1;
+    int64_t blocks = 0;
+    size_t mean = 0, total = 0;   // workspace: partial sums, then the runs' means
+};
+
+// Elements that every row of every tensor allows to be moved at once.
+static int widest(const GnArgs &a, int dtype, int64_t run)
 {
-    const int64_t rows = s.N * s.L;
-    return rows < 1 ? 0 : (rows + 63) / 64 > 64 ? 64 : (rows + 63) / 64;
+    const int64_t e = dtype_size(dtype);
+    for (int ve = 16 / (int)e; ve > 1; ve /= 2) {
+        if (e == 2 && ve == 4) continue;   // 16 bytes, 4 bytes or one at a time
+        if (e == 4 && ve == 2) continue;
+        bool fits = run % ve == 0 && a.C % ve == 0;
+        for (const void *p : {a.x, a.gate, a.dy, (const void *)a.y, (const void *)a.dx, (const void *)a.dgate})
+            fits = fits && !misaligned(p, (unsigned)(ve * e));
+        fits = fits && a.ldx % ve == 0 && (!a.gate || a.ldg % ve == 0) && (!a.dy || a.ldy % ve == 0);
+        if (fits) return ve;
+    }
+    return 1;
+}
+
+// Chooses the kernels and fills in the arguments that go with them.  The
+// workspace does not depend on the pointers' alignment: sizes come from `ve`
+// as given, and every `ve` of a shape needs no more than one at a time does.
+static GnPlan plan_gn(GnArgs &a, bool bwd, int ve_run, int ve_row, int cus)
+{
+    GnPlan P;
+    const int64_t M = (int64_t)a.L * a.cg, pieces = M / ve_run;
+    P.held = pieces <= (int64_t)GT * HELD;
+    if (P.held) {
+        // Two pieces to a thread: fewer threads take part in a run's sums, and
+        // two loads of a tensor are in flight.
+        a.pieces = (int)pieces;
+        a.ppr = a.cg / ve_run;
+        int lw = 0;
+        while (lw < 6 && (int64_t(2) << lw) < pieces) ++lw;
+        if ((int64_t(HELD) << lw) < pieces) lw = 9;
+        const int64_t k = (pieces + (1 << lw) - 1) >> lw;
+        P.k = k <= 1 ? 1 : k <= 2 ? 2 : 4;
+        a.lw = lw;
+        const int slots = GT >> lw;
+        a.gs = a.groups < slots ? a.groups : slots;
+        a.rpb = slots / a.gs;
+        a.sets = (a.groups + a.gs - 1) / a.gs;
+        // The backward's blocks each leave a row of partial sums: 2 for each
+        // CU.  The forward's go on to the next samples only to bound the grid.
+        int64_t rows = (a.N + a.rpb - 1) / a.rpb;
+        const int64_t most = bwd ? (2 * int64_t(cus) + a.sets - 1) / a.sets : (int64_t(1) << 20) / a.sets + 1;
+        if (rows > most) rows = most;
+        P.blocks = rows * a.sets;
+        a.nparts = rows;
+        P.ve = ve_run;
+        P.total = bwd ? (size_t)rows * 2 * a.C * sizeof(float) : 0;
+        return P;
+    }
+    P.ve = ve_row;
+    const int64_t tiles = (a.C / P.ve + GT - 1) / GT;
+    // About four blocks for each CU, of 16 rows or more at a time
+    int64_t parts = (4 * int64_t(cus) + a.N * tiles - 1) / (a.N * tiles);
+    const int64_t most = (a.L + 15) / 16;
+    if (parts > most) parts = most;
+    if (parts < 1) parts = 1;
+    a.per = (a.L + parts - 1) / parts;
+    a.nparts = (a.L + a.per - 1) / a.per;
+    P.blocks = a.N * a.nparts * tiles;
+    P.mean = (size_t)(a.N * a.nparts) * 2 * a.C * sizeof(float);
+    P.total = P.mean + (bwd ? (size_t)(a.N * a.groups) * 2 * sizeof(float) : 0);
+    return P;
+}
+
+// The workspace for any alignment.
+static size_t gn_workspace(const gn_shape &s, bool bwd)
+{
+    if (s.N == 0 || s.L == 0) return 0;
+    size_t most = 0;
+    for (int run : {8, 4, 2, 1})
+        for (int row : {8, 4, 2, 1}) {
+            if ((s.C / s.groups) % run != 0 || s.C % row != 0) continue;
+            GnArgs a{};
+            a.N = s.N;
+            a.L = (int)s.L;
+            a.C = (int)s.C;
+            a.groups = (int)s.groups;
+            a.cg = (int)(s.C / s.groups);
+            const GnPlan P = plan_gn(a, bwd, run, row, ssd::device_cus());
+            if (P.total > most) most = P.total;
+        }
+    return most;
 }
 
 static int gn_args(const gn_shape &s, int64_t ldx, int64_t ldg, int64_t ldy, GnArgs *a)
@@ -193,8 +630,48 @@ static int gn_args(const gn_shape &s, int64_t ldx, int64_t ldg, int64_t ldy, GnA
     a->ldx = ldx ? ldx : s.C;
     a->ldg = ldg ? ldg : s.C;
     a->ldy = ldy ? ldy : s.C;
-    if (s.N > ((int64_t(1) << 31) - 1) / s.groups) return SSD_ERR_SHAPE;
     return SSD_OK;
+}
+
+// Runs BODY with constants VE and K for the plan's.
+#define GN_DISPATCH(P, ...)                                                              \
+    do {                                                                                  \
+        constexpr int FULL = 16 / (int)sizeof(T), PART = sizeof(T) == 2 ? 2 : 1;           \
+        if ((P).ve == FULL) { constexpr int VE = FULL; __VA_ARGS__; }                             \
+        else if ((P).ve == PART) { constexpr int VE = PART; __VA_ARGS__; }                        \
+        else { constexpr int VE = 1; __VA_ARGS__; }                                               \
+    } while (0)
+#define GN_DISPATCH_K(P, ...)                       \
+    do {                                             \
+        if ((P).k == 1) { constexpr int K = 1; __VA_ARGS__; } \
+        else if ((P).k == 2) { constexpr int K = 2; __VA_ARGS__; } \
+        else { constexpr int K = 4; __VA_ARGS__; }          \
+    } while (0)
+
+template <typename T>
+static void run_gn(const GnArgs &a, const GnPlan &P, bool bwd, hipStream_t st)
+{
+    const dim3 grid((unsigned)P.blocks), runs((unsigned)(a.N * a.groups)), blk(GT);
+    GN_DISPATCH(P, {
+        if (P.held) {
+            GN_DISPATCH_K(P, {
+                if (bwd)
+                    k_gn_bwd_held<T, VE, K><<<grid, blk, 0, st>>>(a);
+                else
+                    k_gn_fwd_held<T, VE, K><<<grid, blk, 0, st>>>(a);
+            });
+        } else if (bwd) {
+            k_gn_sums<T, VE, true><<<grid, blk, 0, st>>>(a);
+            if (a.dx || a.dgate) {
+                k_gn_mid<true><<<runs, blk, 0, st>>>(a);
+                k_gn_apply<T, VE, true><<<grid, blk, 0, st>>>(a);
+            }
+        } else {
+            k_gn_sums<T, VE, false><<<grid, blk, 0, st>>>(a);
+            k_gn_mid<false><<<runs, blk, 0, st>>>(a);
+            k_gn_apply<T, VE, false><<<grid, blk, 0, st>>>(a);
+        }
+    });
 }
 
 }  // namespace layer
@@ -203,8 +680,12 @@ using namespace layer;
 
 extern "C" size_t gn_fwd_workspace_size(const gn_shape *shape)
 {
-    if (check_gn(shape, GN_ACT_NONE) != SSD_OK) return (size_t)-1;
-    return 0;
+    return check_gn(shape, GN_ACT_NONE) != SSD_OK ? (size_t)-1 : gn_workspace(*shape, false);
+}
+
+extern "C" size_t gn_bwd_workspace_size(const gn_shape *shape)
+{
+    return check_gn(shape, GN_ACT_NONE) != SSD_OK ? (size_t)-1 : gn_workspace(*shape, true);
 }
 
 extern "C" int gn_fwd(const gn_shape *shape, int dtype, int act, float eps, const void *x, int64_t ld_x,
@@ -225,8 +706,10 @@ extern "C" int gn_fwd(const gn_shape *shape, int dtype, int act, float eps, cons
     if (misaligned(x, e) || misaligned(gate, e) || misaligned(y, e) || misaligned(weight, 4) || misaligned(bias, 4) ||
         misaligned(stats, 4))
         return SSD_ERR_ALIGN;
-    (void)workspace;
-    (void)workspace_bytes;
+    const size_t need = gn_workspace(s, false);
+    if (workspace_bytes < need) return SSD_ERR_WORKSPACE;
+    if (need > 0 && !workspace) return SSD_ERR_NULL;
+    if (need > 0 && misaligned(workspace, 16)) return SSD_ERR_ALIGN;
     hipStream_t st = static_cast<hipStream_t>(stream);
     if (s.L == 0) {
         const int64_t n = 2 * s.N * s.groups;
@@ -240,15 +723,11 @@ extern "C" int gn_fwd(const gn_shape *shape, int dtype, int act, float eps, cons
     a.y = y;
     a.stats = stats;
     a.eps = eps;
-    const bool silu = act == GN_ACT_SILU;
-    LAYER_DISPATCH(dtype, (k_gn_fwd<T><<<dim3((unsigned)(s.N * s.groups)), dim3(GT), 0, st>>>(a, silu)));
+    a.silu = act == GN_ACT_SILU;
+    a.part = static_cast<float *>(workspace);
+    const GnPlan P = plan_gn(a, false, widest(a, dtype, a.cg), widest(a, dtype, a.C), ssd::device_cus());
+    LAYER_DISPATCH(dtype, run_gn<T>(a, P, false, st));
     return launch_status();
-}
-
-extern "C" size_t gn_bwd_workspace_size(const gn_shape *shape)
-{
-    if (check_gn(shape, GN_ACT_NONE) != SSD_OK) return (size_t)-1;
-    return (size_t)wparts(*shape) * 2 * (size_t)shape->C * sizeof(float);
 }
 
 extern "C" int gn_bwd(const gn_shape *shape, int dtype, int act, const void *x, int64_t ld_x, const float *weight,
@@ -271,8 +750,7 @@ extern "C" int gn_bwd(const gn_shape *shape, int dtype, int act, const void *x, 
         misaligned(weight, 4) || misaligned(bias, 4) || misaligned(stats, 4) || misaligned(dweight, 4) ||
         misaligned(dbias, 4))
         return SSD_ERR_ALIGN;
-    const bool wanted = dweight || dbias;
-    const size_t need = wanted ? gn_bwd_workspace_size(shape) : 0;
+    const size_t need = gn_workspace(s, true);
     if (workspace_bytes < need) return SSD_ERR_WORKSPACE;
     if (need > 0 && !workspace) return SSD_ERR_NULL;
     if (need > 0 && misaligned(workspace, 16)) return SSD_ERR_ALIGN;
@@ -287,16 +765,17 @@ extern "C" int gn_bwd(const gn_shape *shape, int dtype, int act, const void *x, 
     a.dgate = dgate;
     a.dw = dweight;
     a.db = dbias;
+    a.silu = act == GN_ACT_SILU;
+    const bool wanted = dweight || dbias;
+    int64_t rows = 0;
     a.part = static_cast<float *>(workspace);
-    a.nparts = work ? wparts(s) : 0;
-    const bool silu = act == GN_ACT_SILU;
-    if (work && (dx || dgate))
-        LAYER_DISPATCH(dtype, (k_gn_bwd<T><<<dim3((unsigned)(s.N * s.groups)), dim3(GT), 0, st>>>(a, silu)));
-    if (wanted) {
-        if (work)
-            LAYER_DISPATCH(dtype, (k_gn_wpart<T><<<dim3((unsigned)((s.C + 63) / 64), (unsigned)a.nparts), dim3(GT), 0,
-                                                  st>>>(a, silu)));
-        k_gn_wsum<<<dim3((unsigned)((2 * s.C + GT - 1) / GT)), dim3(GT), 0, st>>>(a);
+    if (work) {
+        const GnPlan P = plan_gn(a, true, widest(a, dtype, a.cg), widest(a, dtype, a.C), ssd::device_cus());
+        a.mean = reinterpret_cast<float *>(static_cast<char *>(workspace) + P.mean);
+        rows = P.held ? a.nparts : a.N * a.nparts;
+        if (P.held && !wanted) a.part = nullptr;
+        if (wanted || dx || dgate) LAYER_DISPATCH(dtype, run_gn<T>(a, P, true, st));
     }
+    if (wanted) k_gn_wsum<<<dim3((unsigned)((2 * s.C + 31) / 32)), dim3(GT), 0, st>>>(a, rows);
     return launch_status();
 }

@@ -51,6 +51,7 @@ int check_gn(const gn_shape *s, int act)
     const int64_t lim = int64_t(1) << 40;
     if (s->C >= kMaxCount || s->L >= (int64_t(1) << 31) || s->N > lim) return SSD_ERR_SHAPE;
     if (s->N > lim / (s->L + 1) || s->N * (s->L + 1) > lim / s->C) return SSD_ERR_SHAPE;
+    if (s->N > ((int64_t(1) << 30) - 1) / s->groups) return SSD_ERR_SHAPE;   // a block for each run
     return SSD_OK;
 }
 

@@ -443,7 +443,7 @@ int lin_step(const lin_shape *shape, int dtype, const lin_strides *strides,
  * (1 and 0).  stats [N][groups][2] receives mu and rstd.
  * Row n L + l of x, gate, dy starts ld_* elements after the row before it
  * (0: C); y, dx and dgate are dense.  C % groups == 0; N L C < 2^40, C and
- * the strides below 2^24, L < 2^31. */
+ * the strides below 2^24, L < 2^31, N groups < 2^30. */
 typedef struct gn_shape {
     int64_t N, L, C, groups;
 } gn_shape;
