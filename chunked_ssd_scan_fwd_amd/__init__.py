@@ -333,6 +333,9 @@ class KernelTimer:
         return False
 
 
+layer._library = library
+
+
 # ---- selective (Mamba-style) scan
 
 

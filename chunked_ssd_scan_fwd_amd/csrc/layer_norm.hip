@@ -62,6 +62,21 @@ __device__ __forceinline__ Vec<T, VE> load(const T *p, bool on)
     if (on) r = *reinterpret_cast<const Vec<T, VE> *>(p);
     return r;
 }
+// The same for what is read once by the whole call: a non-temporal load.
+// The forward on 16384 rows of 2048 took 40 us with it and 51 without; the
+// backward, whose second tensor pair crowds the caches anyway, 25 both ways.
+template <typename T, int VE>
+__device__ __forceinline__ Vec<T, VE> load_once(const T *p, bool on)
+{
+    typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+    if constexpr (sizeof(Vec<T, VE>) == 16) {
+        u32x4 r = {};
+        if (on) r = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p));
+        return __builtin_bit_cast(Vec<T, VE>, r);
+    } else {
+        return load<T, VE>(p, on);
+    }
+}
 // weight or bias of VE channels
 template <int VE>
 __device__ __forceinline__ void channels(float (&to)[VE], const float *p, float none, bool on)
@@ -126,13 +141,19 @@ __global__ __launch_bounds__(GT) void k_gn_fwd_held(GnArgs a)
     const int64_t step = (int64_t)(gridDim.x / a.sets) * a.rpb;
     const float inv = 1.f / ((float)a.L * (float)a.cg);
     const bool first = (threadIdx.x & ((1 << a.lw) - 1)) == 0;
+    float w[K][VE], b[K][VE];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        channels<VE>(w[k], a.w ? a.w + h.c[k] : nullptr, 1.f, h.on[k]);
+        channels<VE>(b[k], a.b ? a.b + h.c[k] : nullptr, 0.f, h.on[k]);
+    }
     for (int64_t n = h.first; n < a.N; n += step) {
         Vec<T, VE> x[K], gt[K];
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const int64_t row = n * a.L + h.l[k];
-            x[k] = load<T, VE>(static_cast<const T *>(a.x) + row * a.ldx + h.c[k], h.on[k]);
-            if (a.gate) gt[k] = load<T, VE>(static_cast<const T *>(a.gate) + row * a.ldg + h.c[k], h.on[k]);
+            x[k] = load_once<T, VE>(static_cast<const T *>(a.x) + row * a.ldx + h.c[k], h.on[k]);
+            if (a.gate) gt[k] = load_once<T, VE>(static_cast<const T *>(a.gate) + row * a.ldg + h.c[k], h.on[k]);
         }
         float s = 0.f, none = 0.f;
 #pragma unroll
@@ -159,13 +180,10 @@ __global__ __launch_bounds__(GT) void k_gn_fwd_held(GnArgs a)
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             if (!h.on[k]) continue;
-            float w[VE], b[VE];
-            channels<VE>(w, a.w ? a.w + h.c[k] : nullptr, 1.f, true);
-            channels<VE>(b, a.b ? a.b + h.c[k] : nullptr, 0.f, true);
             Vec<T, VE> y;
 #pragma unroll
             for (int i = 0; i < VE; ++i) {
-                const float z = (to_f(x[k].v[i]) - mu) * rstd * w[i] + b[i];
+                const float z = (to_f(x[k].v[i]) - mu) * rstd * w[k][i] + b[k][i];
                 y.v[i] = from_f<T>(a.gate ? z * act(to_f(gt[k].v[i]), a.silu).f : act(z, a.silu).f);
             }
             *reinterpret_cast<Vec<T, VE> *>(static_cast<T *>(a.y) + (n * a.L + h.l[k]) * a.C + h.c[k]) = y;
@@ -241,38 +259,49 @@ __global__ __launch_bounds__(GT) void k_gn_bwd_held(GnArgs a)
         channels<VE>(w[k], a.w ? a.w + h.c[k] : nullptr, 1.f, h.on[k]);
         channels<VE>(b[k], a.b ? a.b + h.c[k] : nullptr, 0.f, h.on[k]);
     }
-    if (h.run >= 0)
-        for (int64_t n = h.first; n < a.N; n += step) {
+    if (h.run >= 0 && h.first < a.N) {
+        // what one sample's run takes, fetched while the one before is worked on
+        struct Row {
             Vec<T, VE> x[K], gt[K], dy[K];
+            float mu, rstd;
+        } r, ahead;
+        const auto fetch = [&](Row &to, int64_t n) {
 #pragma unroll
             for (int k = 0; k < K; ++k) {
                 const int64_t row = n * a.L + h.l[k];
-                x[k] = load<T, VE>(static_cast<const T *>(a.x) + row * a.ldx + h.c[k], h.on[k]);
-                dy[k] = load<T, VE>(static_cast<const T *>(a.dy) + row * a.ldy + h.c[k], h.on[k]);
-                if (a.gate) gt[k] = load<T, VE>(static_cast<const T *>(a.gate) + row * a.ldg + h.c[k], h.on[k]);
+                to.x[k] = load<T, VE>(static_cast<const T *>(a.x) + row * a.ldx + h.c[k], h.on[k]);
+                to.dy[k] = load<T, VE>(static_cast<const T *>(a.dy) + row * a.ldy + h.c[k], h.on[k]);
+                if (a.gate) to.gt[k] = load<T, VE>(static_cast<const T *>(a.gate) + row * a.ldg + h.c[k], h.on[k]);
             }
             const float *st = a.stats + 2 * (n * a.groups + h.run);
-            const float mu = st[0], rstd = st[1];
+            to.mu = st[0];
+            to.rstd = st[1];
+        };
+        fetch(r, h.first);
+        for (int64_t n = h.first; n < a.N; n += step) {
+            fetch(ahead, n + step < a.N ? n + step : n);
+            const float mu = r.mu, rstd = r.rstd;
             float xh[K][VE], d[K][VE], s1 = 0.f, s2 = 0.f;
 #pragma unroll
             for (int k = 0; k < K; ++k) {
                 Vec<T, VE> dg;
 #pragma unroll
                 for (int i = 0; i < VE; ++i) {
-                    const GnGrad r = gn_grad(to_f(x[k].v[i]), mu, rstd, w[k][i], b[k][i], a.gate != nullptr,
-                                             a.gate ? to_f(gt[k].v[i]) : 0.f, to_f(dy[k].v[i]), a.silu);
-                    const float dz = h.on[k] ? r.dz : 0.f;
-                    xh[k][i] = h.on[k] ? r.xh : 0.f;
+                    const GnGrad t = gn_grad(to_f(r.x[k].v[i]), mu, rstd, w[k][i], b[k][i], a.gate != nullptr,
+                                             a.gate ? to_f(r.gt[k].v[i]) : 0.f, to_f(r.dy[k].v[i]), a.silu);
+                    const float dz = h.on[k] ? t.dz : 0.f;
+                    xh[k][i] = h.on[k] ? t.xh : 0.f;
                     d[k][i] = dz * w[k][i];
                     s1 += d[k][i];
                     s2 += d[k][i] * xh[k][i];
                     aw[k][i] += dz * xh[k][i];
                     ab[k][i] += dz;
-                    dg.v[i] = from_f<T>(r.dgate);
+                    dg.v[i] = from_f<T>(t.dgate);
                 }
                 if (a.dgate && h.on[k])
                     *reinterpret_cast<Vec<T, VE> *>(static_cast<T *>(a.dgate) + (n * a.L + h.l[k]) * a.C + h.c[k]) = dg;
             }
+            r = ahead;
             if (!a.dx) continue;
             run_sum(s1, s2, a.lw, red);
             const float m1 = s1 * inv, m2 = s2 * inv;
@@ -285,6 +314,7 @@ __global__ __launch_bounds__(GT) void k_gn_bwd_held(GnArgs a)
                 *reinterpret_cast<Vec<T, VE> *>(static_cast<T *>(a.dx) + (n * a.L + h.l[k]) * a.C + h.c[k]) = dx;
             }
         }
+    }
     if (!a.part) return;
     float *part = a.part + 2 * (int64_t)(blockIdx.x / a.sets) * a.C;
     held_part<VE, K>(a, aw, held, sub, part);
@@ -322,7 +352,7 @@ struct Cut {
 template <typename T, int VE, bool BWD>
 __global__ __launch_bounds__(GT) void k_gn_sums(GnArgs a)
 {
-    __shared__ float red[2][GT * VE], cnt[GT];
+    __shared__ float red[2][VE][GT], cnt[GT];
     const Cut<VE> p(a);
     float s[2][VE] = {}, x0[VE] = {}, w[VE], b[VE], mu[VE], rstd[VE];
     int rows = 0;
@@ -336,6 +366,12 @@ __global__ __launch_bounds__(GT) void k_gn_sums(GnArgs a)
                 mu[i] = st[0];
                 rstd[i] = st[1];
             }
+        }
+        if (!BWD && p.l0 + p.r0 < p.l1) {
+            const Vec<T, VE> x =
+                load<T, VE>(static_cast<const T *>(a.x) + (p.n * a.L + p.l0 + p.r0) * a.ldx + p.c, true);
+#pragma unroll
+            for (int i = 0; i < VE; ++i) x0[i] = to_f(x.v[i]);
         }
 #pragma unroll 4
         for (int l = p.l0 + p.r0; l < p.l1; l += p.rp) {
@@ -354,7 +390,6 @@ __global__ __launch_bounds__(GT) void k_gn_sums(GnArgs a)
                     s[0][i] += r.dz * r.xh;
                     s[1][i] += r.dz;
                 } else {
-                    if (rows == 0) x0[i] = to_f(x.v[i]);
                     const float d = to_f(x.v[i]) - x0[i];
                     s[0][i] += d;
                     s[1][i] += d * d;
@@ -363,46 +398,53 @@ __global__ __launch_bounds__(GT) void k_gn_sums(GnArgs a)
             ++rows;
         }
     }
+    if (!BWD && rows > 0)
 #pragma unroll
-    for (int i = 0; i < VE; ++i) {
-        if (!BWD && rows > 0) {
+        for (int i = 0; i < VE; ++i) {
             const float m = s[0][i] / (float)rows;
             s[1][i] = fmaxf(s[1][i] - m * s[0][i], 0.f) + 0.f * s[1][i];   // and a NaN stays one
             s[0][i] = x0[i] + m;
         }
-        red[0][threadIdx.x * VE + i] = s[0][i];
-        red[1][threadIdx.x * VE + i] = s[1][i];
+    // join the threads of a column of rows, pairs in a fixed order
+    const int cp = min(a.C / VE, GT);
+    float count = (float)rows;
+    int half = 1;
+    while (half < p.rp) half *= 2;
+    for (half /= 2; half > 0; half /= 2) {
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < VE; ++i) {
+            red[0][i][threadIdx.x] = s[0][i];
+            red[1][i][threadIdx.x] = s[1][i];
+        }
+        cnt[threadIdx.x] = count;
+        __syncthreads();
+        const int other = threadIdx.x + half * cp;
+        if (p.r0 < half && p.r0 + half < p.rp) {
+            const float k = cnt[other];
+            if (BWD || k > 0.f) {
+#pragma unroll
+                for (int i = 0; i < VE; ++i) {
+                    const float u = red[0][i][other], v = red[1][i][other];
+                    if (BWD) {
+                        s[0][i] += u;
+                        s[1][i] += v;
+                    } else {   // rows go to the lower threads first, so this one has some
+                        const float d = u - s[0][i], f = k / (count + k);
+                        s[0][i] += d * f;
+                        s[1][i] += v + d * d * count * f;
+                    }
+                }
+                count += k;
+            }
+        }
     }
-    cnt[threadIdx.x] = (float)rows;
-    __syncthreads();
     if (p.on && p.r0 == 0) {
-        const int cp = min(a.C / VE, GT);
         float *to = a.part + (p.n * a.nparts + p.part) * 2 * a.C + p.c;
 #pragma unroll
         for (int i = 0; i < VE; ++i) {
-            float u = 0.f, v = 0.f;
-            if (BWD) {
-                for (int r = 0; r < p.rp; ++r) {
-                    u += red[0][(threadIdx.x + r * cp) * VE + i];
-                    v += red[1][(threadIdx.x + r * cp) * VE + i];
-                }
-            } else {
-                const float base = red[0][threadIdx.x * VE + i];   // the part has a row, and this thread the first
-                float n = 0.f;
-                for (int r = 0; r < p.rp; ++r) {
-                    const float k = cnt[threadIdx.x + r * cp];
-                    if (k > 0.f) u += k * (red[0][(threadIdx.x + r * cp) * VE + i] - base);
-                    n += k;
-                }
-                u = base + u / n;
-                for (int r = 0; r < p.rp; ++r) {
-                    const float k = cnt[threadIdx.x + r * cp];
-                    const float d = red[0][(threadIdx.x + r * cp) * VE + i] - u;
-                    if (k > 0.f) v += red[1][(threadIdx.x + r * cp) * VE + i] + k * d * d;
-                }
-            }
-            to[i] = u;
-            to[a.C + i] = v;
+            to[i] = s[0][i];
+            to[a.C + i] = s[1][i];
         }
     }
 }
@@ -552,18 +594,25 @@ static int widest(const GnArgs &a, int dtype, int64_t run)
 // Chooses the kernels and fills in the arguments that go with them.  The
 // workspace does not depend on the pointers' alignment: sizes come from `ve`
 // as given, and every `ve` of a shape needs no more than one at a time does.
-static GnPlan plan_gn(GnArgs &a, bool bwd, int ve_run, int ve_row, int cus)
+static GnPlan plan_gn(GnArgs &a, bool bwd, int ve_run, int ve_row, int64_t esize, int cus)
 {
     GnPlan P;
     const int64_t M = (int64_t)a.L * a.cg, pieces = M / ve_run;
-    P.held = pieces <= (int64_t)GT * HELD;
+    // A wave holds runs of up to 64 HELD pieces (1000 x 32 x 320 in 32 groups
+    // took 26 us so, and 101 cut), beside its neighbours, so that they share
+    // the lines they fetch.  One that takes a whole block is held only where
+    // its rows fill lines: blocks of neighbouring runs sit on different dies,
+    // and each would fetch the others' part of a line (64 x 1024 x 512 in 32
+    // groups took 106 us so, and 51 cut).
+    P.held = pieces <= 64 * HELD || (pieces <= (int64_t)GT * HELD && (a.L == 1 || a.cg * esize >= 256));
     if (P.held) {
-        // Two pieces to a thread: fewer threads take part in a run's sums, and
-        // two loads of a tensor are in flight.
+        // One piece to a thread while a wave's lanes suffice: the backward of
+        // 5001 x 1536 took 25 us so, and 37 with two (more registers, fewer
+        // waves); the forward took the same.
         a.pieces = (int)pieces;
         a.ppr = a.cg / ve_run;
         int lw = 0;
-        while (lw < 6 && (int64_t(2) << lw) < pieces) ++lw;
+        while (lw < 6 && (int64_t(1) << lw) < pieces) ++lw;
         if ((int64_t(HELD) << lw) < pieces) lw = 9;
         const int64_t k = (pieces + (1 << lw) - 1) >> lw;
         P.k = k <= 1 ? 1 : k <= 2 ? 2 : 4;
@@ -572,10 +621,11 @@ static GnPlan plan_gn(GnArgs &a, bool bwd, int ve_run, int ve_row, int cus)
         a.gs = a.groups < slots ? a.groups : slots;
         a.rpb = slots / a.gs;
         a.sets = (a.groups + a.gs - 1) / a.gs;
-        // The backward's blocks each leave a row of partial sums: 2 for each
-        // CU.  The forward's go on to the next samples only to bound the grid.
+        // Blocks go on from sample to sample with their weights, and the
+        // backward's with their sums, of which each leaves a row: 8 and 2 for
+        // each CU (the backward took 25 us so, 32 with 4 and 27 with 1).
         int64_t rows = (a.N + a.rpb - 1) / a.rpb;
-        const int64_t most = bwd ? (2 * int64_t(cus) + a.sets - 1) / a.sets : (int64_t(1) << 20) / a.sets + 1;
+        const int64_t most = ((bwd ? 2 : 8) * int64_t(cus) + a.sets - 1) / a.sets;
         if (rows > most) rows = most;
         P.blocks = rows * a.sets;
         a.nparts = rows;
@@ -585,8 +635,7 @@ static GnPlan plan_gn(GnArgs &a, bool bwd, int ve_run, int ve_row, int cus)
     }
     P.ve = ve_row;
     const int64_t tiles = (a.C / P.ve + GT - 1) / GT;
-    // About four blocks for each CU, of 16 rows or more at a time
-    int64_t parts = (4 * int64_t(cus) + a.N * tiles - 1) / (a.N * tiles);
+    int64_t parts = (2 * int64_t(cus) + a.N * tiles - 1) / (a.N * tiles);
     const int64_t most = (a.L + 15) / 16;
     if (parts > most) parts = most;
     if (parts < 1) parts = 1;
@@ -598,8 +647,8 @@ static GnPlan plan_gn(GnArgs &a, bool bwd, int ve_run, int ve_row, int cus)
     return P;
 }
 
-// The workspace for any alignment.
-static size_t gn_workspace(const gn_shape &s, bool bwd)
+// The workspace for any alignment and type.
+static size_t gn_workspace_of(const gn_shape &s, bool bwd, int cus)
 {
     if (s.N == 0 || s.L == 0) return 0;
     size_t most = 0;
@@ -612,10 +661,31 @@ static size_t gn_workspace(const gn_shape &s, bool bwd)
             a.C = (int)s.C;
             a.groups = (int)s.groups;
             a.cg = (int)(s.C / s.groups);
-            const GnPlan P = plan_gn(a, bwd, run, row, ssd::device_cus());
-            if (P.total > most) most = P.total;
+            for (int64_t e : {2, 4}) {
+                const GnPlan P = plan_gn(a, bwd, run, row, e, cus);
+                if (P.total > most) most = P.total;
+            }
         }
     return most;
+}
+
+// Working that out takes microseconds, so a thread remembers its last shapes.
+static size_t gn_workspace(const gn_shape &s, bool bwd)
+{
+    struct Known {
+        gn_shape s{-1, 0, 0, 0};
+        int cus = 0;
+        size_t bytes = 0;
+    };
+    static thread_local Known known[2][8];
+    const int cus = ssd::device_cus();
+    Known &k = known[bwd][(s.N ^ s.L ^ s.C >> 3 ^ s.groups) & 7];
+    if (k.s.N != s.N || k.s.L != s.L || k.s.C != s.C || k.s.groups != s.groups || k.cus != cus) {
+        k.s = s;
+        k.cus = cus;
+        k.bytes = gn_workspace_of(s, bwd, cus);
+    }
+    return k.bytes;
 }
 
 static int gn_args(const gn_shape &s, int64_t ldx, int64_t ldg, int64_t ldy, GnArgs *a)
@@ -725,7 +795,7 @@ extern "C" int gn_fwd(const gn_shape *shape, int dtype, int act, float eps, cons
     a.eps = eps;
     a.silu = act == GN_ACT_SILU;
     a.part = static_cast<float *>(workspace);
-    const GnPlan P = plan_gn(a, false, widest(a, dtype, a.cg), widest(a, dtype, a.C), ssd::device_cus());
+    const GnPlan P = plan_gn(a, false, widest(a, dtype, a.cg), widest(a, dtype, a.C), dtype_size(dtype), ssd::device_cus());
     LAYER_DISPATCH(dtype, run_gn<T>(a, P, false, st));
     return launch_status();
 }
@@ -770,7 +840,7 @@ extern "C" int gn_bwd(const gn_shape *shape, int dtype, int act, const void *x, 
     int64_t rows = 0;
     a.part = static_cast<float *>(workspace);
     if (work) {
-        const GnPlan P = plan_gn(a, true, widest(a, dtype, a.cg), widest(a, dtype, a.C), ssd::device_cus());
+        const GnPlan P = plan_gn(a, true, widest(a, dtype, a.cg), widest(a, dtype, a.C), dtype_size(dtype), ssd::device_cus());
         a.mean = reinterpret_cast<float *>(static_cast<char *>(workspace) + P.mean);
         rows = P.held ? a.nparts : a.N * a.nparts;
         if (P.held && !wanted) a.part = nullptr;

@@ -21,6 +21,8 @@ __all__ = ["lin_prefill", "lin_step", "gn_fwd", "gn_bwd", "state_pack", "state_u
 STATE_CACHE_BLOCK = 32   # values of a state's row that share a scale byte
 _i64, _vp, _sz, _int = ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int
 _torch = None
+_library = None   # the package's library()
+_stream_of = _current = None
 _dtypes = {}
 _ACTS = {None: 0, "none": 0, "silu": 1}
 
@@ -61,17 +63,35 @@ def declare(lib):
 
 
 def _init():
-    global _torch
+    global _torch, _stream_of, _current
     import torch
     _dtypes.update({torch.float32: 0, torch.bfloat16: 1, torch.float16: 2})
+    # a call's own time counts where the work takes microseconds: the raw
+    # stream and device, without the objects around them
+    _stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda i: torch.cuda.current_stream(i).cuda_stream)
+    _current = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
     _torch = torch
 
 
 def _lib():
-    from . import library
     if _torch is None:
         _init()
-    return library()
+    return _library()
+
+
+_args = {}
+
+
+def _arg(cls, *fields):
+    """A reference to a struct of these fields; those of recent calls are kept."""
+    key = (cls, fields)
+    r = _args.get(key)
+    if r is None:
+        if len(_args) >= 1024:
+            _args.clear()
+        r = _args[key] = ctypes.byref(cls(*fields))
+    return r
 
 
 def _dtype_of(t, name):
@@ -86,15 +106,15 @@ def _dtype_of(t, name):
 
 
 def _is(t, name, shape, dtype, device):
-    """`t` is a tensor of this shape (a tuple), type and device."""
+    """`t` is a tensor of this shape (a tuple) and type, on HIP device `device` (its number)."""
     if not isinstance(t, _torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on HIP device {device}, got {t.device}")
 
 
 def _dense(t, name, shape, dtype, device):
@@ -118,13 +138,12 @@ def _ids(t, name, n, device):
 
 
 def _call(fn, where, device, *args):
-    """fn(*args, stream) with `device` current, on its current stream."""
-    cuda = _torch.cuda
-    if device.index != cuda.current_device():
-        with cuda.device(device):
-            rc = fn(*args, cuda.current_stream(device).cuda_stream)
+    """fn(*args, stream) with device number `device` current, on its current stream."""
+    if device != _current():
+        with _torch.cuda.device(device):
+            rc = fn(*args, _stream_of(device))
     else:
-        rc = fn(*args, cuda.current_stream(device).cuda_stream)
+        rc = fn(*args, _stream_of(device))
     if rc != 0:
         from . import SsdError
         raise SsdError(rc, where)
@@ -136,38 +155,42 @@ def _bytes(need, device, workspace):
         if need == 0:
             return None, 0, None
         workspace = _torch.empty(need, dtype=_torch.uint8, device=device)
-    else:
-        from . import _workspace_bytes
-        workspace, _ = _workspace_bytes(need, device, workspace)
+        return workspace.data_ptr(), need, workspace
+    from . import _workspace_bytes
+    workspace, _ = _workspace_bytes(need, _torch.device("cuda", device), workspace)
     return workspace.data_ptr() or None, workspace.numel() * workspace.element_size(), workspace
 
 
 def _lin_args(q, k, v, log_decay, states, out, rows_name):
     code = _dtype_of(q, "q")
-    dev, dt = q.device, q.dtype
-    if q.dim() != 3 or v.dim() != 3 or states.dim() != 4:
-        raise ValueError(f"q must be [{rows_name},G,dk], v [{rows_name},H,dv] and states [slots,H,dk,dv]")
+    dev, dt = q.get_device(), q.dtype
+    for t, name, dims in ((v, "v", 3), (states, "states", 4), (log_decay, "log_decay", 0)):
+        if not isinstance(t, _torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if dims and t.dim() != dims or q.dim() != 3:
+            raise ValueError(f"q must be [{rows_name},G,dk], v [{rows_name},H,dv] and states [slots,H,dk,dv]")
     R, G, dk = q.shape
-    H, dv = v.shape[1], v.shape[2]
+    _, H, dv = v.shape
     _is(k, "k", (R, G, dk), dt, dev)
     _is(v, "v", (R, H, dv), dt, dev)
     S = states.shape[0]
     sp = _dense(states, "states", (S, H, dk, dv), _torch.float32, dev)
+    ld = 0
     if log_decay.dim() == 1:
         _is(log_decay, "log_decay", (H,), _torch.float32, dev)
-        ld = 0
     else:
         _is(log_decay, "log_decay", (R, H), _torch.float32, dev)
-        ld = log_decay.stride(0) if R > 1 else H
+        if R > 1:   # 0: the same decays for every row
+            ld = log_decay.stride(0)
     if H > 1 and log_decay.stride(-1) != 1:
         raise ValueError("the last axis of log_decay must be dense")
-    if ld == 0 and log_decay.dim() == 2:
-        log_decay = log_decay[0]   # the same decays for every row
     if out is None:
-        out = _torch.empty((R, H, dv), dtype=dt, device=dev)
+        out = _torch.empty((R, H, dv), dtype=dt, device=v.device)
+        st = (H * dv, dv)
     else:
         _is(out, "out", (R, H, dv), dt, dev)
-    st = LinStridesArg(*_rows(q, "q"), *_rows(k, "k"), *_rows(v, "v"), *_rows(out, "out"))
+        st = _rows(out, "out")
+    st = _arg(LinStridesArg, *_rows(q, "q"), *_rows(k, "k"), *_rows(v, "v"), *st)
     return code, dev, (R, G, H, dk, dv, S), sp, ld, log_decay.data_ptr() or None, out, st
 
 
@@ -198,12 +221,12 @@ def lin_prefill(q, k, v, log_decay, cu_seqlens, states, *, slots=None, carry=Non
     max_seqlen = int(max_seqlen or 0)
     if max_seqlen < 0:
         raise ValueError("max_seqlen must not be negative")
-    s = LinShapeArg(T, N, G, H, dk, dv, S)
-    need = lib.lin_prefill_workspace_size(ctypes.byref(s), max_seqlen)
+    s = _arg(LinShapeArg, T, N, G, H, dk, dv, S)
+    need = lib.lin_prefill_workspace_size(s, max_seqlen)
     if need == _sz(-1).value:
         raise ValueError(f"unsupported or invalid shape: T {T}, N {N}, G {G}, H {H}, dk {dk}, dv {dv}")
     wp, wn, _keep = _bytes(need, dev, workspace)
-    _call(lib.lin_prefill, "lin_prefill", dev, ctypes.byref(s), code, ctypes.byref(st), q.data_ptr() or None,
+    _call(lib.lin_prefill, "lin_prefill", dev, s, code, st, q.data_ptr() or None,
           k.data_ptr() or None, v.data_ptr() or None, lp, ld, cu, _ids(slots, "slots", N, dev),
           _ids(carry, "carry", N, dev), max_seqlen, sp, out.data_ptr() or None, wp, wn)
     return out
@@ -216,8 +239,8 @@ def lin_step(q, k, v, log_decay, states, *, slots=None, out=None):
     a negative slot are skipped and leave ``out`` as it is."""
     lib = _lib()
     code, dev, (N, G, H, dk, dv, S), sp, ld, lp, out, st = _lin_args(q, k, v, log_decay, states, out, "N")
-    s = LinShapeArg(0, N, G, H, dk, dv, S)
-    _call(lib.lin_step, "lin_step", dev, ctypes.byref(s), code, ctypes.byref(st), q.data_ptr() or None,
+    s = _arg(LinShapeArg, 0, N, G, H, dk, dv, S)
+    _call(lib.lin_step, "lin_step", dev, s, code, st, q.data_ptr() or None,
           k.data_ptr() or None, v.data_ptr() or None, lp, ld, _ids(slots, "slots", N, dev), sp,
           out.data_ptr() or None)
     return out
@@ -250,12 +273,12 @@ def _gn_args(x, weight, bias, groups, gate):
     groups = int(groups)
     if groups < 1 or C < 1 or C % groups:
         raise ValueError(f"{C} channels cannot be cut into {groups} groups")
-    dev, shape = x.device, tuple(x.shape)
+    dev, shape = x.get_device(), tuple(x.shape)
     xp, ldx = _gn_rows(x, "x", shape, x.dtype, dev)
     wp = None if weight is None else _dense(weight, "weight", (C,), _torch.float32, dev)
     bp = None if bias is None else _dense(bias, "bias", (C,), _torch.float32, dev)
     gp, ldg = (None, 0) if gate is None else _gn_rows(gate, "gate", shape, x.dtype, dev)
-    return code, dev, shape, GnShapeArg(N, L, C, groups), xp, ldx, wp, bp, gp, ldg
+    return code, dev, shape, (N, L, C, groups), xp, ldx, wp, bp, gp, ldg
 
 
 def _act(act):
@@ -285,13 +308,14 @@ def gn_fwd(x, weight, bias, groups, *, gate=None, act="silu", eps=1e-5, out=None
     if not eps >= 0:
         raise ValueError("eps must not be negative")
     if out is None:
-        out = _torch.empty(shape, dtype=x.dtype, device=dev)
+        out = _torch.empty(shape, dtype=x.dtype, device=x.device)
     if stats is None:
-        stats = _torch.empty((s.N, s.groups, 2), dtype=_torch.float32, device=dev)
+        stats = _torch.empty((s[0], s[3], 2), dtype=_torch.float32, device=x.device)
     op = _dense(out, "out", shape, x.dtype, dev)
-    stp = _dense(stats, "stats", (s.N, s.groups, 2), _torch.float32, dev)
-    wsp, wsn, _keep = _bytes(gn_workspace_size(s.N, s.L, s.C, s.groups), dev, workspace)
-    _call(lib.gn_fwd, "gn_fwd", dev, ctypes.byref(s), code, _act(act), eps, xp, ldx, wp, bp, gp, ldg, op, stp, wsp, wsn)
+    stp = _dense(stats, "stats", (s[0], s[3], 2), _torch.float32, dev)
+    ref = _arg(GnShapeArg, *s)
+    wsp, wsn, _keep = _bytes(lib.gn_fwd_workspace_size(ref), dev, workspace)
+    _call(lib.gn_fwd, "gn_fwd", dev, ref, code, _act(act), eps, xp, ldx, wp, bp, gp, ldg, op, stp, wsp, wsn)
     return out, stats
 
 
@@ -302,18 +326,19 @@ def gn_bwd(x, weight, bias, groups, stats, dy, *, gate=None, act="silu", out=Non
     lib = _lib()
     code, dev, shape, s, xp, ldx, wp, bp, gp, ldg = _gn_args(x, weight, bias, groups, gate)
     dyp, ldy = _gn_rows(dy, "dy", shape, x.dtype, dev)
-    stp = _dense(stats, "stats", (s.N, s.groups, 2), _torch.float32, dev)
+    stp = _dense(stats, "stats", (s[0], s[3], 2), _torch.float32, dev)
     if out is None:
-        dx = _torch.empty(shape, dtype=x.dtype, device=dev)
-        dw, db = (_torch.empty(s.C, dtype=_torch.float32, device=dev) for _ in range(2))
-        dg = None if gate is None else _torch.empty(shape, dtype=x.dtype, device=dev)
+        dx = _torch.empty(shape, dtype=x.dtype, device=x.device)
+        dw, db = (_torch.empty(s[2], dtype=_torch.float32, device=x.device) for _ in range(2))
+        dg = None if gate is None else _torch.empty(shape, dtype=x.dtype, device=x.device)
     else:
         dx, dw, db, dg = tuple(out) if gate is not None else (*tuple(out)[:3], None)
     dxp = _dense(dx, "dx", shape, x.dtype, dev)
-    dwp, dbp = (_dense(t, n, (s.C,), _torch.float32, dev) for t, n in ((dw, "dweight"), (db, "dbias")))
+    dwp, dbp = (_dense(t, n, (s[2],), _torch.float32, dev) for t, n in ((dw, "dweight"), (db, "dbias")))
     dgp = None if dg is None else _dense(dg, "dgate", shape, x.dtype, dev)
-    wsp, wsn, _keep = _bytes(gn_workspace_size(s.N, s.L, s.C, s.groups, True), dev, workspace)
-    _call(lib.gn_bwd, "gn_bwd", dev, ctypes.byref(s), code, _act(act), xp, ldx, wp, bp, gp, ldg, stp, dyp, ldy, dxp, dwp,
+    ref = _arg(GnShapeArg, *s)
+    wsp, wsn, _keep = _bytes(lib.gn_bwd_workspace_size(ref), dev, workspace)
+    _call(lib.gn_bwd, "gn_bwd", dev, ref, code, _act(act), xp, ldx, wp, bp, gp, ldg, stp, dyp, ldy, dxp, dwp,
           dbp, dgp, wsp, wsn)
     return dx, dw, db, dg
 
@@ -321,7 +346,7 @@ def gn_bwd(x, weight, bias, groups, stats, dy, *, gate=None, act="silu", out=Non
 def _cache_args(states, cache, scales, slots, entries):
     if not isinstance(states, _torch.Tensor) or states.dim() != 4 or not states.is_cuda:
         raise ValueError("states must be a [slots,H,dk,dv] tensor on a HIP device")
-    dev = states.device
+    dev = states.get_device()
     S, H, dk, dv = states.shape
     sp = _dense(states, "states", (S, H, dk, dv), _torch.float32, dev)
     if not isinstance(cache, _torch.Tensor) or cache.dim() != 4:
@@ -332,7 +357,7 @@ def _cache_args(states, cache, scales, slots, entries):
     n = slots.shape[0] if slots is not None else entries.shape[0] if entries is not None else min(S, E)
     if (slots is None and n > S) or (entries is None and n > E):
         raise ValueError(f"{n} pairs, {S} slots and {E} entries")
-    return (dev, StateCacheShapeArg(n, S, E, H, dk, dv), sp, cp, ep, _ids(slots, "slots", n, dev),
+    return (dev, _arg(StateCacheShapeArg, n, S, E, H, dk, dv), sp, cp, ep, _ids(slots, "slots", n, dev),
             _ids(entries, "entries", n, dev))
 
 
@@ -344,7 +369,7 @@ def state_pack(states, cache, scales, *, slots=None, entries=None):
     are skipped; of pairs with one entry the last counts."""
     lib = _lib()
     dev, s, sp, cp, ep, ids, ide = _cache_args(states, cache, scales, slots, entries)
-    _call(lib.state_pack, "state_pack", dev, ctypes.byref(s), sp, ids, ide, cp, ep)
+    _call(lib.state_pack, "state_pack", dev, s, sp, ids, ide, cp, ep)
 
 
 def state_unpack(cache, scales, states, *, entries=None, slots=None):
@@ -353,4 +378,4 @@ def state_unpack(cache, scales, states, *, entries=None, slots=None):
     `state_pack`; an entry that does not exist gives NaN."""
     lib = _lib()
     dev, s, sp, cp, ep, ids, ide = _cache_args(states, cache, scales, slots, entries)
-    _call(lib.state_unpack, "state_unpack", dev, ctypes.byref(s), cp, ep, ide, ids, sp)
+    _call(lib.state_unpack, "state_unpack", dev, s, cp, ep, ide, ids, sp)
