@@ -5,10 +5,12 @@
 // q, k, v and y are 1/dk of that), so memory bounds it, and for a few rows
 // the latency of two dependent loads (slot, then state).
 #include "layer_device.h"
+#include "ssd_internal.h"
 
 namespace layer {
 
 constexpr int ST = 256;   // threads of a block
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 struct StepArgs {
     const void *q, *k, *v;
@@ -20,6 +22,24 @@ struct StepArgs {
     lin_strides st;
     int N, G, H, dk, dv, nslots, tiles;
 };
+
+// A piece of a state.  STREAM: non-temporal, past the caches.
+template <int N, bool STREAM>
+__device__ __forceinline__ Vec<float, N> load_state(const float *p)
+{
+    if constexpr (STREAM && N == 4)
+        return __builtin_bit_cast(Vec<float, 4>, __builtin_nontemporal_load(reinterpret_cast<const f32x4 *>(p)));
+    else
+        return *reinterpret_cast<const Vec<float, N> *>(p);
+}
+template <int N, bool STREAM>
+__device__ __forceinline__ void store_state(float *p, const Vec<float, N> &x)
+{
+    if constexpr (STREAM && N == 4)
+        __builtin_nontemporal_store(__builtin_bit_cast(f32x4, x), reinterpret_cast<f32x4 *>(p));
+    else
+        *reinterpret_cast<Vec<float, N> *>(p) = x;
+}
 
 // Looks for other rows of row n's slot: whether an earlier one has it, and
 // the next later one (N if none).  All rows are looked at by every wave, 64
@@ -42,7 +62,7 @@ __device__ __forceinline__ void same_slot(const int32_t *slots, int N, int n, in
 
 // One block takes TV = CL * VEC columns of one head's state for one row: CL
 // threads across a row of the state, ST / CL rows at a time.
-template <typename T, int VEC, int CL>
+template <typename T, int VEC, int CL, bool STREAM>
 __global__ __launch_bounds__(ST) void k_lin_step(StepArgs a)
 {
     constexpr int TV = CL * VEC, R = ST / CL;
@@ -83,13 +103,13 @@ __global__ __launch_bounds__(ST) void k_lin_step(StepArgs a)
         if (on) {
 #pragma unroll 8
             for (int r = r0; r < a.dk; r += R) {
-                V x = *reinterpret_cast<const V *>(S + (int64_t)r * a.dv);
+                V x = load_state<VEC, STREAM>(S + (int64_t)r * a.dv);
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) {
                     x.v[i] = dec * x.v[i] + ks[r] * vv[i];
                     y[i] += qs[r] * x.v[i];
                 }
-                *reinterpret_cast<V *>(S + (int64_t)r * a.dv) = x;
+                store_state<VEC, STREAM>(S + (int64_t)r * a.dv, x);
             }
         }
 #pragma unroll
@@ -113,18 +133,30 @@ __global__ __launch_bounds__(ST) void k_lin_step(StepArgs a)
     }
 }
 
+// Columns of a block: as many as dv has, up to 128, so that no thread is
+// idle (24 heads of 64 columns: 91 us with 64, 97 with 128); fewer while
+// there is no block for every CU (one row of 8 heads of 128 x 128: 4.2 us with
+// 32, 5.9 with 128).
+//
+// States of more than 128 MiB in a call go past the caches: 256 rows of 24
+// heads of 128 x 64 (201 MB) took 84 us so and 91 otherwise where other data
+// passed in between, as other layers' does; the same states alone and again,
+// 82 and 62.
 template <typename T>
-static void launch_step(StepArgs &a, hipStream_t st)
+static void launch_step(StepArgs &a, int cus, hipStream_t st)
 {
-    const bool vec = a.dv % 4 == 0 && !misaligned(a.states, 16);
     const auto go = [&](auto kernel, int tv) {
         a.tiles = (a.dv + tv - 1) / tv;
         kernel<<<dim3((unsigned)((int64_t)a.N * a.H * a.tiles)), dim3(ST), 0, st>>>(a);
     };
-    if (vec)
-        go(k_lin_step<T, 4, 32>, 128);
-    else
-        go(k_lin_step<T, 1, 64>, 64);
+    if (a.dv % 4 != 0 || misaligned(a.states, 16)) return go(k_lin_step<T, 1, 64, false>, 64);
+    const auto blocks = [&](int tv) { return (int64_t)a.N * a.H * ((a.dv + tv - 1) / tv); };
+    const bool stream = (int64_t)a.N * a.H * a.dk * a.dv * 4 > (int64_t(128) << 20);
+    if (a.dv > 64 && blocks(128) >= cus)
+        return stream ? go(k_lin_step<T, 4, 32, true>, 128) : go(k_lin_step<T, 4, 32, false>, 128);
+    if (a.dv > 32 && blocks(64) >= cus)
+        return stream ? go(k_lin_step<T, 4, 16, true>, 64) : go(k_lin_step<T, 4, 16, false>, 64);
+    return stream ? go(k_lin_step<T, 4, 8, true>, 32) : go(k_lin_step<T, 4, 8, false>, 32);
 }
 
 }  // namespace layer
@@ -164,6 +196,6 @@ extern "C" int lin_step(const lin_shape *shape, int dtype, const lin_strides *st
     a.dk = (int)s.dk;
     a.dv = (int)s.dv;
     a.nslots = (int)s.slots;
-    LAYER_DISPATCH(dtype, launch_step<T>(a, static_cast<hipStream_t>(stream)));
+    LAYER_DISPATCH(dtype, launch_step<T>(a, ssd::device_cus(), static_cast<hipStream_t>(stream)));
     return launch_status();
 }
