@@ -12,6 +12,10 @@ namespace layer {
 constexpr int64_t kMaxHeadDim = 256;
 constexpr int64_t kMaxCount = int64_t(1) << 24;   // sequences, slots, entries, row strides
 
+// Blocks of `threads` threads that one launch may have: a grid's threads are
+// counted in 32 bits.
+constexpr int64_t max_blocks(int threads) { return ((int64_t(1) << 32) - 1) / threads; }
+
 int check_dtype(int dtype);
 int check_lin(const lin_shape *s, bool step);
 // The strides to use (dense ones where `st` is null) for `rows` rows, or

@@ -27,12 +27,13 @@ __device__ __forceinline__ bool takes(const CacheArgs &a, int i, int &src, int &
     dst = index_of(a.dst, i);
     if (src < 0 || dst < 0 || dst >= a.ndst) return false;
     if (!a.dst) return true;
+    bool again = false;
+#pragma unroll 4
     for (int j0 = i + 1; j0 < a.n; j0 += 64) {
         const int j = j0 + (int)(threadIdx.x & 63);
-        const bool again = j < a.n && a.dst[j] == dst && index_of(a.src, j) >= 0;
-        if (__ballot(again) != 0) return false;
+        again = again || (j < a.n && a.dst[j < a.n ? j : 0] == dst && index_of(a.src, j < a.n ? j : 0) >= 0);
     }
-    return true;
+    return __ballot(again) == 0;
 }
 
 // One thread holds 4 values of a block, 8 threads the block; a thread takes
@@ -173,7 +174,7 @@ static int cache_args(const state_cache_shape &s, const int32_t *src, int64_t ns
     a->per = (unsigned)(a->rows * a->nb);   // below 2^16 2^8 2^3
     const int64_t chunks = (a->per + CT / 8 * U - 1) / (CT / 8 * U);
     a->chunks = (int)chunks;
-    if (s.n > ((int64_t(1) << 31) - 1) / chunks) return SSD_ERR_SHAPE;
+    if (s.n > max_blocks(CT) / chunks) return SSD_ERR_SHAPE;
     *grid = (unsigned)(s.n * chunks);
     return SSD_OK;
 }

@@ -18,7 +18,8 @@
 //   each channel's sums over a part, k_gn_mid joins these for each run, and
 //   k_gn_apply reads the data again.
 //
-// k_gn_wsum adds up the parts of dweight and dbias in a fixed order.
+// k_gn_wsum, or k_gn_mid's last blocks, add up the parts of dweight and dbias
+// in a fixed order.
 #include "layer_device.h"
 #include "ssd_internal.h"
 
@@ -36,6 +37,7 @@ struct GnArgs {
     float *mean;        // cut, backward: [N][groups][2], mean(d) and mean(d xh)
     int64_t N, ldx, ldg, ldy;
     int64_t nparts, per;   // cut: parts of a sample, rows of a part
+    int64_t block0;        // cut: the launch's first of the blocks
     int L, C, groups, cg;
     float eps;
     bool silu;
@@ -333,10 +335,11 @@ struct Cut {
     bool on;
     __device__ __forceinline__ explicit Cut(const GnArgs &a)
     {
+        const int64_t block = a.block0 + blockIdx.x;
         const int cp = min(a.C / VE, GT), tiles = (a.C / VE + GT - 1) / GT;
-        const int tile = blockIdx.x % tiles;
-        part = blockIdx.x / tiles % a.nparts;
-        n = blockIdx.x / tiles / a.nparts;
+        const int tile = (int)(block % tiles);
+        part = block / tiles % a.nparts;
+        n = block / tiles / a.nparts;
         rp = GT / cp;
         c = (tile * GT + (int)threadIdx.x % cp) * VE;
         r0 = threadIdx.x / cp;
@@ -450,13 +453,12 @@ __global__ __launch_bounds__(GT) void k_gn_sums(GnArgs a)
 }
 
 // Joins a run's parts and channels: forward, its statistics; backward,
-// mean(d) and mean(d xh).  One block for each run.
+// mean(d) and mean(d xh).
 template <bool BWD>
-__global__ __launch_bounds__(GT) void k_gn_mid(GnArgs a)
+__device__ __forceinline__ void gn_join(const GnArgs &a, int64_t run, float (&red)[2][GT / 64])
 {
-    __shared__ float red[2][GT / 64];
-    const int64_t n = blockIdx.x / a.groups;
-    const int c0 = (int)(blockIdx.x % a.groups) * a.cg;
+    const int64_t n = run / a.groups;
+    const int c0 = (int)(run % a.groups) * a.cg;
     const float *part = a.part + n * a.nparts * 2 * a.C + c0;
     const int64_t items = a.nparts * a.cg;
     const float inv = 1.f / ((float)a.L * (float)a.cg);
@@ -492,10 +494,47 @@ __global__ __launch_bounds__(GT) void k_gn_mid(GnArgs a)
         t = 1.f / sqrtf(t * inv + a.eps);
     }
     if (threadIdx.x == 0) {
-        float *to = (BWD ? a.mean : a.stats) + 2 * (int64_t)blockIdx.x;
+        float *to = (BWD ? a.mean : a.stats) + 2 * run;
         to[0] = s;
         to[1] = t;
     }
+}
+
+// dweight and dbias: sums of `rows` rows of 2 C partial sums, in a fixed
+// order and in 64 bits (there may be millions of rows); columns 32 `block`
+// on, 16 threads to a column.
+__device__ __forceinline__ void gn_wsum(const GnArgs &a, int64_t rows, int64_t block, double (&red)[GT])
+{
+    const int64_t e = block * 32 + (threadIdx.x & 31);
+    double s = 0.0;
+    if (e < 2 * (int64_t)a.C) {
+#pragma unroll 8
+        for (int64_t p = threadIdx.x >> 5; p < rows; p += GT / 32) s += (double)a.part[2 * p * a.C + e];
+    }
+    red[threadIdx.x] = s;
+    __syncthreads();
+    if (threadIdx.x < 32 && e < 2 * (int64_t)a.C) {
+        for (int k = 1; k < GT / 32; ++k) s += red[threadIdx.x + 32 * k];
+        float *to = e < a.C ? a.dw : a.db;
+        if (to) to[e < a.C ? e : e - a.C] = (float)s;
+    }
+}
+
+__global__ __launch_bounds__(GT) void k_gn_wsum(GnArgs a, int64_t rows)
+{
+    __shared__ double red[GT];
+    gn_wsum(a, rows, blockIdx.x, red);
+}
+
+// The joined runs, in `joins` blocks; the blocks after them, in the backward,
+// add up dweight and dbias from the same partial sums.
+template <bool BWD>
+__global__ __launch_bounds__(GT) void k_gn_mid(GnArgs a, unsigned joins, int64_t rows)
+{
+    __shared__ float red[2][GT / 64];
+    __shared__ double wide[GT];
+    if (blockIdx.x >= joins) return gn_wsum(a, rows, blockIdx.x - joins, wide);
+    for (int64_t run = blockIdx.x; run < a.N * a.groups; run += joins) gn_join<BWD>(a, run, red);
 }
 
 template <typename T, int VE, bool BWD>
@@ -536,26 +575,6 @@ __global__ __launch_bounds__(GT) void k_gn_apply(GnArgs a)
         T *to = static_cast<T *>(BWD ? a.dx : a.y);
         if (to) *reinterpret_cast<Vec<T, VE> *>(to + row * a.C + p.c) = y;
         if (BWD && a.dgate) *reinterpret_cast<Vec<T, VE> *>(static_cast<T *>(a.dgate) + row * a.C + p.c) = dg;
-    }
-}
-
-// dweight and dbias: sums of `rows` rows of 2 C partial sums, in a fixed
-// order; 32 columns to a block, 16 threads to a column.
-__global__ __launch_bounds__(GT) void k_gn_wsum(GnArgs a, int64_t rows)
-{
-    __shared__ float red[GT];
-    const int64_t e = (int64_t)blockIdx.x * 32 + (threadIdx.x & 31);
-    float s = 0.f;
-    if (e < 2 * (int64_t)a.C) {
-#pragma unroll 8
-        for (int64_t p = threadIdx.x >> 5; p < rows; p += GT / 32) s += a.part[2 * p * a.C + e];
-    }
-    red[threadIdx.x] = s;
-    __syncthreads();
-    if (threadIdx.x < 32 && e < 2 * (int64_t)a.C) {
-        for (int k = 1; k < GT / 32; ++k) s += red[threadIdx.x + 32 * k];
-        float *to = e < a.C ? a.dw : a.db;
-        if (to) to[e < a.C ? e : e - a.C] = s;
     }
 }
 
@@ -641,7 +660,7 @@ static GnPlan plan_gn(GnArgs &a, bool bwd, int ve_run, int ve_row, int64_t esize
     if (parts < 1) parts = 1;
     a.per = (a.L + parts - 1) / parts;
     a.nparts = (a.L + a.per - 1) / a.per;
-    P.blocks = a.N * a.nparts * tiles;
+    P.blocks = a.N * a.nparts * tiles;   // parts and channel tiles of all samples
     P.mean = (size_t)(a.N * a.nparts) * 2 * a.C * sizeof(float);
     P.total = P.mean + (bwd ? (size_t)(a.N * a.groups) * 2 * sizeof(float) : 0);
     return P;
@@ -718,28 +737,38 @@ static int gn_args(const gn_shape &s, int64_t ldx, int64_t ldg, int64_t ldy, GnA
         else { constexpr int K = 4; __VA_ARGS__; }          \
     } while (0)
 
+// `wanted`: dweight and dbias; the held backward leaves their last sums to
+// k_gn_wsum.
 template <typename T>
-static void run_gn(const GnArgs &a, const GnPlan &P, bool bwd, hipStream_t st)
+static void run_gn(GnArgs a, const GnPlan &P, bool bwd, bool wanted, hipStream_t st)
 {
-    const dim3 grid((unsigned)P.blocks), runs((unsigned)(a.N * a.groups)), blk(GT);
+    const dim3 blk(GT);
+    const int64_t runs = a.N * a.groups, most = max_blocks(GT) / 2;
+    const unsigned joins = (unsigned)(runs < most ? runs : most), sums = (unsigned)((2 * a.C + 31) / 32);
+    // all blocks, in as many launches as it takes
+    const auto all = [&](auto kernel) {
+        for (a.block0 = 0; a.block0 < P.blocks; a.block0 += most) {
+            const int64_t left = P.blocks - a.block0;
+            kernel<<<dim3((unsigned)(left < most ? left : most)), blk, 0, st>>>(a);
+        }
+    };
     GN_DISPATCH(P, {
         if (P.held) {
             GN_DISPATCH_K(P, {
                 if (bwd)
-                    k_gn_bwd_held<T, VE, K><<<grid, blk, 0, st>>>(a);
+                    all(k_gn_bwd_held<T, VE, K>);
                 else
-                    k_gn_fwd_held<T, VE, K><<<grid, blk, 0, st>>>(a);
+                    all(k_gn_fwd_held<T, VE, K>);
             });
+            if (wanted) k_gn_wsum<<<dim3(sums), blk, 0, st>>>(a, a.nparts);
         } else if (bwd) {
-            k_gn_sums<T, VE, true><<<grid, blk, 0, st>>>(a);
-            if (a.dx || a.dgate) {
-                k_gn_mid<true><<<runs, blk, 0, st>>>(a);
-                k_gn_apply<T, VE, true><<<grid, blk, 0, st>>>(a);
-            }
+            all(k_gn_sums<T, VE, true>);
+            k_gn_mid<true><<<dim3(joins + (wanted ? sums : 0)), blk, 0, st>>>(a, joins, a.N * a.nparts);
+            if (a.dx || a.dgate) all(k_gn_apply<T, VE, true>);
         } else {
-            k_gn_sums<T, VE, false><<<grid, blk, 0, st>>>(a);
-            k_gn_mid<false><<<runs, blk, 0, st>>>(a);
-            k_gn_apply<T, VE, false><<<grid, blk, 0, st>>>(a);
+            all(k_gn_sums<T, VE, false>);
+            k_gn_mid<false><<<dim3(joins), blk, 0, st>>>(a, joins, 0);
+            all(k_gn_apply<T, VE, false>);
         }
     });
 }
@@ -796,7 +825,7 @@ extern "C" int gn_fwd(const gn_shape *shape, int dtype, int act, float eps, cons
     a.silu = act == GN_ACT_SILU;
     a.part = static_cast<float *>(workspace);
     const GnPlan P = plan_gn(a, false, widest(a, dtype, a.cg), widest(a, dtype, a.C), dtype_size(dtype), ssd::device_cus());
-    LAYER_DISPATCH(dtype, run_gn<T>(a, P, false, st));
+    LAYER_DISPATCH(dtype, run_gn<T>(a, P, false, false, st));
     return launch_status();
 }
 
@@ -837,15 +866,14 @@ extern "C" int gn_bwd(const gn_shape *shape, int dtype, int act, const void *x, 
     a.db = dbias;
     a.silu = act == GN_ACT_SILU;
     const bool wanted = dweight || dbias;
-    int64_t rows = 0;
     a.part = static_cast<float *>(workspace);
     if (work) {
         const GnPlan P = plan_gn(a, true, widest(a, dtype, a.cg), widest(a, dtype, a.C), dtype_size(dtype), ssd::device_cus());
         a.mean = reinterpret_cast<float *>(static_cast<char *>(workspace) + P.mean);
-        rows = P.held ? a.nparts : a.N * a.nparts;
         if (P.held && !wanted) a.part = nullptr;
-        if (wanted || dx || dgate) LAYER_DISPATCH(dtype, run_gn<T>(a, P, true, st));
+        if (wanted || dx || dgate) LAYER_DISPATCH(dtype, run_gn<T>(a, P, true, wanted, st));
+    } else if (wanted) {
+        k_gn_wsum<<<dim3((unsigned)((2 * s.C + 31) / 32)), dim3(GT), 0, st>>>(a, 0);   // sums of nothing
     }
-    if (wanted) k_gn_wsum<<<dim3((unsigned)((2 * s.C + 31) / 32)), dim3(GT), 0, st>>>(a, rows);
     return launch_status();
 }

@@ -319,11 +319,12 @@ __device__ __forceinline__ void rows_of(const PrefillArgs &a, int n, int &begin,
 __device__ __forceinline__ bool taken(const PrefillArgs &a, int n, int slot)
 {
     bool found = false;
+#pragma unroll 4
     for (int j0 = 0; j0 < n; j0 += 64) {
         const int j = j0 + (int)(threadIdx.x & 63);
-        if (__ballot(j < n && a.slots[j < n ? j : 0] == slot) != 0) found = true;
+        found = found || (j < n && a.slots[j < n ? j : 0] == slot);
     }
-    return found;
+    return __ballot(found) != 0;
 }
 
 // What there is to know about sequence n; everything is loaded at once.
@@ -666,16 +667,16 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 // states that the segments make from zero: V values of a state in a thread.
 // The loads of U segments are in flight together.
 template <int V>
-__global__ __launch_bounds__(CT) void k_lin_carry(PrefillArgs a, int chunks)
+__global__ __launch_bounds__(CT) void k_lin_carry(PrefillArgs a)
 {
     typedef Vec<float, V> X;
     constexpr int U = 16;
-    const int h = blockIdx.x / chunks % a.H;
+    const int h = blockIdx.x % a.H;
     Place p;
     int begin, end;
-    about(a, blockIdx.x / (chunks * a.H), p, begin, end);
+    about(a, blockIdx.x / a.H, p, begin, end);
     const int64_t state = (int64_t)a.dk * a.dv;
-    const int64_t e = ((int64_t)(blockIdx.x % chunks) * CT + threadIdx.x) * V;
+    const int64_t e = ((int64_t)blockIdx.y * CT + threadIdx.x) * V;
     if (p.segs <= 1 || p.bad || e >= state) return;
     X cur = {};
     if (p.carry) cur = *reinterpret_cast<const X *>(a.states + ((int64_t)p.slot * a.H + h) * state + e);
@@ -727,6 +728,11 @@ static PrefillPlan plan_prefill(const lin_shape &s, int64_t max_seqlen, int cus)
     if (seg < 128) seg = 128;
     P.ids = (int)s.N;
     if (longest <= 2 * seg) return P;
+    // and no more of them than a launch has blocks for
+    const int64_t most = max_blocks(512) / (s.H * tiles) - s.N;
+    if (most < 1) return P;
+    if (s.T / seg > most) seg = (s.T / most + 64) / 64 * 64;
+    if (longest <= 2 * seg || seg >= (int64_t(1) << 30)) return P;
     P.seg = (int)seg;
     P.ids = (int)(s.T / seg + s.N);
     size_t o = 0;
@@ -747,11 +753,11 @@ static int run_prefill(PrefillArgs &a, hipStream_t st)
         k_lin_chunks<E, KP, VT, C, false, VEC><<<dim3((unsigned)grid), dim3(512), 0, st>>>(a);
         const int v = a.dk * a.dv % 4 == 0 && !misaligned(a.states, 16) ? 4 : 1;
         const int chunks = (a.dk * a.dv + CT * v - 1) / (CT * v);
-        const dim3 g((unsigned)((int64_t)a.N * a.H * chunks));
+        const dim3 g((unsigned)(a.N * a.H), (unsigned)chunks);
         if (v == 4)
-            k_lin_carry<4><<<g, dim3(CT), 0, st>>>(a, chunks);
+            k_lin_carry<4><<<g, dim3(CT), 0, st>>>(a);
         else
-            k_lin_carry<1><<<g, dim3(CT), 0, st>>>(a, chunks);
+            k_lin_carry<1><<<g, dim3(CT), 0, st>>>(a);
     }
     k_lin_chunks<E, KP, VT, C, true, VEC><<<dim3((unsigned)grid), dim3(512), 0, st>>>(a);
     return launch_status();

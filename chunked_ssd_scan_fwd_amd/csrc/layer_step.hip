@@ -42,21 +42,27 @@ __device__ __forceinline__ void store_state(float *p, const Vec<float, N> &x)
 }
 
 // Looks for other rows of row n's slot: whether an earlier one has it, and
-// the next later one (N if none).  All rows are looked at by every wave, 64
-// at a time, so this is one load's latency for a batch of up to 64.
+// the next later one (N if none).  All rows are looked at by every wave, 256
+// at a time, which is one load's latency.
 __device__ __forceinline__ void same_slot(const int32_t *slots, int N, int n, int sl, bool &before, int &next)
 {
     const int lane = threadIdx.x & 63;
     before = false;
     next = N;
-    for (int j0 = 0; j0 < N; j0 += 64) {
-        const int j = j0 + lane;
-        const unsigned long long m = __ballot(j < N && j != n && slots[j < N ? j : 0] == sl);
-        if (m == 0) continue;
-        const int first = j0 + __ffsll((unsigned long long)m) - 1;
-        if (first < n) before = true;
-        const unsigned long long later = n >= j0 ? (n - j0 >= 63 ? 0ull : m & (~0ull << (n - j0 + 1))) : m;
-        if (later != 0 && next == N) next = j0 + __ffsll((unsigned long long)later) - 1;
+    for (int j0 = 0; j0 < N; j0 += 256) {
+        bool same[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int j = j0 + 64 * u + lane;
+            same[u] = j < N && slots[j < N ? j : 0] == sl;
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int j = j0 + 64 * u + lane;
+            before = before || __ballot(same[u] && j < n) != 0;
+            const unsigned long long later = __ballot(same[u] && j > n);
+            if (later != 0 && next == N) next = j0 + 64 * u + __ffsll(later) - 1;
+        }
     }
 }
 

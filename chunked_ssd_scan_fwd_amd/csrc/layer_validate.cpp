@@ -18,10 +18,9 @@ int check_lin(const lin_shape *s, bool step)
     if (s->dk > kMaxHeadDim || s->dv > kMaxHeadDim) return SSD_ERR_UNSUPPORTED;
     if (s->N >= kMaxCount || s->slots >= kMaxCount || s->H >= 65536) return SSD_ERR_SHAPE;
     if (!step && s->T >= (int64_t(1) << 31)) return SSD_ERR_SHAPE;
-    // every launch grid is one-dimensional, with at most 8 column tiles to a
-    // head and a segment for every 64 rows
-    const int64_t rows = step ? s->N : s->T / 64 + s->N;
-    if (rows > ((int64_t(1) << 31) - 1) / (8 * s->H)) return SSD_ERR_SHAPE;
+    // a block for each row (or sequence), head and column tile
+    const int64_t tiles = (s->dv + 31) / 32;
+    if (s->N > max_blocks(512) / (s->H * tiles)) return SSD_ERR_SHAPE;
     return SSD_OK;
 }
 
@@ -51,7 +50,6 @@ int check_gn(const gn_shape *s, int act)
     const int64_t lim = int64_t(1) << 40;
     if (s->C >= kMaxCount || s->L >= (int64_t(1) << 31) || s->N > lim) return SSD_ERR_SHAPE;
     if (s->N > lim / (s->L + 1) || s->N * (s->L + 1) > lim / s->C) return SSD_ERR_SHAPE;
-    if (s->N > ((int64_t(1) << 30) - 1) / s->groups) return SSD_ERR_SHAPE;   // a block for each run
     return SSD_OK;
 }
 

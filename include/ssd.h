@@ -389,8 +389,8 @@ typedef struct lin_strides {
 size_t lin_prefill_workspace_size(const lin_shape *shape, int64_t max_seqlen);
 
 /* The scan of a packed batch.  Sequence n is rows cu_seqlens[n] ..
- * cu_seqlens[n+1]-1 (int32 [N+1], rising, within 0..T; values outside are
- * clamped); rows of no sequence are not read, and their y is left as it was.
+ * cu_seqlens[n+1]-1 (int32 [N+1], rising, within 0..T; other values give
+ * unspecified results, but no row outside 0..T is touched); rows of no sequence are not read, and their y is left as it was.
  * For each sequence and head h, with g = h / (H/G),
  *     S_t = exp(log_decay_t) S_{t-1} + k_t v_t^T,   y_t = S_t^T q_t,
  * in chunks, from the state in slot slots[n] of `states` [slots][H][dk][dv]
@@ -399,8 +399,9 @@ size_t lin_prefill_workspace_size(const lin_shape *shape, int64_t max_seqlen);
  * zero where carry[n] is 0.
  *   log_decay     float32: [H], one for each head, when decay_stride is 0;
  *                 else rows of H, decay_stride apart, one for each token.
- *                 Finite, or -inf (the state is forgotten); positive values
- *                 are growth, and overflow is the caller's risk.
+ *                 Finite, or -inf (the state is forgotten, unless it holds
+ *                 infinities or NaN); positive values are growth, and
+ *                 overflow is the caller's risk.
  *   slots         int32 [N]; NULL: sequence n has slot n (N <= slots).
  *                 Negative: the sequence starts from zero and its state is
  *                 not kept.  Not below `slots`, or the slot of an earlier
@@ -412,8 +413,9 @@ size_t lin_prefill_workspace_size(const lin_shape *shape, int64_t max_seqlen);
  * Infinite and NaN values of a sequence's rows stay within that sequence,
  * and reach rows up to 63 positions before their own.
  * dk, dv in 1..256 (else SSD_ERR_UNSUPPORTED), G >= 1, H % G == 0,
- * T < 2^31, N and slots < 2^24, row strides below 2^24 elements, and strides
- * of y that let no two of its values overlap (else SSD_ERR_SHAPE). */
+ * T < 2^31, N and slots < 2^24, N H ceil(dv / 32) < 2^23, row strides below
+ * 2^24 elements, and strides of y that let no two of its values overlap (else
+ * SSD_ERR_SHAPE). */
 int lin_prefill(const lin_shape *shape, int dtype, const lin_strides *strides,
                 const void *q, const void *k, const void *v,
                 const float *log_decay, int64_t decay_stride,
@@ -443,7 +445,7 @@ int lin_step(const lin_shape *shape, int dtype, const lin_strides *strides,
  * (1 and 0).  stats [N][groups][2] receives mu and rstd.
  * Row n L + l of x, gate, dy starts ld_* elements after the row before it
  * (0: C); y, dx and dgate are dense.  C % groups == 0; N L C < 2^40, C and
- * the strides below 2^24, L < 2^31, N groups < 2^30. */
+ * the strides below 2^24, L < 2^31. */
 typedef struct gn_shape {
     int64_t N, L, C, groups;
 } gn_shape;
@@ -485,7 +487,8 @@ int gn_bwd(const gn_shape *shape, int dtype, int act,
  * with a negative index, or whose destination does not exist, is skipped; a
  * source that does not exist makes the destination NaN; of pairs with one
  * destination the last counts.  The states and the cache must not overlap.
- * 1 <= dk, dv <= 256; n, slots and entries < 2^24. */
+ * 1 <= dk, dv <= 256; n, slots and entries < 2^24; n H dk ceil(dv / 32) < 2^30
+ * (n at most 2^24 states however small). */
 #define STATE_CACHE_BLOCK 32
 typedef struct state_cache_shape {
     int64_t n, slots, entries, H, dk, dv;

@@ -433,6 +433,28 @@ def test_group_norm_far_mean_and_constant_groups():
     ref.within(stats[..., 1], torch.full((20, 4), 1e-5, dtype=torch.float64).rsqrt(), torch.full((1,), 1e-3))
 
 
+def test_group_norm_more_samples_than_a_launch_has_blocks():
+    """Runs that are cut, of more samples than one grid holds: every sample's statistics and results."""
+    N, L = 8_400_000, 257
+    say(f"gn {N} samples of {L}")
+    x = torch.empty(N, L, 1, dtype=F16, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(1)
+    for part in x.split(1 << 20):
+        part.copy_(torch.randn(part.shape, generator=g, device="cuda") * 2 + 1)
+    y, stats = ssd.gn_fwd(x, None, None, 1, act="none")
+    dx, dw, db, _ = ssd.gn_bwd(x, None, None, 1, stats, y, act="none")
+    for a in range(0, N, 1 << 20):
+        X = x[a:a + (1 << 20)].float()
+        var, mu = torch.var_mean(X, dim=1, correction=0, keepdim=True)
+        z = (X - mu) * torch.rsqrt(var + 1e-5)
+        assert float((y[a:a + (1 << 20)].float() - z).abs().max()) < 2.0 ** -11 * 8
+        assert float((stats[a:a + (1 << 20), 0, 0] - mu[:, 0, 0]).abs().max()) < 1e-5
+        # dy = y = xh up to its rounding: dx = rstd (xh - mean xh - xh mean xh^2) is that rounding's size
+        assert float(dx[a:a + (1 << 20)].abs().max()) < 8 * 2.0 ** -10
+    # sum of xh^2 over everything, N L up to roundings of y and sums of 2e9 terms
+    assert abs(float(dw) / (N * L) - 1) < 1e-3
+
+
 def test_group_norm_extreme_gates():
     """SiLU and its derivative where e^-u overflows or vanishes, and of infinite gates."""
     x, w, b, gate, dy = gn_inputs(4, 1, 32, F32, True)

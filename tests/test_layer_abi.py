@@ -49,6 +49,8 @@ def lin(shape, step=False, dtype=1, strides=None, ptr=P, ld=0, max_len=0, ws=(No
     ((5, 1 << 24, 1, 4, 8, 8, 4), SHAPE),
     ((5, 2, 1, 1 << 16, 8, 8, 4), SHAPE),
     ((5, (1 << 24) - 1, 1, 4096, 8, 8, 4), SHAPE),   # more blocks than a grid holds
+    ((5, 1 << 23, 1, 1, 8, 8, 4), SHAPE),
+    ((5, 1 << 21, 1, 1, 8, 97, 4), SHAPE),
 ])
 def test_lin_shapes_refused(step, shape, code):
     assert lin(LinShapeArg(*shape), step) == code
@@ -113,7 +115,7 @@ def gn(shape, bwd=False, dtype=1, act=1, eps=1e-5, ptr=P, ws=(P, 1 << 40), ld=(0
 def test_gn_arguments_refused(bwd):
     s = GnShapeArg(3, 4, 12, 3)
     for bad in ((3, 4, 12, 5), (3, 4, 12, 0), (-1, 4, 12, 3), (3, -1, 12, 3), (3, 4, 0, 3), (3, 4, 1 << 24, 1),
-                (3, 1 << 31, 12, 3), (1 << 40, 1 << 20, 12, 3), (1 << 31, 1, 2, 2)):
+                (3, 1 << 31, 12, 3), (1 << 40, 1 << 20, 12, 3)):
         assert gn(GnShapeArg(*bad), bwd) == SHAPE, bad
     assert gn(s, bwd, dtype=7) == UNSUPPORTED and gn(s, bwd, act=2) == UNSUPPORTED
     assert gn(s, bwd, ld=(-1, 0, 0)) == SHAPE and gn(s, bwd, ld=(0, 1 << 24, 0)) == SHAPE
