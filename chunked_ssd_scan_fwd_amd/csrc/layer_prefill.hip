@@ -395,8 +395,20 @@ struct ChunkLds {
     Decays<C> dec[3];
 };
 
+// Blocks that share a CU.  With 64 columns and 32-row chunks two of them fit
+// its LDS and registers, and fill each other's waits: 20 mixed prompts of 24
+// heads of 128 x 64 took 48 us so, 64 with one and 64-row chunks.  With 128
+// columns one with 64-row chunks did as well as two with 32 (114 us for 65536
+// rows of 8 heads), and better where there is one block for each CU.
+template <typename E, int KP, int VT>
+struct PerCu {
+    static constexpr int n = VT == 64 && KP <= 128 && std::is_same<E, bf16>::value ? 2 : 1;
+    static constexpr int C = n == 2 || sizeof(E) == 4 || KP > 128 || !std::is_same<E, bf16>::value ? 32 : 64;
+};
+
 template <typename E, int KP, int VT, int C, bool OUT, bool VEC>
-__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_lin_chunks(PrefillArgs a)
+__global__ __launch_bounds__(512)
+__attribute__((amdgpu_waves_per_eu(2 * PerCu<E, KP, VT>::n, 2 * PerCu<E, KP, VT>::n))) void k_lin_chunks(PrefillArgs a)
 {
     typedef ChunkLds<E, KP, VT, C, OUT> Lds;
     typedef typename Lds::L L;
@@ -713,21 +725,24 @@ struct PrefillPlan {
 static int col_tile(int64_t dk, int64_t dv) { return dk > 128 || dv <= 64 ? 64 : 128; }
 
 // Sequences are cut where whole ones would leave CUs idle: into segments of a
-// length that makes about one block for each CU out of the batch's rows, at
-// least 128 rows.  Cutting runs a second pass over k and v and a third over
-// the segments' states, so sequences of up to two such lengths stay whole:
-// 20 prompts whose longest was 1.1 segments took 64 us whole and 96 us cut;
-// one of 32 segments takes 178 us cut and 3.4 ms whole.
-static PrefillPlan plan_prefill(const lin_shape &s, int64_t max_seqlen, int cus)
+// length that makes about one block for each place on a CU out of the batch's
+// rows, at least 128 rows.  Cutting runs a second pass over k and v and a
+// third over the segments' states, so while the longest sequence is not twice
+// what a CU's share of the rows is, all stay whole: 20 prompts whose longest
+// was 1.1 shares took 64 us whole and 96 us cut; one of 32 shares takes 178 us
+// cut and 3.4 ms whole.
+static PrefillPlan plan_prefill(const lin_shape &s, int dtype, int64_t max_seqlen, int cus)
 {
     PrefillPlan P;
     const int64_t longest = max_seqlen > 0 && max_seqlen < s.T ? max_seqlen : s.T;
     const int64_t vt = col_tile(s.dk, s.dv), tiles = (s.dv + vt - 1) / vt;
-    int64_t seg = (s.T * s.H * tiles + cus - 1) / cus;
-    seg = (seg + 63) / 64 * 64;
+    const int64_t per_cu = vt == 64 && s.dk <= 128 && dtype == LAYER_BF16 ? 2 : 1;   // PerCu
+    const int64_t work = s.T * s.H * tiles;
+    const auto share = [&](int64_t places) { return (work + places - 1) / places; };
+    int64_t seg = (share(per_cu * cus) + 63) / 64 * 64;
     if (seg < 128) seg = 128;
     P.ids = (int)s.N;
-    if (longest <= 2 * seg) return P;
+    if (longest <= 2 * seg || longest <= 2 * share(cus)) return P;
     // and no more of them than a launch has blocks for
     const int64_t most = max_blocks(512) / (s.H * tiles) - s.N;
     if (most < 1) return P;
@@ -745,9 +760,20 @@ static PrefillPlan plan_prefill(const lin_shape &s, int64_t max_seqlen, int cus)
     return P;
 }
 
-template <typename E, int KP, int VT, int C, bool VEC>
+// The workspace for any element type.
+static size_t prefill_workspace(const lin_shape &s, int64_t max_seqlen, int cus)
+{
+    const size_t a = plan_prefill(s, LAYER_BF16, max_seqlen, cus).total;
+    const size_t b = plan_prefill(s, LAYER_F32, max_seqlen, cus).total;
+    return a > b ? a : b;
+}
+
+template <typename E, int KP, int VT, bool VEC>
 static int run_prefill(PrefillArgs &a, hipStream_t st)
 {
+    // chunks of 64 rows; of 32 for float tiles, which are twice as wide, for
+    // rows of 256, and where two blocks share a CU
+    constexpr int C = PerCu<E, KP, VT>::C;
     const int64_t grid = (int64_t)a.ids * a.H * a.tiles;
     if (a.seg > 0) {
         k_lin_chunks<E, KP, VT, C, false, VEC><<<dim3((unsigned)grid), dim3(512), 0, st>>>(a);
@@ -766,12 +792,10 @@ static int run_prefill(PrefillArgs &a, hipStream_t st)
 template <typename E, bool VEC>
 static int dispatch_prefill(PrefillArgs &a, hipStream_t st)
 {
-    // float tiles are twice as wide: half the rows to a chunk
-    constexpr int C = std::is_same<E, bf16>::value ? 64 : 32;
     const bool wide = col_tile(a.dk, a.dv) == 128;
-    if (a.dk > 128) return run_prefill<E, 256, 64, 32, VEC>(a, st);
-    if (a.dk > 64) return wide ? run_prefill<E, 128, 128, C, VEC>(a, st) : run_prefill<E, 128, 64, C, VEC>(a, st);
-    return wide ? run_prefill<E, 64, 128, C, VEC>(a, st) : run_prefill<E, 64, 64, C, VEC>(a, st);
+    if (a.dk > 128) return run_prefill<E, 256, 64, VEC>(a, st);
+    if (a.dk > 64) return wide ? run_prefill<E, 128, 128, VEC>(a, st) : run_prefill<E, 128, 64, VEC>(a, st);
+    return wide ? run_prefill<E, 64, 128, VEC>(a, st) : run_prefill<E, 64, 64, VEC>(a, st);
 }
 
 }  // namespace layer
@@ -781,7 +805,7 @@ using namespace layer;
 extern "C" size_t lin_prefill_workspace_size(const lin_shape *shape, int64_t max_seqlen)
 {
     if (check_lin(shape, false) != SSD_OK || max_seqlen < 0) return (size_t)-1;
-    return plan_prefill(*shape, max_seqlen, ssd::device_cus()).total;
+    return prefill_workspace(*shape, max_seqlen, ssd::device_cus());
 }
 
 extern "C" int lin_prefill(const lin_shape *shape, int dtype, const lin_strides *strides, const void *q,
@@ -806,10 +830,12 @@ extern "C" int lin_prefill(const lin_shape *shape, int dtype, const lin_strides 
     if (misaligned(q, e) || misaligned(k, e) || misaligned(v, e) || misaligned(y, e) || misaligned(log_decay, 4) ||
         misaligned(slots, 4) || misaligned(states, 4) || misaligned(cu_seqlens, 4) || misaligned(carry, 4))
         return SSD_ERR_ALIGN;
-    const PrefillPlan P = plan_prefill(s, max_seqlen, ssd::device_cus());
-    if (workspace_bytes < P.total) return SSD_ERR_WORKSPACE;
-    if (P.total > 0 && !workspace) return SSD_ERR_NULL;
-    if (P.total > 0 && misaligned(workspace, 16)) return SSD_ERR_ALIGN;
+    const int cus = ssd::device_cus();
+    const PrefillPlan P = plan_prefill(s, dtype, max_seqlen, cus);
+    const size_t need = prefill_workspace(s, max_seqlen, cus);
+    if (workspace_bytes < need) return SSD_ERR_WORKSPACE;
+    if (need > 0 && !workspace) return SSD_ERR_NULL;
+    if (need > 0 && misaligned(workspace, 16)) return SSD_ERR_ALIGN;
     a.q = q;
     a.k = k;
     a.v = v;
