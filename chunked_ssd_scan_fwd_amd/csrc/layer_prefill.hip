@@ -7,9 +7,9 @@
 //
 // A block walks the chunks of one segment of a sequence for one head and VT
 // columns of v, with S in its registers: q, k, v are read once and y is
-// written once, and no chunk's state goes to memory.  Each wave owns 16
-// columns of S, of Y and of V and all dk rows of S, so S never crosses waves;
-// only the masked scores P = Q K^T o D do, through LDS.
+// written once, and no chunk's state goes to memory.  Each of the waves that
+// hold S owns 16 or 32 columns of S, of Y and of V and all dk rows of S, so S
+// never crosses waves; only the masked scores P = Q K^T o D do, through LDS.
 //
 // Sequences longer than the plan's segment are cut: one pass leaves the state
 // each segment makes from zero, a second pass joins them into the states that
@@ -137,10 +137,20 @@ __device__ __forceinline__ void frag_acc(Frag<float> &r, f32x4 a, f32x4 b)
 // sums do.  Two leave 2e-6 and save 5% of the last pass; the first pass over
 // a sequence that is cut takes two (53 against 68 us for 65536 rows of 8
 // heads), since what it makes decays over the segments that follow.
+// Two bf16 numbers by their bits, in a register: as an inline constant of the
+// dot product this compiler passed (-1, 0) the wrong way round.
+__device__ __forceinline__ bf16x2 pair_of(unsigned bits)
+{
+    asm("" : "+s"(bits));
+    return __builtin_bit_cast(bf16x2, bits);
+}
 template <int PARTS>
 __device__ __forceinline__ void weigh(Frag<bf16> (&fw)[3], const Frag<bf16> &fv, f32x4 wa, f32x4 wb)
 {
-    // pairs, so that two values are rounded by one instruction
+    // Pairs: two values are rounded by one instruction, and what is left of
+    // each is taken by one too, a dot product of the rounded pair with (-1, 0)
+    // or (0, -1).
+    const bf16x2 first = pair_of(0x0000bf80u), second = pair_of(0xbf800000u);
 #pragma unroll
     for (int e = 0; e < 8; e += 2) {
         f32x2 x = {(float)fv.x[e], (float)fv.x[e + 1]};
@@ -151,8 +161,10 @@ __device__ __forceinline__ void weigh(Frag<bf16> (&fw)[3], const Frag<bf16> &fv,
             const bf16x2 r = __builtin_convertvector(x, bf16x2);
             fw[u].x[e] = r[0];
             fw[u].x[e + 1] = r[1];
-            x[0] -= (float)r[0];
-            x[1] -= (float)r[1];
+            if (u + 1 < PARTS) {
+                x[0] = __builtin_amdgcn_fdot2_f32_bf16(r, first, x[0], false);
+                x[1] = __builtin_amdgcn_fdot2_f32_bf16(r, second, x[1], false);
+            }
         }
     }
 }
@@ -374,10 +386,10 @@ __device__ __forceinline__ bool find(const PrefillArgs &a, int id, Place &p)
 //
 // The block's first four waves hold S and make Y, 16 NT columns each; the
 // other four fetch the next chunks, write them to LDS and form the next
-// chunk's scores, so that neither waits for the other's loads.  Matrix and
-// vector instructions of a SIMD's waves did not overlap in time, so what
-// counts for the first four is instructions: Q, K and P, which every one of
-// them reads, are read once for NT column tiles.
+// chunk's scores, so that neither waits for the other's loads.  Vector
+// instructions ran beside matrix ones for a sixth of the matrix time only, so
+// what counts for the first four is instructions: Q, K and P, which every one
+// of them reads, are read once for NT column tiles.
 //
 // Every operand is read from LDS 16 bytes at a time, or transposed; pairs of
 // 8-byte reads ran at a quarter of that rate.  So that S can meet Q as it
@@ -533,6 +545,10 @@ __attribute__((amdgpu_waves_per_eu(2 * PerCu<E, KP, VT>::n, 2 * PerCu<E, KP, VT>
     }
 
     // ---- states and outputs
+    //
+    // Ahead of the others where both have something to issue: 435 us for the
+    // largest batch measured, 439 without and 474 the other way round.
+    __builtin_amdgcn_s_setprio(1);
     const int64_t state = (int64_t)a.dk * a.dv;
     float *pool = p.slot < 0 ? nullptr : a.states + ((int64_t)p.slot * a.H + h) * state;
     float *ends = p.segs > 1 ? a.ends + ((int64_t)id * a.H + h) * state : nullptr;
@@ -543,7 +559,12 @@ __attribute__((amdgpu_waves_per_eu(2 * PerCu<E, KP, VT>::n, 2 * PerCu<E, KP, VT>
     // then a lane's values of Y are 8 columns that follow one another.
     // Offsets step by constants from one lane's base; a row past dk lies past
     // the resource's end, and a column past the tile's is sent there.
+    //
+    // The registers hold S / scale: the chunks' decays gather in `scale`, which
+    // costs a factor of Y's instead of a multiplication of all of S, until it
+    // leaves 2^-16 .. 2^16.
     f32x4 S[MT][NT];
+    float scale = 1.f;
     const auto state_at = [&](int m, int n, int i) {
         const int col = w0 + (NT == 2 ? 8 * (l16 >> 2) + 4 * n + (l16 & 3) : l16);
         const uint32_t base = col < cols ? (uint32_t)(2 * g4 * a.dv + c0 + col) * 4u : kOOB;
@@ -587,21 +608,25 @@ __attribute__((amdgpu_waves_per_eu(2 * PerCu<E, KP, VT>::n, 2 * PerCu<E, KP, VT>
             }
 #pragma unroll
             for (int t = 0; t < TT; ++t) {
-                const float e = d.in[16 * t + l16];
+                const float e = d.in[16 * t + l16] * scale;
 #pragma unroll
                 for (int n = 0; n < NT; ++n) Y[n][t] *= e;
             }
         }
-        const float all = d.all;
+        scale = __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(scale * d.all)));
+        if (!(scale > 0x1p-16f && scale < 0x1p16f)) {   // and where it is NaN
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+            for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int n = 0; n < NT; ++n) S[m][n] *= all;
+                for (int n = 0; n < NT; ++n) S[m][n] *= scale;
+            scale = 1.f;
+        }
+        const float unscale = 1.f / scale;
         const auto rows32 = [&](auto step) {   // 32 rows of the chunk
             constexpr int s = decltype(step)::value, PARTS = sizeof(L) == 4 ? 1 : OUT ? 3 : 2;
             Frag<L> fv[NT], fw[NT][3];
-            const f32x4 wa = *reinterpret_cast<const f32x4 *>(d.out + 32 * s + g4);
-            const f32x4 wb = *reinterpret_cast<const f32x4 *>(d.out + 32 * s + 16 + g4);
+            const f32x4 wa = *reinterpret_cast<const f32x4 *>(d.out + 32 * s + g4) * unscale;
+            const f32x4 wb = *reinterpret_cast<const f32x4 *>(d.out + 32 * s + 16 + g4) * unscale;
 #pragma unroll
             for (int n = 0; n < NT; ++n) fv[n] = frag_col<LV, NT == 2>(vs + 32 * s * LV, w0 + 4 * n, lane);
             if (OUT) {
@@ -671,7 +696,7 @@ __attribute__((amdgpu_waves_per_eu(2 * PerCu<E, KP, VT>::n, 2 * PerCu<E, KP, VT>
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) ssd::gstore1(r, state_at(m, n, i), S[m][n][i]);
+            for (int i = 0; i < 4; ++i) ssd::gstore1(r, state_at(m, n, i), S[m][n][i] * scale);
     if (!OUT && tile == 0 && threadIdx.x == 0) a.segdec[(int64_t)id * a.H + h] = expf((float)total);
 }
 
