@@ -109,6 +109,8 @@ def _is(t, name, shape, dtype, device):
     """`t` is a tensor of this shape (a tuple) and type, on HIP device `device` (its number)."""
     if not isinstance(t, _torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype == dtype and t.shape == shape and t.get_device() == device:
+        return
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
@@ -127,9 +129,10 @@ def _dense(t, name, shape, dtype, device):
 def _rows(t, name):
     """Strides of a [rows, heads, d] tensor whose last axis is dense."""
     a, b, c = t.stride()
-    if c != 1 and t.shape[2] > 1:
+    n, h, d = t.shape
+    if c != 1 and d > 1:
         raise ValueError(f"the last axis of {name} must be dense")
-    return (a if t.shape[0] > 1 else 0), (b if t.shape[1] > 1 else 0)
+    return (a if n > 1 else 0), (b if h > 1 else 0)
 
 
 def _ids(t, name, n, device):
@@ -185,7 +188,7 @@ def _lin_args(q, k, v, log_decay, states, out, rows_name):
     if H > 1 and log_decay.stride(-1) != 1:
         raise ValueError("the last axis of log_decay must be dense")
     if out is None:
-        out = _torch.empty((R, H, dv), dtype=dt, device=v.device)
+        out = v.new_empty((R, H, dv))
         st = (H * dv, dv)
     else:
         _is(out, "out", (R, H, dv), dt, dev)
@@ -247,8 +250,10 @@ def lin_step(q, k, v, log_decay, states, *, slots=None, out=None):
 
 
 def _gn_rows(t, name, shape, dtype, device):
-    """Pointer and row stride of x, gate or dy, [N,L,C] or [N,C]."""
+    """Pointer and row stride (0: dense) of x, gate or dy, [N,L,C] or [N,C]."""
     _is(t, name, shape, dtype, device)
+    if t.is_contiguous():
+        return t.data_ptr() or None, 0
     if shape[-1] > 1 and t.stride(-1) != 1:
         raise ValueError(f"the last axis of {name} must be dense")
     if len(shape) == 2:
@@ -307,15 +312,21 @@ def gn_fwd(x, weight, bias, groups, *, gate=None, act="silu", eps=1e-5, out=None
     code, dev, shape, s, xp, ldx, wp, bp, gp, ldg = _gn_args(x, weight, bias, groups, gate)
     if not eps >= 0:
         raise ValueError("eps must not be negative")
+    act = _act(act)
+    st_shape = (s[0], s[3], 2)
     if out is None:
-        out = _torch.empty(shape, dtype=x.dtype, device=x.device)
+        out = x.new_empty(shape)
+        op = out.data_ptr() or None
+    else:
+        op = _dense(out, "out", shape, x.dtype, dev)
     if stats is None:
-        stats = _torch.empty((s[0], s[3], 2), dtype=_torch.float32, device=x.device)
-    op = _dense(out, "out", shape, x.dtype, dev)
-    stp = _dense(stats, "stats", (s[0], s[3], 2), _torch.float32, dev)
+        stats = x.new_empty(st_shape, dtype=_torch.float32)
+        stp = stats.data_ptr() or None
+    else:
+        stp = _dense(stats, "stats", st_shape, _torch.float32, dev)
     ref = _arg(GnShapeArg, *s)
     wsp, wsn, _keep = _bytes(lib.gn_fwd_workspace_size(ref), dev, workspace)
-    _call(lib.gn_fwd, "gn_fwd", dev, ref, code, _act(act), eps, xp, ldx, wp, bp, gp, ldg, op, stp, wsp, wsn)
+    _call(lib.gn_fwd, "gn_fwd", dev, ref, code, act, eps, xp, ldx, wp, bp, gp, ldg, op, stp, wsp, wsn)
     return out, stats
 
 
@@ -325,21 +336,24 @@ def gn_bwd(x, weight, bias, groups, stats, dy, *, gate=None, act="silu", out=Non
     gate.  ``out``: the four (or, without a gate, three) tensors to write."""
     lib = _lib()
     code, dev, shape, s, xp, ldx, wp, bp, gp, ldg = _gn_args(x, weight, bias, groups, gate)
+    act = _act(act)
     dyp, ldy = _gn_rows(dy, "dy", shape, x.dtype, dev)
     stp = _dense(stats, "stats", (s[0], s[3], 2), _torch.float32, dev)
+    C = s[2]
     if out is None:
-        dx = _torch.empty(shape, dtype=x.dtype, device=x.device)
-        dw, db = (_torch.empty(s[2], dtype=_torch.float32, device=x.device) for _ in range(2))
-        dg = None if gate is None else _torch.empty(shape, dtype=x.dtype, device=x.device)
+        dx = x.new_empty(shape)
+        dg = None if gate is None else x.new_empty(shape)
+        dw, db = x.new_empty((2, C), dtype=_torch.float32).unbind()
+        dxp, dwp, dgp = dx.data_ptr() or None, dw.data_ptr(), None if dg is None else dg.data_ptr() or None
+        dbp = dwp + 4 * C
     else:
         dx, dw, db, dg = tuple(out) if gate is not None else (*tuple(out)[:3], None)
-    dxp = _dense(dx, "dx", shape, x.dtype, dev)
-    dwp, dbp = (_dense(t, n, (s[2],), _torch.float32, dev) for t, n in ((dw, "dweight"), (db, "dbias")))
-    dgp = None if dg is None else _dense(dg, "dgate", shape, x.dtype, dev)
+        dxp = _dense(dx, "dx", shape, x.dtype, dev)
+        dwp, dbp = _dense(dw, "dweight", (C,), _torch.float32, dev), _dense(db, "dbias", (C,), _torch.float32, dev)
+        dgp = None if dg is None else _dense(dg, "dgate", shape, x.dtype, dev)
     ref = _arg(GnShapeArg, *s)
     wsp, wsn, _keep = _bytes(lib.gn_bwd_workspace_size(ref), dev, workspace)
-    _call(lib.gn_bwd, "gn_bwd", dev, ref, code, _act(act), xp, ldx, wp, bp, gp, ldg, stp, dyp, ldy, dxp, dwp,
-          dbp, dgp, wsp, wsn)
+    _call(lib.gn_bwd, "gn_bwd", dev, ref, code, act, xp, ldx, wp, bp, gp, ldg, stp, dyp, ldy, dxp, dwp, dbp, dgp, wsp, wsn)
     return dx, dw, db, dg
 
 
