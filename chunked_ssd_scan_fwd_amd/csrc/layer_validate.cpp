@@ -17,7 +17,7 @@ int check_lin(const lin_shape *s, bool step)
     if (s->H % s->G != 0) return SSD_ERR_SHAPE;
     if (s->dk > kMaxHeadDim || s->dv > kMaxHeadDim) return SSD_ERR_UNSUPPORTED;
     if (s->N >= kMaxCount || s->slots >= kMaxCount || s->H >= 65536) return SSD_ERR_SHAPE;
-    if (!step && s->T >= (int64_t(1) << 31)) return SSD_ERR_SHAPE;
+    if (!step && s->T >= (int64_t(1) << 30)) return SSD_ERR_SHAPE;
     // a block for each row (or sequence), head and column tile
     const int64_t tiles = (s->dv + 31) / 32;
     if (s->N > max_blocks(512) / (s->H * tiles)) return SSD_ERR_SHAPE;
@@ -48,7 +48,7 @@ int check_gn(const gn_shape *s, int act)
     if (s->N < 0 || s->L < 0 || s->C < 1 || s->groups < 1 || s->C % s->groups != 0) return SSD_ERR_SHAPE;
     if (act != GN_ACT_NONE && act != GN_ACT_SILU) return SSD_ERR_UNSUPPORTED;
     const int64_t lim = int64_t(1) << 40;
-    if (s->C >= kMaxCount || s->L >= (int64_t(1) << 31) || s->N > lim) return SSD_ERR_SHAPE;
+    if (s->C >= kMaxCount || s->L >= (int64_t(1) << 30) || s->N > lim) return SSD_ERR_SHAPE;
     if (s->N > lim / (s->L + 1) || s->N * (s->L + 1) > lim / s->C) return SSD_ERR_SHAPE;
     return SSD_OK;
 }

@@ -413,7 +413,7 @@ size_t lin_prefill_workspace_size(const lin_shape *shape, int64_t max_seqlen);
  * Infinite and NaN values of a sequence's rows stay within that sequence,
  * and reach rows up to 63 positions before their own.
  * dk, dv in 1..256 (else SSD_ERR_UNSUPPORTED), G >= 1, H % G == 0,
- * T < 2^31, N and slots < 2^24, N H ceil(dv / 32) < 2^23, row strides below
+ * T < 2^30, N and slots < 2^24, N H ceil(dv / 32) < 2^23, row strides below
  * 2^24 elements, and strides of y that let no two of its values overlap (else
  * SSD_ERR_SHAPE). */
 int lin_prefill(const lin_shape *shape, int dtype, const lin_strides *strides,
@@ -445,7 +445,7 @@ int lin_step(const lin_shape *shape, int dtype, const lin_strides *strides,
  * (1 and 0).  stats [N][groups][2] receives mu and rstd.
  * Row n L + l of x, gate, dy starts ld_* elements after the row before it
  * (0: C); y, dx and dgate are dense.  C % groups == 0; N L C < 2^40, C and
- * the strides below 2^24, L < 2^31. */
+ * the strides below 2^24, L < 2^30. */
 typedef struct gn_shape {
     int64_t N, L, C, groups;
 } gn_shape;

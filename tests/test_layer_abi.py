@@ -60,7 +60,7 @@ def test_lin_arguments_refused():
     s = LinShapeArg(5, 2, 1, 4, 8, 8, 4)
     big = 1 << 24
     assert lin(LinShapeArg(-1, 2, 1, 4, 8, 8, 4)) == SHAPE
-    assert lin(LinShapeArg(1 << 31, 2, 1, 4, 8, 8, 4)) == SHAPE
+    assert lin(LinShapeArg(1 << 30, 2, 1, 4, 8, 8, 4)) == SHAPE
     assert lin(s, max_len=-1) == SHAPE
     for step in (False, True):
         assert lin(s, step, dtype=3) == UNSUPPORTED and lin(s, step, dtype=-1) == UNSUPPORTED
@@ -115,7 +115,7 @@ def gn(shape, bwd=False, dtype=1, act=1, eps=1e-5, ptr=P, ws=(P, 1 << 40), ld=(0
 def test_gn_arguments_refused(bwd):
     s = GnShapeArg(3, 4, 12, 3)
     for bad in ((3, 4, 12, 5), (3, 4, 12, 0), (-1, 4, 12, 3), (3, -1, 12, 3), (3, 4, 0, 3), (3, 4, 1 << 24, 1),
-                (3, 1 << 31, 12, 3), (1 << 40, 1 << 20, 12, 3)):
+                (3, 1 << 30, 12, 3), (1 << 40, 1 << 20, 12, 3)):
         assert gn(GnShapeArg(*bad), bwd) == SHAPE, bad
     assert gn(s, bwd, dtype=7) == UNSUPPORTED and gn(s, bwd, act=2) == UNSUPPORTED
     assert gn(s, bwd, ld=(-1, 0, 0)) == SHAPE and gn(s, bwd, ld=(0, 1 << 24, 0)) == SHAPE
