@@ -89,6 +89,52 @@ def test_prefill_slices_of_a_projection(heads, dtype):
     check_prefill("strides", heads, dtype, [70, 0, 100], strided=True, seed=3)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF, F16])
+@pytest.mark.parametrize("layout", ["aligned projection", "heads first", "one row repeated", "one group repeated",
+                                    "states off 16 bytes", "everything off by one"])
+def test_prefill_and_step_layouts(layout, dtype):
+    """Strides and addresses that a caller may hand in, whole and cut."""
+    for heads, lens in (((2, 4, 64, 48), [70, 0, 33]), ((1, 2, 128, 128), [600])):
+        G, H, dk, dv = heads
+        T, N = sum(lens), len(lens)
+        q, k, v, ld, S = (dev(t) for t in ref.inputs(T, G, H, dk, dv, dtype, True, 11, N))
+        out = torch.full((T, H, dv), 7.0, dtype=dtype, device="cuda")
+        pool = S.clone()
+        if layout == "aligned projection":
+            p = torch.cat([q.flatten(1), k.flatten(1), v.flatten(1), torch.full((T, 8), NAN, dtype=dtype, device="cuda")], 1)
+            q, k, v, _ = p.split([G * dk, G * dk, H * dv, 8], 1)
+            q, k, v = q.unflatten(1, (G, dk)), k.unflatten(1, (G, dk)), v.unflatten(1, (H, dv))
+        elif layout == "heads first":
+            q, k, v, out = (t.transpose(0, 1).contiguous().transpose(0, 1) for t in (q, k, v, out))
+        elif layout == "one row repeated":
+            k, ld = k[:1].expand(T, G, dk), ld[:1].expand(T, H)
+        elif layout == "one group repeated":
+            q = q[:, :1].expand(T, G, dk)
+        elif layout == "states off 16 bytes":
+            pool = torch.empty(S.numel() + 1, device="cuda")[1:].view(S.shape).copy_(S)
+        else:
+            def off(t):
+                r = torch.empty(t.numel() + 1, dtype=t.dtype, device="cuda")[1:].view(t.shape)
+                return r.copy_(t)
+            q, k, v, ld, out, pool = (off(t) for t in (q, k, v, ld, out, pool))
+        say(f"layout {layout} {heads} {dtype}")
+        want, S1, ya, Sa = ref.scan(q, k, v, ld, offsets(lens), S)
+        y = ssd.lin_prefill(q, k, v, ld, ids(offsets(lens)), pool, out=out)
+        ref.within(y, want, ref.y_bound(dtype, want, ya))
+        ref.within(pool, S1, ref.state_bound(Sa))
+        rows = min(T, N)
+        before = pool.clone()
+        y = ssd.lin_step(q[:rows], k[:rows], v[:rows], ld[:rows], pool, out=out[:rows])
+        want, S1, ya, Sa = ref.scan(q[:rows], k[:rows], v[:rows], ld[:rows], list(range(rows + 1)), before)
+        ref.within(y, want, ref.HALF[dtype] * want.abs() + 2e-5 * ya + (2.0 ** -25 if dtype == F16 else 0) + 1e-30)
+        ref.within(pool, S1, ref.state_bound(Sa))
+
+
+@pytest.mark.parametrize("heads,dtype", [((1, 1, 256, 130), BF), ((1, 2, 96, 200), F16), ((1, 1, 33, 17), F32), ((2, 2, 64, 64), BF)])
+def test_prefill_cut_at_other_heads(heads, dtype):
+    check_prefill("cut", heads, dtype, [1500, 700], carry=[0, 1], slots=[2, 0], npool=3, tail=2, seed=13)
+
+
 @pytest.mark.parametrize("dtype", [F32, BF])
 @pytest.mark.parametrize("lens,max_seqlen", [([4500], 0), ([4500], 4500), ([3000, 17, 0, 1400], 0), ([2500], 5)])
 def test_prefill_long(lens, max_seqlen, dtype):
@@ -689,6 +735,39 @@ def test_two_graphs_on_a_side_stream():
             torch.cuda.synchronize()
             for a, b in zip(out + [pool], want + [p2]):
                 assert torch.equal(a, b)
+
+
+def test_two_streams_at_once():
+    """The same calls on two streams, each with its own data, not ordered against each other."""
+    sets = [layer_data(s, 3000) for s in (5, 6)]
+    want = []
+    for d in sets:
+        pool, (cache, scales) = d["S"].clone(), cache_of(2, 2, 64, 64)
+        want.append(layer_pass(d, pool, cache, scales, {"prefill": None}) + [pool])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    got = []
+    for d, st in zip(sets, streams):
+        with torch.cuda.stream(st):
+            for _ in range(3):
+                pool, (cache, scales) = d["S"].clone(), cache_of(2, 2, 64, 64)
+                out = layer_pass(d, pool, cache, scales, {"prefill": None}) + [pool]
+        got.append(out)
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_cache_off_16_bytes():
+    S = torch.randn(3, 2, 8, 64, generator=torch.Generator().manual_seed(1))
+    pool = torch.empty(S.numel() + 1, device="cuda")[1:].view(S.shape).copy_(S)
+    raw = torch.zeros(S.numel() + 3, dtype=torch.uint8, device="cuda")[3:].view(S.shape)
+    cache, scales = raw.view(torch.float8_e4m3fn), torch.zeros(3, 2, 8, 2, dtype=torch.uint8, device="cuda")
+    ssd.state_pack(pool, cache, scales)
+    code, sc = ref.pack(S.numpy())
+    assert np.array_equal(raw.cpu().numpy(), code) and np.array_equal(scales.cpu().numpy(), sc)
+    ssd.state_unpack(cache, scales, pool)
+    assert np.array_equal(pool.cpu().double().numpy(), ref.unpack(code, sc))
 
 
 def test_binding_refuses():
