@@ -134,9 +134,10 @@ __device__ __forceinline__ void frag_acc(Frag<float> &r, f32x4 a, f32x4 b)
 // V's rows times e^{b_L - b} (wa, wb: the fragment's first and last four
 // rows), in PARTS summands.  float32 takes one.  Three bf16 numbers hold what
 // a float32 product does: states came out within 2e-7 of 64 bits, as float32
-// sums do.  Two leave 2e-6 and save 5% of the last pass; the first pass over
-// a sequence that is cut takes two (53 against 68 us for 65536 rows of 8
-// heads), since what it makes decays over the segments that follow.
+// sums do.  Two leave 2e-6 and save a tenth of the last pass where it is bound
+// by issue (91 against 102 us for 65536 rows of 8 heads); the first pass over
+// a sequence that is cut takes two (55 against 69 us), since what it makes
+// decays over the segments that follow.
 // Two bf16 numbers by their bits, in a register: as an inline constant of the
 // dot product this compiler passed (-1, 0) the wrong way round.
 __device__ __forceinline__ bf16x2 pair_of(unsigned bits)
@@ -409,9 +410,10 @@ struct ChunkLds {
 
 // Blocks that share a CU.  With 64 columns and 32-row chunks two of them fit
 // its LDS and registers, and fill each other's waits: 20 mixed prompts of 24
-// heads of 128 x 64 took 48 us so, 64 with one and 64-row chunks.  With 128
-// columns one with 64-row chunks did as well as two with 32 (114 us for 65536
-// rows of 8 heads), and better where there is one block for each CU.
+// heads of 128 x 64 took 44 us so, 59 with one and 64-row chunks.  Heads of
+// 128 columns are faster as one block of them with 64-row chunks than as two
+// blocks of 64 with 32-row ones (102 against 121 us for the last pass over
+// 65536 rows of 8 heads, 439 against 520 for 16 prompts of 8192 and 16 heads).
 template <typename E, int KP, int VT>
 struct PerCu {
     static constexpr int n = VT == 64 && KP <= 128 && std::is_same<E, bf16>::value ? 2 : 1;
@@ -546,8 +548,8 @@ __attribute__((amdgpu_waves_per_eu(2 * PerCu<E, KP, VT>::n, 2 * PerCu<E, KP, VT>
 
     // ---- states and outputs
     //
-    // Ahead of the others where both have something to issue: 435 us for the
-    // largest batch measured, 439 without and 474 the other way round.
+    // Ahead of the others where both have something to issue: 486 us on
+    // average for the largest batch measured, 497 without.
     __builtin_amdgcn_s_setprio(1);
     const int64_t state = (int64_t)a.dk * a.dv;
     float *pool = p.slot < 0 ? nullptr : a.states + ((int64_t)p.slot * a.H + h) * state;
@@ -754,8 +756,8 @@ static int col_tile(int64_t dk, int64_t dv) { return dk > 128 || dv <= 64 ? 64 :
 // rows, at least 128 rows.  Cutting runs a second pass over k and v and a
 // third over the segments' states, so while the longest sequence is not twice
 // what a CU's share of the rows is, all stay whole: 20 prompts whose longest
-// was 1.1 shares took 64 us whole and 96 us cut; one of 32 shares takes 178 us
-// cut and 3.4 ms whole.
+// was 1.1 shares took 44 us whole and 82 us cut; one of 32 shares takes 162 us
+// cut and 2.3 ms whole.
 static PrefillPlan plan_prefill(const lin_shape &s, int dtype, int64_t max_seqlen, int cus)
 {
     PrefillPlan P;
