@@ -37,6 +37,7 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int CT = 256;   // threads of a block of the carry pass
+constexpr int SORTED = 512, KEY = 10;   // most sequences that are put in order, by as many bits of their lengths
 
 struct PrefillArgs {
     const void *q, *k, *v;
@@ -49,6 +50,7 @@ struct PrefillArgs {
     int T, N, G, H, dk, dv, nslots, tiles;
     int seg;       // rows of a segment; 0: sequences are not cut
     int ids;       // blocks' segment numbers, T / seg + N
+    int shift;     // lengths >> shift order the segments; -1: as they come
 };
 
 // ---- fragments of the matrix products
@@ -354,30 +356,106 @@ __device__ __forceinline__ void about(const PrefillArgs &a, int n, Place &p, int
     p.segs = a.seg == 0 ? 1 : max(1, (end - begin + a.seg - 1) / a.seg);
 }
 
-// Segment number `id`.  Sequence n has the numbers from begin / seg + n on;
-// there are at least as many up to the next sequence's first as it has
-// segments, and the ones left over have none.  All 64 lanes look at
-// sequences, so a batch of 64 takes one load's latency.
-__device__ __forceinline__ bool find(const PrefillArgs &a, int id, Place &p)
+// Segment number r in the order of falling lengths, for every wave by itself:
+// the whole ones (of a.seg rows) by their sequence, then each sequence's rest,
+// or the sequence where none is cut, by KEY bits of its length from `shift`
+// on, equal ones as they come.  An empty sequence counts as a rest.  False:
+// there are no more.
+__device__ __forceinline__ bool by_length(const PrefillArgs &a, int r, int &n, int &s)
 {
-    int n = id;
-    if (a.seg > 0) {
+    constexpr int U = SORTED / 64;
+    const int lane = threadIdx.x & 63;
+    int key[U];
+    bool have = false;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        key[u] = -1;
+        if (64 * u >= a.N) continue;
+        const int j = 64 * u + lane;
+        int b, e;
+        rows_of(a, min(j, a.N - 1), b, e);
+        const int len = j < a.N ? e - b : 0, whole = a.seg > 0 ? len / a.seg : 0, rest = len - whole * a.seg;
+        if (j < a.N && (rest > 0 || len == 0)) key[u] = min(rest >> a.shift, (1 << KEY) - 1);
+        if (a.seg > 0 && !have) {
+            int sum = whole;   // of the lanes up to this one
+            for (int d = 1; d < 64; d *= 2) {
+                const int x = __shfl_up(sum, d);
+                if (lane >= d) sum += x;
+            }
+            const unsigned long long m = __ballot(sum > r);
+            if (m != 0) {
+                const int at = __ffsll(m) - 1;
+                n = 64 * u + at;
+                s = r - __builtin_amdgcn_readlane(sum - whole, at);
+                have = true;
+            } else {
+                r -= __builtin_amdgcn_readlane(sum, 63);
+            }
+        }
+    }
+    if (have) return true;
+    // bit by bit, the r-th largest key
+    int found = 0;
+    for (int bit = KEY - 1; bit >= 0; --bit) {
+        const int want = found >> bit | 1;
+        int c = 0;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (64 * u < a.N) c += __popcll(__ballot(key[u] >> bit == want));
+        if (r < c)
+            found = want << bit;
+        else
+            r -= c;
+    }
+    // and the sequence among those that have it
+    n = -1;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        if (64 * u < a.N) {
+            const unsigned long long m = __ballot(key[u] == found);
+            const int before = __builtin_amdgcn_mbcnt_hi((unsigned)(m >> 32), __builtin_amdgcn_mbcnt_lo((unsigned)m, 0));
+            const unsigned long long hit = __ballot(key[u] == found && before == r);
+            if (hit != 0) n = 64 * u + __ffsll(hit) - 1;
+            r -= __popcll(m);
+        }
+    s = -1;   // the last
+    return n >= 0;
+}
+
+// Where block number `id` works, and the number of its segment in its place.
+// Sequence n's segments have the numbers from begin / seg + n on; there are at
+// least as many up to the next sequence's first as it has segments, and the
+// ones left over have none.  All 64 lanes look at sequences, so a batch of 64
+// takes one load's latency.
+__device__ __forceinline__ bool find(const PrefillArgs &a, int &id, Place &p)
+{
+    int n = id, s = 0;
+    if (a.shift >= 0) {
+        if (!by_length(a, id, n, s)) return false;
+    } else if (a.seg > 0) {
         n = -1;
         for (int j0 = 0; j0 < a.N; j0 += 64) {
             const int j = j0 + (int)(threadIdx.x & 63);
             int b = 0, e = 0;
             if (j < a.N) rows_of(a, j, b, e);
-            const int s = id - (b / a.seg + j);
-            const unsigned long long m = __ballot(j < a.N && s >= 0 && (s == 0 || s * (int64_t)a.seg < e - b));
+            const int t = id - (b / a.seg + j);
+            const unsigned long long m = __ballot(j < a.N && t >= 0 && (t == 0 || t * (int64_t)a.seg < e - b));
             if (m != 0 && n < 0) n = j0 + __ffsll(m) - 1;
         }
         if (n < 0) return false;
     }
     int begin, end;
     about(a, n, p, begin, end);
-    p.s = a.seg == 0 ? 0 : id - (begin / a.seg + n);
-    p.begin = begin + p.s * a.seg;
-    p.rows = a.seg == 0 ? end - begin : min(a.seg, end - p.begin);
+    p.s = 0;
+    p.begin = begin;
+    p.rows = end - begin;
+    if (a.seg > 0) {
+        const int first = begin / a.seg + n;
+        p.s = a.shift < 0 ? id - first : s < 0 ? p.segs - 1 : s;
+        id = first + p.s;
+        p.begin += p.s * a.seg;
+        p.rows = min(a.seg, end - p.begin);
+    }
     return true;
 }
 
@@ -433,7 +511,8 @@ __attribute__((amdgpu_waves_per_eu(2 * PerCu<E, KP, VT>::n, 2 * PerCu<E, KP, VT>
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int l16 = lane & 15, g4 = (lane >> 4) * 4;
-    const int tile = blockIdx.x % a.tiles, h = blockIdx.x / a.tiles % a.H, id = blockIdx.x / (a.tiles * a.H);
+    const int tile = blockIdx.x % a.tiles, h = blockIdx.x / a.tiles % a.H;
+    int id = blockIdx.x / (a.tiles * a.H);
     Place p;
     if (!find(a, id, p)) return;
     if (!OUT && p.s + 1 >= p.segs) return;   // nothing follows the last segment
@@ -751,13 +830,16 @@ struct PrefillPlan {
 
 static int col_tile(int64_t dk, int64_t dv) { return dk > 128 || dv <= 64 ? 64 : 128; }
 
-// Sequences are cut where whole ones would leave CUs idle: into segments of a
+// Sequences are cut where that is faster by an estimate: into segments of a
 // length that makes about one block for each place on a CU out of the batch's
-// rows, at least 128 rows.  Cutting runs a second pass over k and v and a
-// third over the segments' states, so while the longest sequence is not twice
-// what a CU's share of the rows is, all stay whole: 20 prompts whose longest
-// was 1.1 shares took 44 us whole and 82 us cut; one of 32 shares takes 162 us
-// cut and 2.3 ms whole.
+// rows, at least 128 rows.  Whole, the longest one's chain of chunks counts.
+// Cut, a segment's two passes count for twice its rows, with 7 us for the two
+// launches more and the time to write, carry and read the segments' states.
+// A row takes 37 ns in bf16, 30 and 1 more for 128 values of a state on fp32
+// MFMA.  Measured whole and cut, in us: one prompt of 384 rows 20 and 23, of
+// 768 34 and 23, of 65536 2350 and 158 (8 heads of 128); mixed prompts, 30 of
+// up to 1004 rows 49 and 69 (the same heads), 8 of up to 4526 171 and 121, 8 of
+// 8192 326 and 352 (16 heads).
 static PrefillPlan plan_prefill(const lin_shape &s, int dtype, int64_t max_seqlen, int cus)
 {
     PrefillPlan P;
@@ -765,16 +847,19 @@ static PrefillPlan plan_prefill(const lin_shape &s, int dtype, int64_t max_seqle
     const int64_t vt = col_tile(s.dk, s.dv), tiles = (s.dv + vt - 1) / vt;
     const int64_t per_cu = vt == 64 && s.dk <= 128 && dtype == LAYER_BF16 ? 2 : 1;   // PerCu
     const int64_t work = s.T * s.H * tiles;
-    const auto share = [&](int64_t places) { return (work + places - 1) / places; };
-    int64_t seg = (share(per_cu * cus) + 63) / 64 * 64;
+    const int64_t places = per_cu * cus;
+    int64_t seg = ((work + places - 1) / places + 63) / 64 * 64;
     if (seg < 128) seg = 128;
     P.ids = (int)s.N;
-    if (longest <= 2 * seg || longest <= 2 * share(cus)) return P;
+    const double state = (double)s.H * (double)(s.dk * s.dv);
+    const double row = dtype == LAYER_BF16 ? 37.0 : 30.0 + (double)(s.dk * (s.dv < vt ? s.dv : vt)) / 128.0;
+    const double cut = 2.0 * row * (double)seg + 7000.0 + (double)(s.T / seg + s.N) * state * 16.0 / 4500.0;
+    if (longest <= seg || row * (double)longest <= cut) return P;
     // and no more of them than a launch has blocks for
     const int64_t most = max_blocks(512) / (s.H * tiles) - s.N;
     if (most < 1) return P;
     if (s.T / seg > most) seg = (s.T / most + 64) / 64 * 64;
-    if (longest <= 2 * seg || seg >= (int64_t(1) << 30)) return P;
+    if (longest <= seg || seg >= (int64_t(1) << 30)) return P;
     P.seg = (int)seg;
     P.ids = (int)(s.T / seg + s.N);
     size_t o = 0;
@@ -785,6 +870,24 @@ static PrefillPlan plan_prefill(const lin_shape &s, int dtype, int64_t max_seqle
     o += (size_t)P.ids * s.H * sizeof(float);
     P.total = (o + 255) / 256 * 256;
     return P;
+}
+
+// Segments start in the order of falling lengths, so that the long ones have
+// company that ends early and none is left to the end: 40 mixed prompts of 24
+// heads of 128 x 64 took 79 us so and 98 as they came, 60 of 8 heads of 128 74
+// and 85, 16 that are cut of 16 such heads 210 and 266.  Not where each block
+// has a CU for itself: finding a place in the order takes a block two
+// dependent loads for one (20 equal prompts of 24 heads: 35 us and 33).  Nor
+// for more than SORTED sequences, where the order is slow to find and any one
+// of them is a small part.
+static int order_shift(const lin_shape &s, const PrefillPlan &P, int64_t max_seqlen, int64_t blocks, int cus)
+{
+    if (s.N < 2 || s.N > SORTED || blocks <= cus) return -1;
+    const int64_t most = max_seqlen > 0 && max_seqlen < s.T ? max_seqlen : s.T;
+    const int64_t longest = P.seg > 0 ? P.seg : most;
+    int shift = 0;
+    while (longest >> shift >= 1 << KEY) ++shift;
+    return shift;
 }
 
 // The workspace for any element type.
@@ -886,6 +989,7 @@ extern "C" int lin_prefill(const lin_shape *shape, int dtype, const lin_strides 
     a.tiles = (a.dv + vt - 1) / vt;
     a.seg = P.seg;
     a.ids = P.ids;
+    a.shift = order_shift(s, P, max_seqlen, (int64_t)a.ids * a.H * a.tiles, cus);
     // 16 bytes at a time where every row of every head begins on 16 bytes and
     // holds a whole number of them
     const auto rows16 = [&](const void *ptr, int64_t row, int64_t head, int64_t d) {

@@ -135,6 +135,26 @@ def test_prefill_cut_at_other_heads(heads, dtype):
     check_prefill("cut", heads, dtype, [1500, 700], carry=[0, 1], slots=[2, 0], npool=3, tail=2, seed=13)
 
 
+@pytest.mark.parametrize("n", [2, 63, 65, 511, 512, 513])
+@pytest.mark.parametrize("longest,hint", [(40, 40), (40, 1), (1700, 0)])
+def test_prefill_many_ragged(n, longest, hint):
+    """More blocks than the card has CUs, of lengths with gaps and ties, around the number of sequences that are
+    put in order; whole (with a bound of the lengths, or one that is too low) and cut."""
+    H = 8 if n > 40 else 160
+    w = torch.rand(n, generator=torch.Generator().manual_seed(n)) ** 6
+    lens = (w * 40).long().tolist()
+    lens[n // 2], lens[n - 1] = longest, 640 if longest > 40 else 0
+    got, pool = check_prefill("ragged", (2, H, 16, 8), BF, lens, carry=[i % 3 for i in range(n)],
+                              slots=[(i * 7 + 3) % n if n % 7 else i for i in range(n)], max_seqlen=hint, seed=n, tail=1)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF, F16])
+@pytest.mark.parametrize("lens", [[256, 128, 0, 1024, 384], [640, 640, 512], [0, 1300, 0, 0, 1]])
+def test_prefill_segments_that_end_with_the_sequence(lens, dtype):
+    """Lengths that are multiples of a segment's: no rest."""
+    check_prefill("whole segments", (4, 64, 32, 32), dtype, lens, max_seqlen=0, seed=3, carry=[i % 2 for i in range(len(lens))])
+
+
 @pytest.mark.parametrize("dtype", [F32, BF])
 @pytest.mark.parametrize("lens,max_seqlen", [([4500], 0), ([4500], 4500), ([3000, 17, 0, 1400], 0), ([2500], 5)])
 def test_prefill_long(lens, max_seqlen, dtype):
