@@ -581,8 +581,7 @@ __global__ __launch_bounds__(GT) void k_gn_apply(GnArgs a)
 // Statistics of samples without rows.
 __global__ void k_gn_zero(float *p, int64_t n)
 {
-    const int64_t i = (int64_t)blockIdx.x * GT + threadIdx.x;
-    if (i < n) p[i] = 0.f;
+    for (int64_t i = (int64_t)blockIdx.x * GT + threadIdx.x; i < n; i += (int64_t)gridDim.x * GT) p[i] = 0.f;
 }
 
 // ---- host side
@@ -812,7 +811,8 @@ extern "C" int gn_fwd(const gn_shape *shape, int dtype, int act, float eps, cons
     hipStream_t st = static_cast<hipStream_t>(stream);
     if (s.L == 0) {
         const int64_t n = 2 * s.N * s.groups;
-        k_gn_zero<<<dim3((unsigned)((n + GT - 1) / GT)), dim3(GT), 0, st>>>(stats, n);
+        const int64_t blocks = (n + GT - 1) / GT, most = max_blocks(GT);
+        k_gn_zero<<<dim3((unsigned)(blocks < most ? blocks : most)), dim3(GT), 0, st>>>(stats, n);
         return launch_status();
     }
     a.x = x;

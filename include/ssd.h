@@ -390,7 +390,8 @@ size_t lin_prefill_workspace_size(const lin_shape *shape, int64_t max_seqlen);
 
 /* The scan of a packed batch.  Sequence n is rows cu_seqlens[n] ..
  * cu_seqlens[n+1]-1 (int32 [N+1], rising, within 0..T; other values give
- * unspecified results, but no row outside 0..T is touched); rows of no sequence are not read, and their y is left as it was.
+ * unspecified results, but no row outside 0..T is touched); rows of no
+ * sequence are not read, and their y is left as it was.
  * For each sequence and head h, with g = h / (H/G),
  *     S_t = exp(log_decay_t) S_{t-1} + k_t v_t^T,   y_t = S_t^T q_t,
  * in chunks, from the state in slot slots[n] of `states` [slots][H][dk][dv]
