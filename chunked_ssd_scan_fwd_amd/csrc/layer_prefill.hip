@@ -37,7 +37,7 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int CT = 256;   // threads of a block of the carry pass
-constexpr int SORTED = 512, KEY = 10;   // most sequences that are put in order, by as many bits of their lengths
+constexpr int SORTED = 64, KEY = 8;   // most sequences that are put in order, by as many bits of their lengths
 
 struct PrefillArgs {
     const void *q, *k, *v;
@@ -356,70 +356,47 @@ __device__ __forceinline__ void about(const PrefillArgs &a, int n, Place &p, int
     p.segs = a.seg == 0 ? 1 : max(1, (end - begin + a.seg - 1) / a.seg);
 }
 
-// Segment number r in the order of falling lengths, for every wave by itself:
-// the whole ones (of a.seg rows) by their sequence, then each sequence's rest,
-// or the sequence where none is cut, by KEY bits of its length from `shift`
-// on, equal ones as they come.  An empty sequence counts as a rest.  False:
-// there are no more.
+// Segment number r in the order of falling lengths, for every wave by itself,
+// a sequence to a lane: the whole ones (of a.seg rows) by their sequence, then
+// each sequence's rest, or the sequence where none is cut, by KEY bits of its
+// length from `shift` on, equal ones as they come.  An empty sequence counts
+// as a rest.  False: there are no more.
 __device__ __forceinline__ bool by_length(const PrefillArgs &a, int r, int &n, int &s)
 {
-    constexpr int U = SORTED / 64;
     const int lane = threadIdx.x & 63;
-    int key[U];
-    bool have = false;
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-        key[u] = -1;
-        if (64 * u >= a.N) continue;
-        const int j = 64 * u + lane;
-        int b, e;
-        rows_of(a, min(j, a.N - 1), b, e);
-        const int len = j < a.N ? e - b : 0, whole = a.seg > 0 ? len / a.seg : 0, rest = len - whole * a.seg;
-        if (j < a.N && (rest > 0 || len == 0)) key[u] = min(rest >> a.shift, (1 << KEY) - 1);
-        if (a.seg > 0 && !have) {
-            int sum = whole;   // of the lanes up to this one
-            for (int d = 1; d < 64; d *= 2) {
-                const int x = __shfl_up(sum, d);
-                if (lane >= d) sum += x;
-            }
-            const unsigned long long m = __ballot(sum > r);
-            if (m != 0) {
-                const int at = __ffsll(m) - 1;
-                n = 64 * u + at;
-                s = r - __builtin_amdgcn_readlane(sum - whole, at);
-                have = true;
-            } else {
-                r -= __builtin_amdgcn_readlane(sum, 63);
-            }
+    const bool on = lane < a.N;
+    int b, e;
+    rows_of(a, min(lane, a.N - 1), b, e);
+    const int len = on ? e - b : 0, whole = a.seg > 0 ? len / a.seg : 0, rest = len - whole * a.seg;
+    if (a.seg > 0) {
+        int sum = whole;   // of the lanes up to this one
+        for (int d = 1; d < 64; d *= 2) {
+            const int x = __shfl_up(sum, d);
+            if (lane >= d) sum += x;
         }
+        const unsigned long long m = __ballot(sum > r);
+        if (m != 0) {
+            n = __ffsll(m) - 1;
+            s = r - __builtin_amdgcn_readlane(sum - whole, n);
+            return true;
+        }
+        r -= __builtin_amdgcn_readlane(sum, 63);
     }
-    if (have) return true;
-    // bit by bit, the r-th largest key
-    int found = 0;
+    // bit by bit, the lanes that have the r-th largest key
+    const int key = min(rest >> a.shift, (1 << KEY) - 1);
+    unsigned long long left = __ballot(on && (rest > 0 || len == 0));
+#pragma unroll
     for (int bit = KEY - 1; bit >= 0; --bit) {
-        const int want = found >> bit | 1;
-        int c = 0;
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (64 * u < a.N) c += __popcll(__ballot(key[u] >> bit == want));
-        if (r < c)
-            found = want << bit;
-        else
-            r -= c;
+        const unsigned long long set = __ballot(key >> bit & 1) & left;
+        const int c = __popcll(set);
+        left = r < c ? set : left & ~set;
+        r -= r < c ? 0 : c;
     }
-    // and the sequence among those that have it
-    n = -1;
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-        if (64 * u < a.N) {
-            const unsigned long long m = __ballot(key[u] == found);
-            const int before = __builtin_amdgcn_mbcnt_hi((unsigned)(m >> 32), __builtin_amdgcn_mbcnt_lo((unsigned)m, 0));
-            const unsigned long long hit = __ballot(key[u] == found && before == r);
-            if (hit != 0) n = 64 * u + __ffsll(hit) - 1;
-            r -= __popcll(m);
-        }
+    const int before = __builtin_amdgcn_mbcnt_hi((unsigned)(left >> 32), __builtin_amdgcn_mbcnt_lo((unsigned)left, 0));
+    const unsigned long long hit = __ballot(before == r) & left;
+    n = __ffsll(hit) - 1;
     s = -1;   // the last
-    return n >= 0;
+    return hit != 0;
 }
 
 // Where block number `id` works, and the number of its segment in its place.
@@ -873,20 +850,23 @@ static PrefillPlan plan_prefill(const lin_shape &s, int dtype, int64_t max_seqle
 }
 
 // Segments start in the order of falling lengths, so that the long ones have
-// company that ends early and none is left to the end: 40 mixed prompts of 24
-// heads of 128 x 64 took 79 us so and 98 as they came, 60 of 8 heads of 128 74
-// and 85, 16 that are cut of 16 such heads 210 and 266.  Not where each block
-// has a CU for itself: finding a place in the order takes a block two
-// dependent loads for one (20 equal prompts of 24 heads: 35 us and 33).  Nor
-// for more than SORTED sequences, where the order is slow to find and any one
-// of them is a small part.
+// company that ends early and none is left to the end.  Mixed prompts in us,
+// so and as they came: 40 of up to 1248 rows and 24 heads of 128 x 64 76 and
+// 98, 60 of up to 1262 and 8 heads of 128 72 and 84, 16 of up to 6180 and such
+// heads, cut, 127 and 142.  Finding its place in the order costs a block about
+// a microsecond, so it is not done where each block has a CU for itself, nor
+// for prompts that are short (64 of up to 259 rows and 24 heads: 40 and 36) or
+// equal by the bound of their lengths, nor for more of them than a wave has
+// lanes (an order of 100 of up to 512 rows and 8 heads: 73 and 70).
 static int order_shift(const lin_shape &s, const PrefillPlan &P, int64_t max_seqlen, int64_t blocks, int cus)
 {
-    if (s.N < 2 || s.N > SORTED || blocks <= cus) return -1;
-    const int64_t most = max_seqlen > 0 && max_seqlen < s.T ? max_seqlen : s.T;
-    const int64_t longest = P.seg > 0 ? P.seg : most;
+    const int64_t longest = max_seqlen > 0 && max_seqlen < s.T ? max_seqlen : s.T;
+    if (s.N < 2 || s.N > SORTED || blocks <= cus || longest < 512 ||
+        longest * s.N < s.T + s.T / 2)
+        return -1;
+    const int64_t most = P.seg > 0 ? P.seg : longest;
     int shift = 0;
-    while (longest >> shift >= 1 << KEY) ++shift;
+    while (most >> shift >= 1 << KEY) ++shift;
     return shift;
 }
 

@@ -148,6 +148,19 @@ def test_prefill_many_ragged(n, longest, hint):
                               slots=[(i * 7 + 3) % n if n % 7 else i for i in range(n)], max_seqlen=hint, seed=n, tail=1)
 
 
+@pytest.mark.parametrize("n", [2, 3, 40, 63, 64, 65])
+@pytest.mark.parametrize("hint", [700, 640, 0])
+def test_prefill_ragged_long(n, hint):
+    """Batches that start with their longest sequences: whole, with a bound or one that is too low, and by the
+    number of rows alone."""
+    H = 4096 // n
+    w = torch.rand(n, generator=torch.Generator().manual_seed(n)) ** 3
+    lens = (w * 300).long().tolist()
+    lens[0], lens[n - 1], lens[n // 2] = 1, 700, 600 if n > 2 else 40
+    check_prefill("ragged", (1, H, 8, 4), BF, lens, carry=[i % 2 for i in range(n)],
+                  slots=[n - 1 - i for i in range(n)], max_seqlen=hint, seed=n, tail=3)
+
+
 @pytest.mark.parametrize("dtype", [F32, BF, F16])
 @pytest.mark.parametrize("lens", [[256, 128, 0, 1024, 384], [640, 640, 512], [0, 1300, 0, 0, 1]])
 def test_prefill_segments_that_end_with_the_sequence(lens, dtype):
