@@ -358,7 +358,9 @@ int mamba_fwd_bwd(const mamba_shape *shape,
  *
  * Types.  `dtype` is the element type of q, k, v, y (x, dy, gate, dx, dgate);
  * states, log decays, weights, statistics and all sums are float32.  Outputs
- * are rounded to `dtype` once.
+ * are rounded to `dtype` once.  lin_prefill of bfloat16 also rounds the masked
+ * scores and a copy of the state that meets q to bfloat16; the state itself it
+ * does not.
  *
  * Ownership, asynchrony and status codes are those of ssd_fwd, with these
  * differences: pointers need the alignment of their element type only (16
