@@ -102,7 +102,7 @@ __global__ __launch_bounds__(CT) void k_state_pack(CacheArgs a, const float *sta
             for (int e = 0; e < 4; ++e)
                 if (col + e < a.dv) to[e] = (uint8_t)(word >> (8 * e));
         }
-        if (part == 0) scales[dst * a.per + b] = bad ? 255 : (uint8_t)(s + 127);
+        if (part == 0) scales[(int64_t)dst * a.per + b] = bad ? 255 : (uint8_t)(s + 127);
     }
 }
 
@@ -133,7 +133,7 @@ __global__ __launch_bounds__(CT) void k_state_unpack(CacheArgs a, const uint8_t 
             for (int e = 0; e < 4; ++e)
                 if (on && col + e < a.dv) word[u] |= (unsigned)from[e] << (8 * e);
         }
-        sb[u] = on ? scales[src * a.per + b] : 255;
+        sb[u] = on ? scales[(int64_t)src * a.per + b] : 255;
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {

@@ -834,3 +834,20 @@ def test_binding_refuses():
     c, s = cache_of(3, 2, 8, 8)
     with pytest.raises(ValueError):
         ssd.state_pack(S, c, s, slots=ids([0, 1]), entries=ids([0]))
+
+
+def test_cache_scales_past_32_bits():
+    """Entries whose scales start 2^32 bytes into their array; the first entries' stay as they are."""
+    H, dk, n = 16, 256, (1 << 20) + 2
+    say(f"cache of {n} entries of {H} x {dk} x 1")
+    cache, scales = cache_of(n, H, dk, 1)
+    S = torch.randn(2, H, dk, 1, generator=torch.Generator().manual_seed(7)) * 3.0
+    pool = dev(S)
+    ssd.state_pack(pool, cache, scales, slots=ids([0, 1]), entries=ids([n - 2, n - 1]))
+    code, sc = ref.pack(S.numpy())
+    assert np.array_equal(cache[n - 2:].view(torch.uint8).cpu().numpy(), code)
+    assert np.array_equal(scales[n - 2:].cpu().numpy(), sc)
+    assert not bool(cache[:2].view(torch.uint8).any()) and not bool(scales[:2].any())
+    pool.zero_()
+    ssd.state_unpack(cache, scales, pool, slots=ids([1, 0]), entries=ids([n - 2, n - 1]))
+    assert np.array_equal(pool.cpu().double().numpy(), ref.unpack(code, sc)[::-1])
