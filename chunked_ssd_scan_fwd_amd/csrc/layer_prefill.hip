@@ -141,10 +141,8 @@ __device__ __forceinline__ void frag_acc(Frag<float> &r, f32x4 a, f32x4 b)
 // V's rows times e^{b_L - b} (wa, wb: the fragment's first and last four
 // rows), in PARTS summands.  float32 takes one.  Three bf16 numbers hold what
 // a float32 product does: states came out within 2e-7 of 64 bits, as float32
-// sums do.  Two leave 2e-6 and save a tenth of the last pass where it is bound
-// by issue (91 against 102 us for 65536 rows of 8 heads); the first pass over
-// a sequence that is cut takes two (55 against 69 us), since what it makes
-// decays over the segments that follow.
+// sums do.  Two leave 2e-6, and a slow decay carries that to the end of the
+// sequence, so the first pass over one that is cut takes three as well.
 // Two bf16 numbers by their bits, in a register: as an inline constant of the
 // dot product this compiler passed (-1, 0) the wrong way round.
 __device__ __forceinline__ bf16x2 pair_of(unsigned bits)
@@ -686,7 +684,7 @@ __attribute__((amdgpu_waves_per_eu(2 * PerCu<E, KP, VT>::n, 2 * PerCu<E, KP, VT>
         }
         const float unscale = 1.f / scale;
         const auto rows32 = [&](auto step) {   // 32 rows of the chunk
-            constexpr int s = decltype(step)::value, PARTS = sizeof(L) == 4 ? 1 : OUT ? 3 : 2;
+            constexpr int s = decltype(step)::value, PARTS = sizeof(L) == 4 ? 1 : 3;
             Frag<L> fv[NT], fw[NT][3];
             const f32x4 wa = *reinterpret_cast<const f32x4 *>(d.out + 32 * s + g4) * unscale;
             const f32x4 wb = *reinterpret_cast<const f32x4 *>(d.out + 32 * s + 16 + g4) * unscale;

@@ -851,3 +851,46 @@ def test_cache_scales_past_32_bits():
     pool.zero_()
     ssd.state_unpack(cache, scales, pool, slots=ids([1, 0]), entries=ids([n - 2, n - 1]))
     assert np.array_equal(pool.cpu().double().numpy(), ref.unpack(code, sc)[::-1])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF, F16])
+@pytest.mark.parametrize("heads", [(1, 2, 64, 64), (1, 1, 128, 128), (1, 1, 200, 48)])
+@pytest.mark.parametrize("T,at", [(90, 5), (90, 70), (1500, 5), (1500, 700), (1500, 1490)])
+def test_prefill_state_of_one_row(T, at, heads, dtype):
+    """float32 accuracy of a state that one row makes and nothing fades, whole and cut.
+
+    The state is k v^T.  It may go through v times a decay of the chunk and
+    back: the two factors, the products with them and the sum of the product's
+    parts are a dozen roundings of 2^-24, within 2^-20.  v times a decay in two
+    bfloat16 parts would be off by up to 2^-16."""
+    G, H, dk, dv = heads
+    say(f"one row {heads} {dtype} T {T} at {at}")
+    q, k, v, _, S = ref.inputs(T, G, H, dk, dv, dtype, True, 21, 1)
+    row = k[at].clone()
+    k.zero_()
+    k[at] = row
+    ld = torch.zeros(T, H)
+    ld[at] = -0.3
+    pool = dev(S)
+    ssd.lin_prefill(dev(q), dev(k), dev(v), dev(ld), ids([0, T]), pool, carry=ids([0]))
+    want = ref.scan(q, k, v, ld, [0, T], S, carry=[0])[1]
+    ref.within(pool, want, 2.0 ** -20 * want.abs() + 1e-30)
+
+
+@pytest.mark.parametrize("la,dtype", [(la, d) for la in ("forget", "all", "growth", "strong", "none", "slow") for d in (F32, BF, F16)
+                                      if (la, d) != ("growth", F16)])   # there y passes float16's 65504
+def test_prefill_decays_of_cut_sequences(la, dtype):
+    def change(ld):
+        ld = ld.clone()
+        if la == "forget":   # first, last and inner rows of chunks, segments and sequences
+            ld[[0, 10, 64, 70, 71, 127, 128, 130, 255, 256, 800, 1499, 1500, 2000]] = -np.inf
+        elif la == "all":
+            ld[:] = -np.inf
+        elif la == "growth":
+            ld[:] = ld.abs() * 0.05
+        elif la == "strong":
+            ld[:] = -60.0 + ld
+        else:
+            ld[:] = -1e-4 if la == "slow" else 0
+        return ld
+    check_prefill("cut, decay " + la, (1, 2, 64, 64), dtype, [1500, 700], la=change, seed=2, max_seqlen=0)
