@@ -37,6 +37,7 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef f16 f16x2 __attribute__((ext_vector_type(2)));
 typedef bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
@@ -192,6 +193,18 @@ __device__ __forceinline__ void store4(float *p, const float (&x)[4])
 
 // ---- tiles of q, k and v: global memory to registers to LDS
 
+// sum + 0 x of the elements x in a register.
+template <typename E>
+__device__ __forceinline__ float add_zero_times(unsigned bits, float sum)
+{
+    if constexpr (std::is_same<E, bf16>::value)
+        return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, bits), pair_of(0), sum, false);
+    else if constexpr (std::is_same<E, f16>::value)
+        return __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, bits), f16x2{}, sum, false);
+    else
+        return __builtin_fmaf(__uint_as_float(bits), 0.f, sum);
+}
+
 // A ROWS x COLS tile of elements E, PER pieces of 16 bytes to each of PT threads.
 template <typename E, int ROWS, int COLS, int PT>
 struct Tile {
@@ -238,6 +251,18 @@ struct Tile {
                 __builtin_memcpy(&buf[u], x, 16);
             }
         }
+    }
+
+    // 0, or NaN where one of the thread's elements is an infinity or a NaN: the
+    // sum of 0 times each, in four chains that do not wait for each other.
+    __device__ __forceinline__ float zero_times() const
+    {
+        float sum[4] = {};
+#pragma unroll
+        for (int u = 0; u < PER; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sum[i] = add_zero_times<E>(buf[u][i], sum[i]);
+        return (sum[0] + sum[1]) + (sum[2] + sum[3]);
     }
 
     template <int LD, typename L>
@@ -464,6 +489,7 @@ struct ChunkLds {
     static constexpr int LK = KP + PAD, LV = VT + PAD, LP = C + PAD;
     L q[2][OUT ? C * LK : 8], k[2][C * LK], v[2][C * LV], p[2][OUT ? C * LP : 8];
     Decays<C> dec[3];
+    alignas(16) float odd[2][256];   // by fetching thread: 0, or NaN where its part of v has an infinity or a NaN
 };
 
 // Blocks that share a CU.  With 64 columns and 32-row chunks two of them fit
@@ -515,10 +541,14 @@ __attribute__((amdgpu_waves_per_eu(2 * PerCu<E, KP, VT>::n, 2 * PerCu<E, KP, VT>
         const float *la = a.la + (a.la_t ? p.begin * a.la_t : 0) + h;
         Tile<E, C, KP, PT> tq, tk;
         Tile<E, C, VT, PT> tv;
+        // The tiles of chunk c, after those of the chunk before it went to LDS.
+        // Whether v's had infinities or NaN is looked at with the loads of q
+        // and k on their way, and told in the place that was stored last.
         const auto load = [&](int c) {
             const int t0 = c * C, rows = p.rows - t0;
             if (OUT) tq.template load<VEC>(q + t0 * a.st.q_t, a.st.q_t, min(C, rows), a.dk, tid);
             tk.template load<VEC>(k + t0 * a.st.k_t, a.st.k_t, min(C, rows), a.dk, tid);
+            if (c > 0) lds.odd[(c - 1) & 1][tid] = tv.zero_times();
             tv.template load<VEC>(v + t0 * a.st.v_t, a.st.v_t, min(C, rows), cols, tid);
         };
         const auto log_decay = [&](int c) {
@@ -648,6 +678,8 @@ __attribute__((amdgpu_waves_per_eu(2 * PerCu<E, KP, VT>::n, 2 * PerCu<E, KP, VT>
         const int b = c & 1;
         const Decays<C> &d = lds.dec[c % 3];
         const L *qs = lds.q[b], *ks = lds.k[b], *vs = lds.v[b], *ps = lds.p[b];
+        const f32x4 o = *reinterpret_cast<const f32x4 *>(lds.odd[b] + 4 * lane);
+        const bool odd = __ballot(!((o[0] + o[1]) + (o[2] + o[3]) == 0.f)) != 0;
         f32x4 Y[NT][TT];
         if (OUT) {
             // Y^T = diag(e^b) S^T Q^T, rows: columns of v, columns: queries
@@ -667,13 +699,8 @@ __attribute__((amdgpu_waves_per_eu(2 * PerCu<E, KP, VT>::n, 2 * PerCu<E, KP, VT>
                     for (int n = 0; n < NT; ++n) Y[n][t] = mma(fs[n], fq, Y[n][t]);
                 }
             }
-#pragma unroll
-            for (int t = 0; t < TT; ++t) {
-                const float e = d.in[16 * t + l16] * scale;
-#pragma unroll
-                for (int n = 0; n < NT; ++n) Y[n][t] *= e;
-            }
         }
+        const float entered = scale;
         scale = __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(scale * d.all)));
         if (!(scale > 0x1p-16f && scale < 0x1p16f)) {   // and where it is NaN
 #pragma unroll
@@ -681,6 +708,56 @@ __attribute__((amdgpu_waves_per_eu(2 * PerCu<E, KP, VT>::n, 2 * PerCu<E, KP, VT>
 #pragma unroll
                 for (int n = 0; n < NT; ++n) S[m][n] *= scale;
             scale = 1.f;
+        }
+        // The terms of v's infinities and NaN, which are 0 in the tile from then
+        // on: at the scores above the diagonal, where P is 0, they would reach
+        // earlier rows, and the parts of a product with an infinity do not add
+        // up to it.  No other wave reads this one's columns.  (Y is scaled by
+        // e^b after them, which leaves an infinity one or makes it NaN.)
+        const auto odd_terms = [&]() {
+            const auto finite = [](float x) { return __builtin_fabsf(x) < __builtin_inff(); };
+#pragma unroll 1
+            for (int j = 0; j < min(C, p.rows - c * C); ++j) {
+                L *vj = lds.v[b] + j * LV + w0;
+                const L *pj = ps + 32 * (j / 32) + 8 * (j % 16 / 4) + 4 * (j / 16 % 2) + j % 4;
+                if (OUT) {
+                    float score[TT], x[4 * NT];
+#pragma unroll
+                    for (int t = 0; t < TT; ++t) score[t] = to_f(pj[(16 * t + l16) * LP]);
+#pragma unroll
+                    for (int e = 0; e < 4 * NT; ++e) x[e] = to_f(vj[NT * g4 + e]);
+#pragma unroll
+                    for (int e = 0; e < 4 * NT; ++e)
+#pragma unroll
+                        for (int t = 0; t < TT; ++t)
+                            Y[e / 4][t][e % 4] += finite(x[e]) || j > 16 * t + l16 ? 0.f : score[t] * x[e];
+                }
+                __builtin_amdgcn_wave_barrier();   // the lanes have read the row's values that others take out
+                const float out = d.out[j];
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    L *at = vj + (NT == 2 ? 8 * (l16 >> 2) + 4 * n + (l16 & 3) : l16);
+                    const float x = to_f(*at);
+                    if (finite(x)) continue;
+                    *at = (L)0.f;
+#pragma unroll
+                    for (int s = 0; s < KS; ++s) {
+                        const Frag<L> fk = frag8(ks + j * LK + 32 * s + 2 * g4);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) S[2 * s + i / 4][n][i % 4] += to_f(fk.x[i]) * (x * out);
+                    }
+                }
+            }
+            __builtin_amdgcn_wave_barrier();
+        };
+        if (__builtin_expect(odd, 0)) odd_terms();
+        if (OUT) {
+#pragma unroll
+            for (int t = 0; t < TT; ++t) {
+                const float e = d.in[16 * t + l16] * entered;
+#pragma unroll
+                for (int n = 0; n < NT; ++n) Y[n][t] *= e;
+            }
         }
         const float unscale = 1.f / scale;
         const auto rows32 = [&](auto step) {   // 32 rows of the chunk

@@ -413,8 +413,10 @@ size_t lin_prefill_workspace_size(const lin_shape *shape, int64_t max_seqlen);
  *   max_seqlen    an upper bound of the lengths, 0 if unknown (then T).  It
  *                 only chooses how the work is split; a sequence that is
  *                 longer all the same is still computed.
- * Infinite and NaN values of a sequence's rows stay within that sequence,
- * and reach rows up to 63 positions before their own.
+ * Infinite and NaN values of a row reach, as in the recurrence, only it and
+ * the rows after it in its sequence, and one in v no column but its own.
+ * Where the recurrence gives an infinity, NaN may stand in y, and in the
+ * state where it comes from k or decays by a factor that vanishes in float32.
  * dk, dv in 1..256 (else SSD_ERR_UNSUPPORTED), G >= 1, H % G == 0,
  * T < 2^30, N and slots < 2^24, N H ceil(dv / 32) < 2^23, row strides below
  * 2^24 elements, and strides of y that let no two of its values overlap (else

@@ -894,3 +894,46 @@ def test_prefill_decays_of_cut_sequences(la, dtype):
             ld[:] = -1e-4 if la == "slow" else 0
         return ld
     check_prefill("cut, decay " + la, (1, 2, 64, 64), dtype, [1500, 700], la=change, seed=2, max_seqlen=0)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF, F16])
+@pytest.mark.parametrize("heads", [(1, 2, 64, 64), (1, 1, 64, 128), (1, 1, 128, 64), (1, 1, 128, 128), (1, 1, 256, 64), (1, 2, 33, 97)])
+@pytest.mark.parametrize("T,rows", [(130, (0, 17, 63, 100)), (1100, (300, 1050))])
+def test_prefill_poison_reaches_no_earlier_row(T, rows, heads, dtype):
+    """One infinity or NaN among the inputs: rows before it, columns beside it in v and other heads' results are
+    what they are without it; what it does reach is not finite; an infinite v makes the state infinite, by its sign."""
+    G, H, dk, dv = heads
+    base = dict(zip(("q", "k", "v", "ld", "S"), ref.inputs(T, G, H, dk, dv, dtype, True, 5, 1, la_mu=-5.0)))
+    y0, S0, ya, Sa = ref.scan(*(base[n] for n in ("q", "k", "v", "ld")), [0, T], base["S"])
+    yb, Sb = ref.y_bound(dtype, y0, ya), ref.state_bound(Sa)
+    col, h = dv // 2, H - 1
+    where = {"q": (0, 0), "k": (0, dk // 2), "v": (h, col), "ld": (h,)}
+    others = [c for c in range(dv) if c != col]
+    for at in rows:
+        for name, bad in (("v", np.inf), ("v", -np.inf), ("v", NAN), ("k", np.inf), ("q", NAN), ("ld", NAN)):
+            say(f"{bad} in {name} {heads} {dtype} T {T} row {at}")
+            x = {n: t.clone() for n, t in base.items()}
+            x[name][(at, *where[name])] = bad
+            pool = dev(x["S"])
+            y = ssd.lin_prefill(*(dev(x[n]) for n in ("q", "k", "v", "ld")), ids([0, T]), pool, max_seqlen=0).cpu()
+            S = pool.cpu()
+            ref.within(y[:at], y0[:at], yb[:at])
+            if name == "v":
+                ref.within(y[:, h, others], y0[:, h, others], yb[:, h, others])
+                ref.within(S[0, h][:, others], S0[0, h][:, others], Sb[0, h][:, others])
+                assert not bool(torch.isfinite(y[at:, h, col]).any())
+                # k times it: infinities of either sign, or NaN
+                np.testing.assert_array_equal(S[0, h, :, col].double().numpy(), (x["k"][at, 0].double() * bad).numpy())
+            elif name == "k":
+                rest = [r for r in range(dk) if r != dk // 2]
+                ref.within(S[0][:, rest], S0[0][:, rest], Sb[0][:, rest])
+                assert not bool(torch.isfinite(S[0][:, dk // 2]).any())
+            elif name == "q":
+                assert not bool(torch.isfinite(y[at]).any())
+                ref.within(y[at + 1:], y0[at + 1:], yb[at + 1:])
+                ref.within(S, S0, Sb)
+            else:
+                assert not bool(torch.isfinite(y[at:, h]).any()) and not bool(torch.isfinite(S[0, h]).any())
+            if name in ("v", "ld"):   # the other heads
+                ref.within(y[:, :h], y0[:, :h], yb[:, :h])
+                ref.within(S[0, :h], S0[0, :h], Sb[0, :h])
