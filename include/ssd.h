@@ -445,8 +445,12 @@ int lin_step(const lin_shape *shape, int dtype, const lin_strides *strides,
  * rstd = 1 / sqrt(variance + eps) and z = (x - mu) rstd weight + bias:
  *     y = act(z)            without a gate
  *     y = z act(gate)       with one
- * where act is SiLU, u / (1 + e^-u), or nothing.  L = 1 with a group for each
- * head is the norm that follows the scan.  weight, bias: float32 [C] or NULL
+ * where act is SiLU, u / (1 + e^-u), or nothing.  An infinity or a NaN in x
+ * or dy reaches only its run and dweight and dbias of the run's channels; one
+ * in a gate only y and dgate at its place, dx in its run and dweight and dbias
+ * of its channel.  SiLU of -infinity, and its derivative at either infinity,
+ * are NaN, as the formulas give them.  L = 1 with a group for each head is the
+ * norm that follows the scan.  weight, bias: float32 [C] or NULL
  * (1 and 0).  stats [N][groups][2] receives mu and rstd.
  * Row n L + l of x, gate, dy starts ld_* elements after the row before it
  * (0: C); y, dx and dgate are dense.  C % groups == 0; N L C < 2^40, C and

@@ -937,3 +937,27 @@ def test_prefill_poison_reaches_no_earlier_row(T, rows, heads, dtype):
             if name in ("v", "ld"):   # the other heads
                 ref.within(y[:, :h], y0[:, :h], yb[:, :h])
                 ref.within(S[0, :h], S0[0, :h], Sb[0, :h])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF, F16])
+@pytest.mark.parametrize("L", [1, 5, 700])
+def test_group_norm_of_infinite_gates(L, dtype):
+    """SiLU of +infinity is infinite, of -infinity NaN, its derivative at both NaN; what belongs to other places,
+    channels and runs stays as it is."""
+    x, w, b, gate, dy = (dev(t) for t in gn_inputs(4, L, 32, dtype, True))
+    bad = gate.clone()
+    bad[1, 0, 3], bad[2, L - 1, 30] = np.inf, -np.inf
+
+    def run(g):
+        y, st = ssd.gn_fwd(x, w, b, 4, gate=g)
+        return (y, *ssd.gn_bwd(x, w, b, 4, st, dy, gate=g))
+    (y, dx, dw, db, dg), clean = run(bad), run(gate)
+    place = torch.zeros(4, L, 32, dtype=torch.bool, device="cuda")
+    place[1, 0, 3] = place[2, L - 1, 30] = True
+    run_of = torch.zeros_like(place)
+    run_of[1, :, :8] = run_of[2, :, 24:] = True
+    channel = place.any(0).any(0)
+    assert bool(torch.isinf(y[1, 0, 3])) and bool(torch.isnan(y[2, L - 1, 30])) and bool(torch.isnan(dg[place]).all())
+    for got, want, where in zip((y, dx, dw, db, dg), clean, (place, run_of, channel, channel, place)):
+        assert not bool(torch.isfinite(got[where]).any())
+        assert torch.equal(got[~where], want[~where])
