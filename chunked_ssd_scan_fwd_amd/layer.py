@@ -368,6 +368,11 @@ def _cache_args(states, cache, scales, slots, entries):
     E = cache.shape[0]
     cp = _dense(cache, "cache", (E, H, dk, dv), _torch.float8_e4m3fn, dev)
     ep = _dense(scales, "scales", (E, H, dk, -(-dv // STATE_CACHE_BLOCK)), _torch.uint8, dev)
+    for t, name in ((slots, "slots"), (entries, "entries")):
+        if t is not None and not isinstance(t, _torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t is not None and t.dim() != 1:
+            raise ValueError(f"{name} must be a tensor of indexes, one for each pair")
     n = slots.shape[0] if slots is not None else entries.shape[0] if entries is not None else min(S, E)
     if (slots is None and n > S) or (entries is None and n > E):
         raise ValueError(f"{n} pairs, {S} slots and {E} entries")

@@ -961,3 +961,20 @@ def test_group_norm_of_infinite_gates(L, dtype):
     for got, want, where in zip((y, dx, dw, db, dg), clean, (place, run_of, channel, channel, place)):
         assert not bool(torch.isfinite(got[where]).any())
         assert torch.equal(got[~where], want[~where])
+
+
+def test_cache_binding_refuses_index_arrays():
+    """What is no tensor, of no axis or of more than one, of another type, on the host, or not dense."""
+    S = torch.ones(4, 1, 2, 8, device="cuda")
+    cache, scales = cache_of(4, 1, 2, 8)
+    for bad, err in (([0, 1], TypeError), (np.zeros(2, np.int32), TypeError), (ids([0, 1]).long(), TypeError),
+                     (ids([[0, 1]]), ValueError), (ids(0), ValueError), (ids([0, 1]).cpu(), ValueError),
+                     (ids([0, 1, 2, 3])[::2], ValueError)):
+        for name in ("slots", "entries"):
+            other = {"slots": "entries", "entries": "slots"}[name]
+            for given in ({name: bad}, {name: bad, other: ids([1, 0])}):
+                with pytest.raises(err):
+                    ssd.state_pack(S, cache, scales, **given)
+                with pytest.raises(err):
+                    ssd.state_unpack(cache, scales, S, **given)
+    assert bool((S == 1).all()) and not bool(scales.any())
