@@ -22,6 +22,7 @@
 // y is 0.0023 from 64 bits where its own rounding makes 0.0017 (up to 0.0036
 // in a row of one term, whose P is not averaged with others).  S itself, its
 // update and all sums stay float32, so nothing of it adds up over a sequence.
+// q, k and v handed in as float32 are rounded nowhere.
 #include <type_traits>
 
 #include "layer_device.h"
@@ -494,10 +495,11 @@ struct ChunkLds {
 
 // Blocks that share a CU.  With 64 columns and 32-row chunks two of them fit
 // its LDS and registers, and fill each other's waits: 20 mixed prompts of 24
-// heads of 128 x 64 took 44 us so, 59 with one and 64-row chunks.  Heads of
-// 128 columns are faster as one block of them with 64-row chunks than as two
-// blocks of 64 with 32-row ones (102 against 121 us for the last pass over
-// 65536 rows of 8 heads, 439 against 520 for 16 prompts of 8192 and 16 heads).
+// heads of 128 x 64 took 44 us so, 49 with one and 64-row chunks, 20 of 500
+// rows 33 and 46, one of 32768 155 and 216; 8 of 2048 took 73 and 69.  Heads
+// of 128 columns are faster as one block of them with 64-row chunks than as
+// two blocks of 64 with 32-row ones (171 against 210 us for 65536 rows of 8
+// heads, 428 against 523 for 16 prompts of 8192 and 16 heads).
 template <typename E, int KP, int VT>
 struct PerCu {
     static constexpr int n = VT == 64 && KP <= 128 && std::is_same<E, bf16>::value ? 2 : 1;
@@ -637,8 +639,8 @@ __attribute__((amdgpu_waves_per_eu(2 * PerCu<E, KP, VT>::n, 2 * PerCu<E, KP, VT>
 
     // ---- states and outputs
     //
-    // Ahead of the others where both have something to issue: 486 us on
-    // average for the largest batch measured, 497 without.
+    // Ahead of the others where both have something to issue: 204 us for 65536
+    // rows of 16 heads of 64, 206 without; other shapes within the noise.
     __builtin_amdgcn_s_setprio(1);
     const int64_t state = (int64_t)a.dk * a.dv;
     float *pool = p.slot < 0 ? nullptr : a.states + ((int64_t)p.slot * a.H + h) * state;
@@ -893,10 +895,12 @@ static int col_tile(int64_t dk, int64_t dv) { return dk > 128 || dv <= 64 ? 64 :
 // Cut, a segment's two passes count for twice its rows, with 7 us for the two
 // launches more and the time to write, carry and read the segments' states.
 // A row takes 37 ns in bf16, 30 and 1 more for 128 values of a state on fp32
-// MFMA.  Measured whole and cut, in us: one prompt of 384 rows 20 and 23, of
-// 768 34 and 23, of 65536 2350 and 158 (8 heads of 128); mixed prompts, 30 of
-// up to 1004 rows 49 and 69 (the same heads), 8 of up to 4526 171 and 121, 8 of
-// 8192 326 and 352 (16 heads).
+// MFMA; that is measured at heads of 128 and 128 x 64 with rows on 16 bytes.
+// Rows that are not take about twice as long, which the estimate leaves out.
+// Measured whole and cut, in us: one prompt of 384 rows 20 and 24, of 768 34
+// and 24, of 65536 2374 and 167 (8 heads of 128); mixed prompts, 30 of up to
+// 1004 rows 49 and 71 (the same heads), 8 of up to 4526 177 and 132, 8 of 8192
+// 320 and 338 (16 heads).
 static PrefillPlan plan_prefill(const lin_shape &s, int dtype, int64_t max_seqlen, int cus)
 {
     PrefillPlan P;
@@ -931,11 +935,11 @@ static PrefillPlan plan_prefill(const lin_shape &s, int dtype, int64_t max_seqle
 
 // Segments start in the order of falling lengths, so that the long ones have
 // company that ends early and none is left to the end.  Mixed prompts in us,
-// so and as they came: 40 of up to 1248 rows and 24 heads of 128 x 64 76 and
-// 98, 60 of up to 1262 and 8 heads of 128 72 and 84, 16 of up to 6180 and such
-// heads, cut, 127 and 142.  Finding its place in the order costs a block about
+// so and as they came: 40 of up to 1248 rows and 24 heads of 128 x 64 81 and
+// 105, 60 of up to 1262 and 8 heads of 128 74 and 87, 16 of up to 6180 and such
+// heads, cut, 132 and 151.  Finding its place in the order costs a block about
 // a microsecond, so it is not done where each block has a CU for itself, nor
-// for prompts that are short (64 of up to 259 rows and 24 heads: 40 and 36) or
+// for prompts that are short (64 of up to 259 rows and 24 heads: 45 and 43) or
 // equal by the bound of their lengths, nor for more of them than a wave has
 // lanes (an order of 100 of up to 512 rows and 8 heads: 73 and 70).
 static int order_shift(const lin_shape &s, const PrefillPlan &P, int64_t max_seqlen, int64_t blocks, int cus)

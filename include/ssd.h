@@ -360,7 +360,7 @@ int mamba_fwd_bwd(const mamba_shape *shape,
  * states, log decays, weights, statistics and all sums are float32.  Outputs
  * are rounded to `dtype` once.  lin_prefill of bfloat16 also rounds the masked
  * scores and a copy of the state that meets q to bfloat16; the state itself it
- * does not.
+ * does not.  q, k and v in float32 are rounded nowhere.
  *
  * Ownership, asynchrony and status codes are those of ssd_fwd, with these
  * differences: pointers need the alignment of their element type only (16
@@ -417,6 +417,7 @@ size_t lin_prefill_workspace_size(const lin_shape *shape, int64_t max_seqlen);
  * the rows after it in its sequence, and one in v no column but its own.
  * Where the recurrence gives an infinity, NaN may stand in y, and in the
  * state where it comes from k or decays by a factor that vanishes in float32.
+ * Values of k v beyond 2^110 in magnitude may become infinite before they would.
  * dk, dv in 1..256 (else SSD_ERR_UNSUPPORTED), G >= 1, H % G == 0,
  * T < 2^30, N and slots < 2^24, N H ceil(dv / 32) < 2^23, row strides below
  * 2^24 elements, and strides of y that let no two of its values overlap (else
