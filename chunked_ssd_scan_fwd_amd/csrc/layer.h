@@ -18,6 +18,7 @@ constexpr int64_t max_blocks(int threads) { return ((int64_t(1) << 32) - 1) / th
 
 int check_dtype(int dtype);
 int check_lin(const lin_shape *s, bool step);
+int check_delta(const lin_shape *s, bool step);
 // The strides to use (dense ones where `st` is null) for `rows` rows, or
 // SSD_ERR_SHAPE where they are out of range or let values of y overlap.
 int resolve_strides(const lin_shape *s, const lin_strides *st, lin_strides *out, int64_t rows);

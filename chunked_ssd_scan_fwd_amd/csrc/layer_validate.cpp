@@ -24,6 +24,14 @@ int check_lin(const lin_shape *s, bool step)
     return SSD_OK;
 }
 
+int check_delta(const lin_shape *s, bool step)
+{
+    const int rc = check_lin(s, step);
+    if (rc != SSD_OK || step) return rc;
+    // a block for each chunk (of 32 rows or more) and head
+    return s->T / 32 + s->N > max_blocks(256) / s->H ? SSD_ERR_SHAPE : SSD_OK;
+}
+
 int resolve_strides(const lin_shape *s, const lin_strides *st, lin_strides *o, int64_t rows)
 {
     if (!st) {

@@ -1,5 +1,5 @@
-"""Operators of a linear-attention layer: Python binding of the lin_, gn_ and
-state_ calls of ``ssd.h``.
+"""Operators of a linear-attention layer: Python binding of the lin_, delta_,
+gn_ and state_ calls of ``ssd.h``.
 
 Like the rest of the binding it only marshals arguments: every step runs in
 the library's HIP kernels, on PyTorch's current stream of the inputs' device,
@@ -15,8 +15,8 @@ from __future__ import annotations
 
 import ctypes
 
-__all__ = ["lin_prefill", "lin_step", "gn_fwd", "gn_bwd", "state_pack", "state_unpack", "lin_prefill_workspace_size",
-           "gn_workspace_size", "STATE_CACHE_BLOCK"]
+__all__ = ["lin_prefill", "lin_step", "gn_fwd", "gn_bwd", "state_pack", "state_unpack", "delta_prefill", "delta_step",
+           "lin_prefill_workspace_size", "delta_prefill_workspace_size", "gn_workspace_size", "STATE_CACHE_BLOCK"]
 
 STATE_CACHE_BLOCK = 32   # values of a state's row that share a scale byte
 _i64, _vp, _sz, _int = ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int
@@ -50,6 +50,11 @@ def declare(lib):
     lib.lin_prefill_workspace_size.restype = _sz
     lib.lin_prefill.argtypes = [lp, _int, tp, _vp, _vp, _vp, _vp, _i64, _vp, _vp, _vp, _i64, _vp, _vp, _vp, _sz, _vp]
     lib.lin_step.argtypes = [lp, _int, tp, _vp, _vp, _vp, _vp, _i64, _vp, _vp, _vp, _vp]
+    lib.delta_prefill_workspace_size.argtypes = [lp, _i64]
+    lib.delta_prefill_workspace_size.restype = _sz
+    lib.delta_prefill.argtypes = [lp, _int, tp, _vp, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _vp, _vp, _vp,
+                                  _sz, _vp]
+    lib.delta_step.argtypes = [lp, _int, tp, _vp, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp]
     for fn in (lib.gn_fwd_workspace_size, lib.gn_bwd_workspace_size):
         fn.argtypes = [gp]
         fn.restype = _sz
@@ -58,7 +63,8 @@ def declare(lib):
                            _vp]
     lib.state_pack.argtypes = [cp, _vp, _vp, _vp, _vp, _vp, _vp]
     lib.state_unpack.argtypes = [cp, _vp, _vp, _vp, _vp, _vp, _vp]
-    for fn in (lib.lin_prefill, lib.lin_step, lib.gn_fwd, lib.gn_bwd, lib.state_pack, lib.state_unpack):
+    for fn in (lib.lin_prefill, lib.lin_step, lib.gn_fwd, lib.gn_bwd, lib.state_pack, lib.state_unpack,
+               lib.delta_prefill, lib.delta_step):
         fn.restype = _int
 
 
@@ -205,6 +211,18 @@ def lin_prefill_workspace_size(T, N, G, H, dk, dv, slots, max_seqlen=0) -> int:
     return int(n)
 
 
+def _packed(cu_seqlens, max_seqlen, dev):
+    """Number of sequences, pointer of the offsets, the bound of the lengths."""
+    if not isinstance(cu_seqlens, _torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
+        raise ValueError("cu_seqlens must be a tensor of N+1 offsets")
+    N = cu_seqlens.shape[0] - 1
+    cu = _dense(cu_seqlens, "cu_seqlens", (N + 1,), _torch.int32, dev)
+    max_seqlen = int(max_seqlen or 0)
+    if max_seqlen < 0:
+        raise ValueError("max_seqlen must not be negative")
+    return N, cu, max_seqlen
+
+
 def lin_prefill(q, k, v, log_decay, cu_seqlens, states, *, slots=None, carry=None, max_seqlen=0, out=None,
                 workspace=None):
     """y[T,H,dv] of the scan over a packed batch: q, k [T,G,dk], v [T,H,dv]
@@ -217,13 +235,7 @@ def lin_prefill(q, k, v, log_decay, cu_seqlens, states, *, slots=None, carry=Non
     becomes of negative, missing and repeated slots."""
     lib = _lib()
     code, dev, (T, G, H, dk, dv, S), sp, ld, lp, out, st = _lin_args(q, k, v, log_decay, states, out, "T")
-    if not isinstance(cu_seqlens, _torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
-        raise ValueError("cu_seqlens must be a tensor of N+1 offsets")
-    N = cu_seqlens.shape[0] - 1
-    cu = _dense(cu_seqlens, "cu_seqlens", (N + 1,), _torch.int32, dev)
-    max_seqlen = int(max_seqlen or 0)
-    if max_seqlen < 0:
-        raise ValueError("max_seqlen must not be negative")
+    N, cu, max_seqlen = _packed(cu_seqlens, max_seqlen, dev)
     s = _arg(LinShapeArg, T, N, G, H, dk, dv, S)
     need = lib.lin_prefill_workspace_size(s, max_seqlen)
     if need == _sz(-1).value:
@@ -246,6 +258,54 @@ def lin_step(q, k, v, log_decay, states, *, slots=None, out=None):
     _call(lib.lin_step, "lin_step", dev, s, code, st, q.data_ptr() or None,
           k.data_ptr() or None, v.data_ptr() or None, lp, ld, _ids(slots, "slots", N, dev), sp,
           out.data_ptr() or None)
+    return out
+
+
+def _beta_args(beta, rows, H, device):
+    """Pointer and row stride of beta."""
+    _is(beta, "beta", (rows, H), _torch.float32, device)
+    if H > 1 and beta.stride(1) != 1:
+        raise ValueError("the last axis of beta must be dense")
+    return beta.data_ptr() or None, (beta.stride(0) if rows > 1 else 0)
+
+
+def delta_prefill_workspace_size(T, N, G, H, dk, dv, slots, max_seqlen=0) -> int:
+    """Workspace bytes of `delta_prefill` for T rows, N sequences and a pool of `slots` states."""
+    n = _lib().delta_prefill_workspace_size(ctypes.byref(LinShapeArg(T, N, G, H, dk, dv, slots)), max_seqlen)
+    if n == _sz(-1).value:
+        raise ValueError(f"unsupported or invalid shape {(T, N, G, H, dk, dv, slots)}")
+    return int(n)
+
+
+def delta_prefill(q, k, v, log_decay, beta, cu_seqlens, states, *, slots=None, carry=None, max_seqlen=0, out=None,
+                  workspace=None):
+    """y[T,H,dv] of the gated delta rule over a packed batch: `lin_prefill`
+    with S_t = a_t S_{t-1} + k_t u_t^T, u_t = beta_t (v_t - a_t S_{t-1}^T k_t)
+    and beta float32 [T,H].  The other arguments are those of `lin_prefill`."""
+    lib = _lib()
+    code, dev, (T, G, H, dk, dv, S), sp, ld, lp, out, st = _lin_args(q, k, v, log_decay, states, out, "T")
+    bp, lb = _beta_args(beta, T, H, dev)
+    N, cu, max_seqlen = _packed(cu_seqlens, max_seqlen, dev)
+    s = _arg(LinShapeArg, T, N, G, H, dk, dv, S)
+    need = lib.delta_prefill_workspace_size(s, max_seqlen)
+    if need == _sz(-1).value:
+        raise ValueError(f"unsupported or invalid shape: T {T}, N {N}, G {G}, H {H}, dk {dk}, dv {dv}")
+    wp, wn, _keep = _bytes(need, dev, workspace)
+    _call(lib.delta_prefill, "delta_prefill", dev, s, code, st, q.data_ptr() or None, k.data_ptr() or None,
+          v.data_ptr() or None, lp, ld, bp, lb, cu, _ids(slots, "slots", N, dev), _ids(carry, "carry", N, dev),
+          max_seqlen, sp, out.data_ptr() or None, wp, wn)
+    return out
+
+
+def delta_step(q, k, v, log_decay, beta, states, *, slots=None, out=None):
+    """y[N,H,dv] of one step of the gated delta rule for each row: `lin_step`
+    with beta float32 [N,H]."""
+    lib = _lib()
+    code, dev, (N, G, H, dk, dv, S), sp, ld, lp, out, st = _lin_args(q, k, v, log_decay, states, out, "N")
+    bp, lb = _beta_args(beta, N, H, dev)
+    s = _arg(LinShapeArg, 0, N, G, H, dk, dv, S)
+    _call(lib.delta_step, "delta_step", dev, s, code, st, q.data_ptr() or None, k.data_ptr() or None,
+          v.data_ptr() or None, lp, ld, bp, lb, _ids(slots, "slots", N, dev), sp, out.data_ptr() or None)
     return out
 
 

@@ -439,6 +439,41 @@ int lin_step(const lin_shape *shape, int dtype, const lin_strides *strides,
              const float *log_decay, int64_t decay_stride,
              const int32_t *slots, float *states, void *y, void *stream);
 
+/* The gated delta rule over the same packed batches and pools: a layer whose
+ * state takes back what it held under a key before it takes the new value,
+ *     S_t = a_t S_{t-1} + k_t u_t^T,   u_t = beta_t (v_t - a_t S_{t-1}^T k_t),
+ *     y_t = S_t^T q_t,                 a_t = exp(log_decay_t),
+ * which is a_t (I - beta_t k_t k_t^T) S_{t-1} + beta_t k_t v_t^T.  Arguments,
+ * checks, limits and what becomes of indexes are those of lin_prefill and
+ * lin_step, with
+ *   beta          float32: rows of H, beta_stride apart, one for each token
+ *                 and head (0: the same row for all).  Any finite value; with
+ *                 k of length 1 and 0 <= beta <= 1 (and decays of at most 1)
+ *                 no state grows, and outside of that growth and its rounding
+ *                 are the caller's risk.
+ * Rounding: q, k and v in float32 are rounded nowhere.  bfloat16 calls hold
+ * the state, u and all that they come from to float32's accuracy; in y the
+ * masked scores and the copy of the state that meets q are rounded to
+ * bfloat16 too.
+ * Infinite and NaN values of a row reach, as in the recurrence, only it and
+ * the rows after it in its sequence, and one in v no column but its own; a
+ * sequence that holds them is slow from there on, where they reached a state
+ * to its end.  Where the recurrence gives an infinity, NaN may stand.
+ * (T / 32 + N) H < 2^24 besides, and workspaces for every call. */
+size_t delta_prefill_workspace_size(const lin_shape *shape, int64_t max_seqlen);
+int delta_prefill(const lin_shape *shape, int dtype, const lin_strides *strides,
+                  const void *q, const void *k, const void *v,
+                  const float *log_decay, int64_t decay_stride,
+                  const float *beta, int64_t beta_stride,
+                  const int32_t *cu_seqlens, const int32_t *slots, const int32_t *carry,
+                  int64_t max_seqlen, float *states, void *y,
+                  void *workspace, size_t workspace_bytes, void *stream);
+int delta_step(const lin_shape *shape, int dtype, const lin_strides *strides,
+               const void *q, const void *k, const void *v,
+               const float *log_decay, int64_t decay_stride,
+               const float *beta, int64_t beta_stride,
+               const int32_t *slots, float *states, void *y, void *stream);
+
 /* Group norm, channels last, with an activation.  x is N samples of L rows
  * of C channels; the channels are cut into `groups` runs of C / groups, and
  * the mean mu and the variance (over the L rows and the run's channels, the

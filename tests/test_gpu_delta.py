@@ -1,0 +1,225 @@
+"""The gated delta rule on the GPU, element by element against its 64-bit
+form (delta_ref)."""
+import numpy as np
+import pytest
+import torch
+
+import chunked_ssd_scan_fwd_amd as ssd
+import delta_ref as ref
+from gpu_util import need_gpu, say
+from layer_ref import beyond
+from test_gpu_layer import dev, fused, ids, offsets
+
+pytestmark = pytest.mark.gpu
+BF, F16, F32 = torch.bfloat16, torch.float16, torch.float32
+NAN, INF = float("nan"), float("inf")
+
+
+@pytest.fixture(autouse=True)
+def _gpu():
+    need_gpu()
+
+
+def check_prefill(name, heads, dtype, lens, per_token=True, carry=None, slots=None, npool=None, strided=False, tail=0,
+                  max_seqlen=None, change=None, seed=0, **more):
+    G, H, dk, dv = heads
+    say(f"delta_prefill {name} {heads} {dtype} lens {lens[:6]} tail {tail} max {max_seqlen}")
+    N = len(lens)
+    cu = offsets(lens)
+    T = cu[-1] + tail
+    q, k, v, ld, beta, S = ref.inputs(T, G, H, dk, dv, dtype, per_token, seed, npool or max(N, 1), strided, **more)
+    if change is not None:
+        q, k, v, ld, beta, S = change(q, k, v, ld, beta, S)
+    out = torch.full((T, H, dv), 7.0, dtype=dtype, device="cuda")
+    pool = dev(S)
+    move = fused if strided else dev
+    got = ssd.delta_prefill(move(q), move(k), move(v), dev(ld), dev(beta), ids(cu), pool,
+                            slots=None if slots is None else ids(slots), carry=None if carry is None else ids(carry),
+                            max_seqlen=max(lens, default=0) if max_seqlen is None else max_seqlen, out=out)
+    torch.cuda.synchronize()
+    y, S1, ye, Se, ym = ref.rule(q, k, v, ld, beta, cu, S, slots, carry)
+    e = beyond(got[:cu[-1]], y[:cu[-1]], ref.y_bound(dtype, y, ye, ym)[:cu[-1]])
+    es = beyond(pool, S1, Se + 1e-30)
+    say(f"  y {e:.3f} states {es:.3f} of the bound")
+    assert e <= 1 and es <= 1
+    assert bool((got[cu[-1]:] == 7.0).all())
+    untouched = sorted(set(range(S.shape[0])) - set(range(N) if slots is None else slots))
+    assert torch.equal(pool.cpu()[untouched], S[untouched])
+    return got, pool
+
+
+HEADS = [(1, 1, 128, 128), (2, 4, 48, 40), (2, 8, 128, 128), (1, 6, 128, 64), (3, 3, 64, 64), (1, 2, 256, 128),
+         (1, 2, 64, 256), (1, 1, 256, 256), (1, 2, 1, 1), (1, 3, 33, 97), (2, 2, 5, 200), (1, 1, 200, 3), (1, 1, 130, 129)]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF, F16])
+@pytest.mark.parametrize("heads", HEADS)
+def test_prefill_heads(heads, dtype):
+    check_prefill("heads", heads, dtype, [1, 64, 130, 63, 65], per_token=heads[2] != 64, carry=[1, 0, 1, 0, 1],
+                  slots=[4, 2, 0, 5, 1], npool=7, tail=3, seed=heads[2] * 7 + heads[3])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("n", [1, 2, 15, 16, 17, 31, 32, 33, 47, 48, 49, 63, 64, 65, 127, 128, 129, 200])
+def test_prefill_lengths(n, dtype):
+    check_prefill("length", (1, 2, 64, 128), dtype, [n], seed=n)
+    check_prefill("length", (2, 2, 128, 64), dtype, [n, 3], per_token=False, seed=n)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF, F16])
+@pytest.mark.parametrize("heads", [(2, 4, 48, 40), (1, 3, 128, 128), (1, 2, 33, 97)])
+def test_prefill_slices_of_a_projection(heads, dtype):
+    check_prefill("strides", heads, dtype, [70, 0, 100], strided=True, seed=3)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("near", [0.5, 0.9, 1.0])
+def test_prefill_near_keys(near, dtype):
+    """Keys that are nearly or quite the same: the inverse's powers would be huge."""
+    def change(q, k, v, ld, beta, S):
+        return q, k, v, ld, torch.ones_like(beta) if near == 1.0 else beta, S
+    check_prefill("near", (1, 2, 128, 128), dtype, [64, 150], near=near, mu=-8.0, seed=4, change=change)
+    check_prefill("near", (1, 2, 64, 64), dtype, [64, 150], near=near, mu=-8.0, seed=5, change=change)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("kind", ["beta 0", "beta 1", "beta 2", "beta mixed", "long keys", "no keys", "forget", "all",
+                                  "growth", "strong", "none", "same decay and beta"])
+def test_prefill_betas_and_decays(kind, dtype):
+    def change(q, k, v, ld, beta, S):
+        ld, beta = ld.clone(), beta.clone()
+        if kind.startswith("beta"):
+            beta[:] = {"0": 0.0, "1": 1.0, "2": 2.0}.get(kind[5:], 0.0)
+            if kind == "beta mixed":
+                beta[::3] = 1.0
+        elif kind == "long keys":
+            k = (k.float() * 1.3).to(k.dtype)
+        elif kind == "no keys":
+            k = k.clone()
+            k[::2] = 0
+        elif kind == "forget":   # the state is forgotten here and there, twice in a chunk too
+            ld[[0, 10, 64, 70, 71, 130]] = -np.inf
+        elif kind == "all":
+            ld[:] = -np.inf
+        elif kind == "growth":
+            ld[:] = ld.abs() * 0.3
+        elif kind == "strong":
+            ld[:] = -60.0 + ld
+        elif kind == "none":
+            ld[:] = 0
+        else:
+            ld, beta = ld[:1].expand_as(ld), beta[:1].expand_as(beta)
+        return q, k, v, ld, beta, S
+    for heads in ((1, 2, 128, 128), (2, 4, 64, 48)):
+        check_prefill(kind, heads, dtype, [150, 70], seed=8, change=change)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF, F16])
+def test_prefill_empty_and_missing(dtype):
+    """Sequences of no rows, no slots, slots that cannot be used; rows of no sequence."""
+    G, H, dk, dv = 1, 2, 64, 128
+    check_prefill("empty", (G, H, dk, dv), dtype, [0, 5, 0, 0, 70, 0], carry=[0, 1, 1, 0, 0, 1], seed=1, tail=2)
+    lens = [40, 30, 20, 10]
+    q, k, v, ld, beta, S = (dev(t) for t in ref.inputs(100, G, H, dk, dv, dtype, True, 2, 4))
+    pool = S.clone()
+    y = ssd.delta_prefill(q, k, v, ld, beta, ids(offsets(lens)), pool, slots=ids([-1, 2, 2, 9]))
+    assert bool(torch.isnan(y[70:]).all()) and bool(torch.isfinite(y[:70]).all())
+    want, S1, ye, Se, ym = ref.rule(q[:70], k[:70], v[:70], ld[:70], beta[:70], offsets(lens[:2]), S, [-1, 2])
+    assert beyond(y[:70], want, ref.y_bound(dtype, want, ye, ym)) <= 1
+    assert beyond(pool, S1, Se + 1e-30) <= 1
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("where", ["q", "k", "v", "beta", "decay", "state"])
+@pytest.mark.parametrize("bad", [NAN, INF])
+def test_prefill_infinities_and_nan(where, bad, dtype):
+    """They reach the rows after them, in v only their column."""
+    for heads in ((1, 2, 128, 128), (1, 2, 64, 64)):
+        G, H, dk, dv = heads
+        q, k, v, ld, beta, S = ref.inputs(200, G, H, dk, dv, dtype, True, 9, 2)
+        clean = [dev(t) for t in (q, k, v, ld, beta)], dev(S)
+        want = ssd.delta_prefill(*clean[0], ids([0, 90, 200]), clean[1])
+        row, col = 131, 7
+        t = {"q": q, "k": k, "v": v, "beta": beta, "decay": ld, "state": S}[where]
+        if where in ("q", "k"):
+            t[row, 0, col] = bad
+        elif where == "v":
+            t[row, 1, col] = bad
+        elif where == "state":
+            t[1, 1, 3, col] = bad
+        else:
+            t[row, 1] = bad
+        say(f"delta_prefill {where} {bad} {heads} {dtype}")
+        pool = dev(S)
+        y = ssd.delta_prefill(*(dev(x) for x in (q, k, v, ld, beta)), ids([0, 90, 200]), pool)
+        y, want = y.cpu(), want.cpu()
+        assert torch.equal(y[:90], want[:90])
+        if where in ("v", "state"):
+            rest = [c for c in range(dv) if c != col]
+            assert torch.equal(y[:, 0], want[:, 0])
+            # the other columns of the wave go row by row from there on: the same to rounding
+            assert bool(torch.isfinite(y[:, 1][:, rest]).all())
+            d = (y[:, 1][:, rest].double() - want[:, 1][:, rest].double()).abs().max()
+            assert d < 0.05
+        if where != "state":
+            first = row if where != "q" else row
+            assert bool(torch.isfinite(y[:first]).all())
+            assert float((y[:first].double() - want[:first].double()).abs().max()) < 0.05
+        if where == "q":
+            assert bool(torch.isfinite(y[row + 1:]).all()) and bool(torch.isfinite(pool).all())
+            assert not bool(torch.isfinite(y[row]).any())
+        elif where == "state":
+            assert not bool(torch.isfinite(pool[1, 1, 3, col]))
+        else:
+            assert not bool(torch.isfinite(pool[1, 1, :, col]).all())
+
+
+@pytest.mark.parametrize("dtype", [F32, BF, F16])
+@pytest.mark.parametrize("heads", HEADS + [(1, 3, 128, 68), (2, 2, 64, 32)])
+def test_step_heads(heads, dtype):
+    G, H, dk, dv = heads
+    for N, slots in ((1, [2]), (5, [4, 6, 0, -1, 1]), (300, None)):
+        if N == 300 and dk * dv > 20000:
+            continue
+        npool = 7 if N < 8 else 300
+        q, k, v, ld, beta, S = ref.inputs(N, G, H, dk, dv, dtype, N != 5, 3 + N, npool)
+        pool = dev(S)
+        out = torch.full((N, H, dv), 7.0, dtype=dtype, device="cuda")
+        say(f"delta_step {heads} {dtype} {N}")
+        y = ssd.delta_step(*(dev(t) for t in (q, k, v, ld, beta)), pool, slots=None if slots is None else ids(slots),
+                           out=out)
+        rows = list(range(N)) if slots is None else slots
+        want, S1, ye, Se, ym = ref.rule(q, k, v, ld, beta, list(range(N + 1)), S, rows)
+        live = [n for n in range(N) if rows[n] >= 0]
+        assert beyond(y[live], want[live], ref.y_bound(dtype, want, ye, ym, False)[live]) <= 1
+        assert beyond(pool, S1, Se + 1e-30) <= 1
+        assert bool((y[[n for n in range(N) if rows[n] < 0]] == 7.0).all())
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_step_repeated_missing_and_padded_slots(dtype):
+    G, H, dk, dv = 1, 3, 64, 96
+    slots = [3, 1, 3, -1, 5, 3, 1, 99]
+    q, k, v, ld, beta, S = ref.inputs(8, G, H, dk, dv, dtype, True, 6, 6)
+    pool = dev(S)
+    out = torch.full((8, H, dv), 7.0, dtype=dtype, device="cuda")
+    y = ssd.delta_step(*(dev(t) for t in (q, k, v, ld, beta)), pool, slots=ids(slots), out=out)
+    want, S1, ye, Se, ym = ref.rule(q[:7], k[:7], v[:7], ld[:7], beta[:7], list(range(8)), S, slots[:7])
+    live = [0, 1, 2, 4, 5, 6]
+    assert beyond(y[live], want[live], ref.y_bound(dtype, want, ye, ym, False)[live]) <= 1
+    assert beyond(pool, S1, Se + 1e-30) <= 1
+    assert bool((y[3] == 7.0).all()) and bool(torch.isnan(y[7]).all())
+
+
+def test_steps_go_on_from_a_prefill():
+    """A prompt at once, and its last rows one by one, give the same as the whole."""
+    for dtype in (F32, BF):
+        G, H, dk, dv = 2, 4, 64, 64
+        q, k, v, ld, beta, S = ref.inputs(80, G, H, dk, dv, dtype, True, 12, 1)
+        pool = dev(S)
+        d = [dev(t) for t in (q, k, v, ld, beta)]
+        ssd.delta_prefill(*(t[:70] for t in d), ids([0, 70]), pool)
+        ys = [ssd.delta_step(*(t[i:i + 1] for t in d), pool) for i in range(70, 80)]
+        want, S1, ye, Se, ym = ref.rule(q, k, v, ld, beta, [0, 80], S)
+        assert beyond(torch.cat(ys), want[70:], ref.y_bound(dtype, want, ye, ym, False)[70:]) <= 1
+        assert beyond(pool, S1, Se + 1e-30) <= 1
