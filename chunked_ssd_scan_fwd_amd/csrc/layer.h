@@ -19,9 +19,11 @@ constexpr int64_t max_blocks(int threads) { return ((int64_t(1) << 32) - 1) / th
 int check_dtype(int dtype);
 int check_lin(const lin_shape *s, bool step);
 int check_delta(const lin_shape *s, bool step);
+int check_delta_bwd(const lin_shape *s);
 // The strides to use (dense ones where `st` is null) for `rows` rows, or
-// SSD_ERR_SHAPE where they are out of range or let values of y overlap.
-int resolve_strides(const lin_shape *s, const lin_strides *st, lin_strides *out, int64_t rows);
+// SSD_ERR_SHAPE where they are out of range or, where y is written, let values
+// of it overlap.
+int resolve_strides(const lin_shape *s, const lin_strides *st, lin_strides *out, int64_t rows, bool written = true);
 int check_gn(const gn_shape *s, int act);
 int check_cache(const state_cache_shape *s);
 inline bool misaligned(const void *p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }

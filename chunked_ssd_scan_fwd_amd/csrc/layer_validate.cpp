@@ -32,7 +32,17 @@ int check_delta(const lin_shape *s, bool step)
     return s->T / 32 + s->N > max_blocks(256) / s->H ? SSD_ERR_SHAPE : SSD_OK;
 }
 
-int resolve_strides(const lin_shape *s, const lin_strides *st, lin_strides *o, int64_t rows)
+int check_delta_bwd(const lin_shape *s)
+{
+    const int rc = check_delta(s, false);
+    if (rc != SSD_OK) return rc;
+    // both walks of a sequence in one launch, and four columns of a row's q to a thread
+    const int64_t tiles = (s->dv + 63) / 64;
+    if (s->N > max_blocks(512) / (2 * s->H * tiles)) return SSD_ERR_SHAPE;
+    return s->G != s->H && s->T > max_blocks(256) * 256 / (s->G * s->dk) ? SSD_ERR_SHAPE : SSD_OK;
+}
+
+int resolve_strides(const lin_shape *s, const lin_strides *st, lin_strides *o, int64_t rows, bool written)
 {
     if (!st) {
         *o = {s->G * s->dk, s->dk, s->G * s->dk, s->dk, s->H * s->dv, s->dv, s->H * s->dv, s->dv};
@@ -43,6 +53,7 @@ int resolve_strides(const lin_shape *s, const lin_strides *st, lin_strides *o, i
         if (x < 0 || x >= kMaxCount) return SSD_ERR_SHAPE;
     for (int64_t x : {o->q_g, o->k_g, o->v_h, o->y_h})
         if (x < 0 || x >= (int64_t(1) << 40)) return SSD_ERR_SHAPE;
+    if (!written) return SSD_OK;
     // two values of y never share their place: heads inside rows, or rows inside heads
     const int64_t d = s->dv, H = s->H;
     const bool in_rows = (H == 1 || o->y_h >= d) && (rows <= 1 || o->y_t >= (H == 1 ? 0 : (H - 1) * o->y_h) + d);

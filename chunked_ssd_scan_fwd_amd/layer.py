@@ -16,6 +16,7 @@ from __future__ import annotations
 import ctypes
 
 __all__ = ["lin_prefill", "lin_step", "gn_fwd", "gn_bwd", "state_pack", "state_unpack", "delta_prefill", "delta_step",
+           "delta_bwd", "delta_bwd_workspace_size",
            "lin_prefill_workspace_size", "delta_prefill_workspace_size", "gn_workspace_size", "STATE_CACHE_BLOCK"]
 
 STATE_CACHE_BLOCK = 32   # values of a state's row that share a scale byte
@@ -55,6 +56,10 @@ def declare(lib):
     lib.delta_prefill.argtypes = [lp, _int, tp, _vp, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _vp, _vp, _vp,
                                   _sz, _vp]
     lib.delta_step.argtypes = [lp, _int, tp, _vp, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp]
+    lib.delta_bwd_workspace_size.argtypes = [lp]
+    lib.delta_bwd_workspace_size.restype = _sz
+    lib.delta_bwd.argtypes = [lp, _int, tp, _vp, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                              _int, _vp, _vp, _vp, _sz, _vp]
     for fn in (lib.gn_fwd_workspace_size, lib.gn_bwd_workspace_size):
         fn.argtypes = [gp]
         fn.restype = _sz
@@ -64,7 +69,7 @@ def declare(lib):
     lib.state_pack.argtypes = [cp, _vp, _vp, _vp, _vp, _vp, _vp]
     lib.state_unpack.argtypes = [cp, _vp, _vp, _vp, _vp, _vp, _vp]
     for fn in (lib.lin_prefill, lib.lin_step, lib.gn_fwd, lib.gn_bwd, lib.state_pack, lib.state_unpack,
-               lib.delta_prefill, lib.delta_step):
+               lib.delta_prefill, lib.delta_step, lib.delta_bwd):
         fn.restype = _int
 
 
@@ -307,6 +312,71 @@ def delta_step(q, k, v, log_decay, beta, states, *, slots=None, out=None):
     _call(lib.delta_step, "delta_step", dev, s, code, st, q.data_ptr() or None, k.data_ptr() or None,
           v.data_ptr() or None, lp, ld, bp, lb, _ids(slots, "slots", N, dev), sp, out.data_ptr() or None)
     return out
+
+
+def delta_bwd_workspace_size(T, N, G, H, dk, dv) -> int:
+    """Workspace bytes of `delta_bwd` for T rows and N sequences."""
+    n = _lib().delta_bwd_workspace_size(ctypes.byref(LinShapeArg(T, N, G, H, dk, dv, N)))
+    if n == _sz(-1).value:
+        raise ValueError(f"unsupported or invalid shape {(T, N, G, H, dk, dv)}")
+    return int(n)
+
+
+def delta_bwd(q, k, v, log_decay, beta, cu_seqlens, dy, *, states=None, dstates=None, max_seqlen=0, out=None,
+              workspace=None):
+    """(dq, dk, dv, dlog_decay, dbeta, dstates0): the gradients of
+    sum(dy * y) + sum(dstates * last states) for `delta_prefill` of the same
+    batch whose sequence n starts from states[n] (float32 [N,H,dk,dv]; None:
+    zero, and dstates0 is None).  dy [T,H,dv], its last axis dense; dstates
+    float32 [N,H,dk,dv] or None.  dlog_decay has log_decay's shape: [T,H], or
+    [H] summed over the rows.  ``out``: the six (or, without states, five)
+    tensors to write, dense; gradients of rows of no sequence are left as they
+    are in it (zero without it).  max_seqlen is not needed."""
+    lib = _lib()
+    code = _dtype_of(q, "q")
+    dev, dt = q.get_device(), q.dtype
+    for t, name in ((v, "v"), (log_decay, "log_decay")):
+        if not isinstance(t, _torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+    if q.dim() != 3 or v.dim() != 3:
+        raise ValueError("q must be [T,G,dk] and v [T,H,dv]")
+    (T, G, dk), (_, H, dv) = q.shape, v.shape
+    _is(k, "k", (T, G, dk), dt, dev)
+    _is(v, "v", (T, H, dv), dt, dev)
+    _is(dy, "dy", (T, H, dv), dt, dev)
+    by_row = log_decay.dim() != 1
+    _is(log_decay, "log_decay", (T, H) if by_row else (H,), _torch.float32, dev)
+    if H > 1 and log_decay.stride(-1) != 1:
+        raise ValueError("the last axis of log_decay must be dense")
+    ld = log_decay.stride(0) if by_row and T > 1 else 0
+    bp, lb = _beta_args(beta, T, H, dev)
+    N, cu, _ = _packed(cu_seqlens, max_seqlen, dev)
+    st = (N, H, dk, dv)
+    sp, dsp = (None if t is None else _dense(t, name, st, _torch.float32, dev)
+               for t, name in ((states, "states"), (dstates, "dstates")))
+    if out is None:
+        # rows of no sequence get no gradient; where the last offset ends is known on the device alone
+        new = v.new_zeros
+        dq, dk_, dv_ = new((T, G, dk)), new((T, G, dk)), new((T, H, dv))
+        dla = new(log_decay.shape, dtype=_torch.float32)
+        dbeta = new((T, H), dtype=_torch.float32)
+        d0 = None if states is None else v.new_empty(st, dtype=_torch.float32)
+    else:
+        dq, dk_, dv_, dla, dbeta, d0 = tuple(out) if states is not None else (*tuple(out)[:5], None)
+    ptrs = [_dense(t, name, shape, kind, dev) for t, name, shape, kind in (
+        (dq, "dq", (T, G, dk), dt), (dk_, "dk", (T, G, dk), dt), (dv_, "dv", (T, H, dv), dt),
+        (dla, "dlog_decay", tuple(log_decay.shape), _torch.float32), (dbeta, "dbeta", (T, H), _torch.float32))]
+    d0p = None if d0 is None else _dense(d0, "dstates0", st, _torch.float32, dev)
+    s = _arg(LinShapeArg, T, N, G, H, dk, dv, N)
+    need = lib.delta_bwd_workspace_size(s)
+    if need == _sz(-1).value:
+        raise ValueError(f"unsupported or invalid shape: T {T}, N {N}, G {G}, H {H}, dk {dk}, dv {dv}")
+    wp, wn, _keep = _bytes(need, dev, workspace)
+    strides = _arg(LinStridesArg, *_rows(q, "q"), *_rows(k, "k"), *_rows(v, "v"), *_rows(dy, "dy"))
+    _call(lib.delta_bwd, "delta_bwd", dev, s, code, strides, q.data_ptr() or None, k.data_ptr() or None,
+          v.data_ptr() or None, log_decay.data_ptr() or None, ld, bp, lb, cu, sp, dy.data_ptr() or None, dsp, *ptrs[:4],
+          int(by_row), ptrs[4], d0p, wp, wn)
+    return dq, dk_, dv_, dla, dbeta, d0
 
 
 def _gn_rows(t, name, shape, dtype, device):

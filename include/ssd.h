@@ -474,6 +474,33 @@ int delta_step(const lin_shape *shape, int dtype, const lin_strides *strides,
                const float *beta, int64_t beta_stride,
                const int32_t *slots, float *states, void *y, void *stream);
 
+/* The gradients of sum(dy * y) + sum(dstates_last * last states) for
+ * delta_prefill of the same batch, in which sequence n starts from states[n]
+ * (NULL: from zero): dq, dk [T][G][dk] (summed over the heads of a group) and
+ * dv [T][H][dv], dense, of the type `dtype`; dlog_decay, rows of H where
+ * decay_by_row is not 0, else [H], summed over all rows (in 64 bits, in a
+ * fixed order); dbeta [T][H]; dstates [N][H][dk][dv], or NULL if not wanted.
+ * states and dstates_last are float32 [N][H][dk][dv] or NULL; the strides of
+ * y are dy's, and may be 0 here.  shape->slots is not read.  Rows of no
+ * sequence are not read, and their gradients are left as they were.
+ * Every sum and every value between is float32, or three bfloat16 numbers
+ * that hold one; nothing of a forward call is needed.  The states of every
+ * 64th row (32nd for dk over 128) are kept in the workspace meanwhile, twice.
+ * An infinity or a NaN reaches gradients of its sequence in the heads of its
+ * group, and dlog_decay of those heads where that is a sum, no others; where
+ * the formulas give an infinity, NaN may stand.
+ * Limits as for delta_prefill, 2 N H ceil(dv / 64) < 2^23, and T G dk < 2^32
+ * where heads share q and k. */
+size_t delta_bwd_workspace_size(const lin_shape *shape);
+int delta_bwd(const lin_shape *shape, int dtype, const lin_strides *strides,
+              const void *q, const void *k, const void *v,
+              const float *log_decay, int64_t decay_stride,
+              const float *beta, int64_t beta_stride, const int32_t *cu_seqlens,
+              const float *states, const void *dy, const float *dstates_last,
+              void *dq, void *dk, void *dv, float *dlog_decay, int decay_by_row,
+              float *dbeta, float *dstates,
+              void *workspace, size_t workspace_bytes, void *stream);
+
 /* Group norm, channels last, with an activation.  x is N samples of L rows
  * of C channels; the channels are cut into `groups` runs of C / groups, and
  * the mean mu and the variance (over the L rows and the run's channels, the

@@ -223,3 +223,178 @@ def test_steps_go_on_from_a_prefill():
         want, S1, ye, Se, ym = ref.rule(q, k, v, ld, beta, [0, 80], S)
         assert beyond(torch.cat(ys), want[70:], ref.y_bound(dtype, want, ye, ym, False)[70:]) <= 1
         assert beyond(pool, S1, Se + 1e-30) <= 1
+
+
+# ---- gradients
+
+
+def check_bwd(name, heads, dtype, lens, per_token=True, entered=True, strided=False, tail=0, change=None, seed=0, **more):
+    G, H, dk, dv = heads
+    say(f"delta_bwd {name} {heads} {dtype} lens {lens[:6]} tail {tail}")
+    N, cu = len(lens), offsets(lens)
+    T = cu[-1] + tail
+    q, k, v, ld, beta, S = ref.inputs(T, G, H, dk, dv, dtype, per_token, seed, N, strided, **more)
+    g = torch.Generator().manual_seed(seed + 100)
+    dy, dS = torch.randn(T, H, dv, generator=g).to(dtype), torch.randn(N, H, dk, dv, generator=g) * 0.5
+    if change is not None:
+        q, k, v, ld, beta, S, dy, dS = change(q, k, v, ld, beta, S, dy, dS)
+    if not entered:
+        S = dS = None
+    move = fused if strided else dev
+    opt = lambda t: None if t is None else dev(t)   # noqa: E731
+    got = ssd.delta_bwd(move(q), move(k), move(v), dev(ld), dev(beta), ids(cu), dev(dy), states=opt(S), dstates=opt(dS))
+    torch.cuda.synchronize()
+    want, err = ref.gradients(q, k, v, ld, beta, cu, dy, S, dS)
+    worst = {}
+    for n, t in zip(("dq", "dk", "dv", "dlog_decay", "dbeta", "dstates"), got):
+        if n == "dstates" and not entered:
+            assert t is None
+            continue
+        kind = dtype if n in ("dq", "dk", "dv") else F32
+        assert t.shape == want[n].shape and t.dtype == kind
+        worst[n] = round(beyond(t, want[n], ref.gradient_bound(kind, want[n], err[n])), 4)
+        # The bounds above add magnitudes over columns; the errors themselves do not line up.  As a whole, in the
+        # 2-norm, a gradient is within its own rounding and 2^-15, which is 32 of the steps that the bounds count.
+        size = float(want[n].norm())
+        if size > 0:
+            off = float((t.detach().cpu().double() - want[n]).norm()) / size
+            assert off <= ref.HALF[kind] + 2.0 ** -15, (n, off)
+    say(f"  {worst}")
+    assert max(worst.values()) <= 1, worst
+    return got
+
+
+@pytest.mark.parametrize("dtype", [F32, BF, F16])
+@pytest.mark.parametrize("heads", HEADS)
+def test_bwd_heads(heads, dtype):
+    check_bwd("heads", heads, dtype, [1, 64, 130, 63, 65], per_token=heads[2] != 64, entered=heads[3] != 64, tail=3,
+              seed=heads[2] * 7 + heads[3])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("n", [1, 2, 15, 16, 17, 31, 32, 33, 47, 48, 49, 63, 64, 65, 95, 96, 97, 127, 128, 129, 200])
+def test_bwd_lengths(n, dtype):
+    check_bwd("length", (1, 2, 64, 128), dtype, [n], seed=n)
+    check_bwd("length", (2, 2, 128, 64), dtype, [n, 3], per_token=False, seed=n)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_bwd_empty_sequences(dtype):
+    check_bwd("empty", (1, 2, 64, 64), dtype, [0, 5, 0, 0, 70, 0], tail=2, seed=1)
+    got = check_bwd("no rows", (1, 2, 16, 16), dtype, [0, 0], seed=1, per_token=False)
+    assert bool((got[3] == 0).all())
+    check_bwd("no rows", (1, 2, 16, 16), dtype, [0, 0], seed=1)
+    check_bwd("no sequences", (1, 2, 16, 16), dtype, [], seed=1, per_token=False)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF, F16])
+@pytest.mark.parametrize("heads", [(2, 4, 48, 40), (1, 3, 128, 128), (1, 2, 33, 97)])
+def test_bwd_slices_of_a_projection(heads, dtype):
+    check_bwd("strides", heads, dtype, [70, 0, 100], strided=True, seed=3)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("kind", ["beta 0", "beta 1", "beta 2", "beta mixed", "long keys", "no keys", "near keys", "same keys",
+                                  "forget", "all", "growth", "strong", "none", "same decay and beta", "one row of dy"])
+def test_bwd_betas_and_decays(kind, dtype):
+    def change(q, k, v, ld, beta, S, dy, dS):
+        ld, beta = ld.clone(), beta.clone()
+        if kind.startswith("beta"):
+            beta[:] = {"0": 0.0, "1": 1.0, "2": 2.0}.get(kind[5:], 0.0)
+            if kind == "beta mixed":
+                beta[::3] = 1.0
+        elif kind == "long keys":
+            k = (k.float() * 1.3).to(k.dtype)
+        elif kind == "no keys":
+            k = k.clone()
+            k[::2] = 0
+        elif kind == "same keys":
+            beta[:] = 1
+        elif kind == "forget":
+            ld[[0, 10, 64, 70, 71, 130]] = -np.inf
+        elif kind == "all":
+            ld[:] = -np.inf
+        elif kind == "growth":
+            ld[:] = ld.abs() * 0.3
+        elif kind == "strong":
+            ld[:] = -60.0 + ld
+        elif kind == "none":
+            ld[:] = 0
+        elif kind == "one row of dy":
+            dy = dy[:1].expand_as(dy)
+        else:
+            ld, beta = ld[:1].expand_as(ld), beta[:1].expand_as(beta)
+        return q, k, v, ld, beta, S, dy, dS
+    near = {"near keys": 0.9, "same keys": 1.0}.get(kind, 0.0)
+    for heads in ((1, 2, 128, 128), (2, 4, 64, 48)):
+        check_bwd(kind, heads, dtype, [150, 70], seed=8, change=change, near=near, mu=-8.0 if near else -4.0)
+
+
+def test_bwd_against_differences():
+    """The gradients against differences of delta_prefill itself, in float32."""
+    G, H, dk, dv = 2, 4, 24, 20
+    cu = [0, 70, 100]
+    q, k, v, ld, beta, S = (dev(t) for t in ref.inputs(100, G, H, dk, dv, F32, True, 21, 2))
+    g = torch.Generator().manual_seed(4)
+    dy, dS = dev(torch.randn(100, H, dv, generator=g)), dev(torch.randn(2, H, dk, dv, generator=g))
+    got = ssd.delta_bwd(q, k, v, ld, beta, ids(cu), dy, states=S, dstates=dS)
+
+    def loss(x):
+        pool = x[5].clone()
+        y = ssd.delta_prefill(*x[:5], ids(cu), pool)
+        return float((y.double() * dy).sum() + (pool.double() * dS).sum())
+
+    x = [q, k, v, ld, beta, S]
+    for i, grad in enumerate(got):
+        d = dev(torch.randn(x[i].shape, generator=g))
+        h = 2.0 ** -6 / float(d.norm() / x[i].norm()) / 8
+        num = (loss(x[:i] + [x[i] + h * d] + x[i + 1:]) - loss(x[:i] + [x[i] - h * d] + x[i + 1:])) / (2 * h)
+        want = float((grad.double() * d).sum())
+        # the differences' own error: their third-order term, and float32's in the two losses
+        assert abs(num - want) <= 2e-3 * float(grad.double().norm() * d.double().norm()), (i, num, want)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("where", ["q", "k", "v", "beta", "decay", "dy", "state", "dstate"])
+def test_bwd_nan_stays_in_its_sequence(where, dtype):
+    G, H, dk, dv = 2, 4, 64, 64
+    cu = [0, 90, 200, 260]
+    q, k, v, ld, beta, S = ref.inputs(260, G, H, dk, dv, dtype, True, 9, 3)
+    g = torch.Generator().manual_seed(4)
+    dy, dS = torch.randn(260, H, dv, generator=g).to(dtype), torch.randn(3, H, dk, dv, generator=g)
+    x = {"q": q, "k": k, "v": v, "beta": beta, "decay": ld, "dy": dy, "state": S, "dstate": dS}
+    run = lambda: [t.cpu() for t in ssd.delta_bwd(dev(q), dev(k), dev(v), dev(ld), dev(beta), ids(cu), dev(dy),   # noqa: E731
+                                                  states=dev(S), dstates=dev(dS))]
+    want = run()
+    t = x[where]
+    if where in ("state", "dstate"):
+        t[1, 1, 3, 5] = NAN
+    else:
+        t[131, 0 if where == "q" or where == "k" else 1] = NAN
+    got = run()
+    for i, (a, b) in enumerate(zip(got, want)):
+        if i == 5:
+            assert torch.equal(a[[0, 2]], b[[0, 2]]) and torch.equal(a[1, 2:], b[1, 2:])
+            continue
+        assert torch.equal(a[:90], b[:90]) and torch.equal(a[200:], b[200:])
+        n = a.shape[1] // G   # the other group
+        assert torch.equal(a[:, n:], b[:, n:])
+    assert not bool(torch.isfinite(got[4][90:200]).all()) or where == "q"
+
+
+def test_bwd_out_and_rows_of_no_sequence():
+    G, H, dk, dv = 1, 3, 40, 24
+    q, k, v, ld, beta, S = (dev(t) for t in ref.inputs(90, G, H, dk, dv, BF, True, 2, 2))
+    cu = ids([5, 60, 80])
+    dy = torch.ones_like(v)
+    first = ssd.delta_bwd(q, k, v, ld, beta, cu, dy, states=S)
+    out = [torch.full_like(t, 7.0) for t in first]
+    ws = torch.full((ssd.layer.delta_bwd_workspace_size(90, 2, G, H, dk, dv),), 255, dtype=torch.uint8, device="cuda")
+    again = ssd.delta_bwd(q, k, v, ld, beta, cu, dy, states=S, out=out, workspace=ws)
+    for a, b, o in zip(first, again, out):
+        assert b is o
+        if a.shape[0] == 90:
+            assert torch.equal(a[5:80], b[5:80]) and bool((a[:5] == 0).all()) and bool((a[80:] == 0).all())
+            assert bool((b[:5] == 7).all()) and bool((b[80:] == 7).all())
+        else:
+            assert torch.equal(a, b)
