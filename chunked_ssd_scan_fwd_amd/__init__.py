@@ -20,12 +20,13 @@ import ctypes
 import os
 
 from . import layer
-from .layer import delta_bwd, delta_prefill, delta_step, gn_bwd, gn_fwd, lin_prefill, lin_step, state_pack, state_unpack
+from .layer import (beam_select, delta_bwd, delta_prefill, delta_step, gn_bwd, gn_fwd, lin_prefill, lin_step,
+                    state_pack, state_reorder, state_unpack)
 
 __all__ = ["fwd", "bwd", "library", "ShapeArg", "SsdError", "workspace_size",
            "workspace_layout", "KernelTimer", "CHUNK", "bwd_from_fwd", "WS_REGIONS", "fwd_noalloc",
            "NOALLOC_WORKSPACE_BYTES", "lin_prefill", "lin_step", "gn_fwd", "gn_bwd", "state_pack", "state_unpack",
-           "delta_prefill", "delta_step", "delta_bwd"]
+           "delta_prefill", "delta_step", "delta_bwd", "beam_select", "state_reorder"]
 
 CHUNK = 64
 WS_REGIONS = 4   # SSD_WS_REGIONS: decay weights, states, dstates, split partial sums

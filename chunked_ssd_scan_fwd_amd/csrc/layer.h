@@ -26,6 +26,8 @@ int check_delta_bwd(const lin_shape *s);
 int resolve_strides(const lin_shape *s, const lin_strides *st, lin_strides *out, int64_t rows, bool written = true);
 int check_gn(const gn_shape *s, int act);
 int check_cache(const state_cache_shape *s);
+int check_beam(const beam_shape *s);
+int check_reorder(const state_reorder_shape *s);
 inline bool misaligned(const void *p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
 inline unsigned dtype_size(int dtype) { return dtype == LAYER_F32 ? 4u : 2u; }
 

@@ -81,4 +81,24 @@ int check_cache(const state_cache_shape *s)
     return SSD_OK;
 }
 
+int check_beam(const beam_shape *s)
+{
+    if (!s) return SSD_ERR_NULL;
+    if (s->requests < 0 || s->beams < 1 || s->vocabulary < 1 || s->n < 1) return SSD_ERR_SHAPE;
+    if (s->beams > BEAM_MAX || s->n > BEAM_MAX) return SSD_ERR_UNSUPPORTED;
+    if (s->requests >= kMaxCount || s->vocabulary > ((int64_t(1) << 31) - 1) / s->beams) return SSD_ERR_SHAPE;
+    // a wave for 2048 logits or more
+    const int64_t pieces = (s->vocabulary + 2047) / 2048;
+    return s->requests * s->beams > max_blocks(256) / pieces ? SSD_ERR_SHAPE : SSD_OK;
+}
+
+int check_reorder(const state_reorder_shape *s)
+{
+    if (!s) return SSD_ERR_NULL;
+    if (s->requests < 0 || s->beams < 1 || s->slots < 0 || s->H < 1 || s->dk < 1 || s->dv < 1) return SSD_ERR_SHAPE;
+    if (s->beams > BEAM_MAX || s->dk > kMaxHeadDim || s->dv > kMaxHeadDim) return SSD_ERR_UNSUPPORTED;
+    if (s->requests >= kMaxCount || s->slots >= kMaxCount || s->H >= 65536) return SSD_ERR_SHAPE;
+    return SSD_OK;
+}
+
 }  // namespace layer

@@ -1,5 +1,5 @@
 """Operators of a linear-attention layer: Python binding of the lin_, delta_,
-gn_ and state_ calls of ``ssd.h``.
+gn_, state_ and beam_ calls of ``ssd.h``.
 
 Like the rest of the binding it only marshals arguments: every step runs in
 the library's HIP kernels, on PyTorch's current stream of the inputs' device,
@@ -16,9 +16,10 @@ from __future__ import annotations
 import ctypes
 
 __all__ = ["lin_prefill", "lin_step", "gn_fwd", "gn_bwd", "state_pack", "state_unpack", "delta_prefill", "delta_step",
-           "delta_bwd", "delta_bwd_workspace_size",
+           "delta_bwd", "delta_bwd_workspace_size", "beam_select", "beam_select_workspace_size", "state_reorder", "BEAM_MAX",
            "lin_prefill_workspace_size", "delta_prefill_workspace_size", "gn_workspace_size", "STATE_CACHE_BLOCK"]
 
+BEAM_MAX = 64            # most beams of a request, and most candidates taken
 STATE_CACHE_BLOCK = 32   # values of a state's row that share a scale byte
 _i64, _vp, _sz, _int = ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int
 _torch = None
@@ -42,6 +43,14 @@ class GnShapeArg(ctypes.Structure):
 
 class StateCacheShapeArg(ctypes.Structure):
     _fields_ = [(n, _i64) for n in ("n", "slots", "entries", "H", "dk", "dv")]
+
+
+class BeamShapeArg(ctypes.Structure):
+    _fields_ = [(n, _i64) for n in ("requests", "beams", "vocabulary", "n")]
+
+
+class StateReorderShapeArg(ctypes.Structure):
+    _fields_ = [(n, _i64) for n in ("requests", "beams", "slots", "H", "dk", "dv")]
 
 
 def declare(lib):
@@ -68,8 +77,13 @@ def declare(lib):
                            _vp]
     lib.state_pack.argtypes = [cp, _vp, _vp, _vp, _vp, _vp, _vp]
     lib.state_unpack.argtypes = [cp, _vp, _vp, _vp, _vp, _vp, _vp]
+    bp, rp = ctypes.POINTER(BeamShapeArg), ctypes.POINTER(StateReorderShapeArg)
+    lib.beam_select_workspace_size.argtypes = [bp]
+    lib.beam_select_workspace_size.restype = _sz
+    lib.beam_select.argtypes = [bp, _int, _vp, _i64, _i64, _vp, _vp, ctypes.c_int32, _vp, _vp, _vp, _vp, _sz, _vp]
+    lib.state_reorder.argtypes = [rp, _vp, _vp, _vp, _vp]
     for fn in (lib.lin_prefill, lib.lin_step, lib.gn_fwd, lib.gn_bwd, lib.state_pack, lib.state_unpack,
-               lib.delta_prefill, lib.delta_step, lib.delta_bwd):
+               lib.delta_prefill, lib.delta_step, lib.delta_bwd, lib.beam_select, lib.state_reorder):
         fn.restype = _int
 
 
@@ -528,3 +542,73 @@ def state_unpack(cache, scales, states, *, entries=None, slots=None):
     lib = _lib()
     dev, s, sp, cp, ep, ids, ide = _cache_args(states, cache, scales, slots, entries)
     _call(lib.state_unpack, "state_unpack", dev, s, cp, ep, ide, ids, sp)
+
+
+def beam_select_workspace_size(requests, beams, vocabulary, n) -> int:
+    """Workspace bytes of `beam_select`."""
+    r = _lib().beam_select_workspace_size(ctypes.byref(BeamShapeArg(requests, beams, vocabulary, n)))
+    if r == _sz(-1).value:
+        raise ValueError(f"unsupported or invalid shape {(requests, beams, vocabulary, n)}")
+    return int(r)
+
+
+def beam_select(logits, scores, n, *, ended=None, end_token=0, out=None, workspace=None):
+    """(scores, tokens, parents), each [requests,n]: of each request's beams
+    and tokens the n candidates of the greatest scores[k] + log_softmax(
+    logits[k])[v], in falling order (ties: the lowest beam, then the lowest
+    token).  logits [requests,beams,V] (its last axis dense), scores float32
+    [requests,beams].  Beams whose `ended` (bool or uint8 [requests,beams]) is
+    set offer end_token alone, at the score they have; beams of score -inf
+    offer nothing.  Missing candidates are -inf, -1, -1.  ``out``: the three
+    tensors to write (float32, int32, int32)."""
+    lib = _lib()
+    code = _dtype_of(logits, "logits")
+    if logits.dim() != 3:
+        raise ValueError("logits must be [requests,beams,V]")
+    dev = logits.get_device()
+    R, K, V = logits.shape
+    n, end_token = int(n), int(end_token)
+    sp = _dense(scores, "scores", (R, K), _torch.float32, dev)
+    a, b, c = logits.stride()
+    if V > 1 and c != 1:
+        raise ValueError("the last axis of logits must be dense")
+    ep = None
+    if ended is not None:
+        ep = _dense(ended, "ended", (R, K), _torch.bool if getattr(ended, "dtype", None) == _torch.bool else _torch.uint8,
+                    dev)
+        if not 0 <= end_token < V:
+            raise ValueError(f"end_token {end_token} is not in the vocabulary of {V}")
+    s = _arg(BeamShapeArg, R, K, V, n)
+    need = lib.beam_select_workspace_size(s)
+    if need == _sz(-1).value:
+        raise ValueError(f"unsupported or invalid shape: {R} requests, {K} beams, {V} tokens, {n} candidates")
+    if out is None:
+        best = logits.new_empty((R, n), dtype=_torch.float32)
+        tokens, parents = logits.new_empty((2, R, n), dtype=_torch.int32).unbind()
+    else:
+        best, tokens, parents = out
+    ptrs = [_dense(t, name, (R, n), kind, dev) for t, name, kind in (
+        (best, "scores", _torch.float32), (tokens, "tokens", _torch.int32), (parents, "parents", _torch.int32))]
+    wp, wn, _keep = _bytes(need, dev, workspace)
+    _call(lib.beam_select, "beam_select", dev, s, code, logits.data_ptr() or None, a if R > 1 else 0, b if K > 1 else 0,
+          sp, ep, end_token, *ptrs, wp, wn)
+    return best, tokens, parents
+
+
+def state_reorder(states, parents, *, slots=None):
+    """The states of beams after a selection, in place: the state of beam j of
+    request r becomes that of its beam parents[r,j] (int32 [requests,beams];
+    negative: it stays).  Beam j of request r has slot slots[r*beams+j] of
+    states (float32 [slots,H,dk,dv]); slots None: slot r*beams+j."""
+    lib = _lib()
+    if not isinstance(states, _torch.Tensor) or states.dim() != 4 or not states.is_cuda:
+        raise ValueError("states must be a [slots,H,dk,dv] tensor on a HIP device")
+    dev = states.get_device()
+    S, H, dk, dv = states.shape
+    sp = _dense(states, "states", (S, H, dk, dv), _torch.float32, dev)
+    if not isinstance(parents, _torch.Tensor) or parents.dim() != 2:
+        raise ValueError("parents must be a [requests,beams] tensor")
+    R, K = parents.shape
+    pp = _dense(parents, "parents", (R, K), _torch.int32, dev)
+    s = _arg(StateReorderShapeArg, R, K, S, H, dk, dv)
+    _call(lib.state_reorder, "state_reorder", dev, s, pp, _ids(slots, "slots", R * K, dev), sp)

@@ -570,6 +570,54 @@ int state_pack(const state_cache_shape *shape, const float *states, const int32_
 int state_unpack(const state_cache_shape *shape, const uint8_t *cache, const uint8_t *scales,
                  const int32_t *entries, const int32_t *slots, float *states, void *stream);
 
+/* Beam search over a pool of states: a step's selection, and the states after
+ * it.  A recurrent layer's beams own their states, so those have to follow.
+ *
+ * beam_select: of each request's beams k and its vocabulary's tokens v, the n
+ * candidates of the greatest
+ *     score(k, v) = scores[k] + logits[k][v] - log sum_u exp(logits[k][u]),
+ * in falling order, of equal ones the lowest k vocabulary + v first.  Sums of
+ * exponentials are float32 within 2048 logits of a lane's part and 64 bits
+ * beyond; scores are compared in 64 bits and rounded once.
+ *   logits    of type `dtype`, a row of `vocabulary` for each beam, ld_beam
+ *             elements apart, ld_request between requests
+ *   scores    float32 [requests][beams]: the sum of log probabilities so far.
+ *             A beam of -infinity or NaN offers nothing (so the beams of a
+ *             request that has just begun can be 0, -inf, -inf, ...).
+ *   ended     uint8 [requests][beams] or NULL: a beam that is not 0 offers
+ *             end_token alone, at the score that it has
+ *   out_scores, tokens, parents  [requests][n]: score, token and beam; -inf,
+ *             -1, -1 where there are fewer than n candidates
+ * A logit of -infinity is never taken.  A beam whose logits hold a NaN or
+ * +infinity, or nothing but -infinity, offers nothing.  Rows of beams that
+ * offer nothing by their score, or have ended, are not read.
+ * 1 <= n, beams <= BEAM_MAX, beams vocabulary < 2^31, requests < 2^24 and
+ * requests beams ceil(vocabulary / 2048) < 2^24. */
+#define BEAM_MAX 64
+typedef struct beam_shape {
+    int64_t requests, beams, vocabulary, n;
+} beam_shape;
+size_t beam_select_workspace_size(const beam_shape *shape);
+int beam_select(const beam_shape *shape, int dtype, const void *logits, int64_t ld_request, int64_t ld_beam,
+                const float *scores, const uint8_t *ended, int32_t end_token,
+                float *out_scores, int32_t *tokens, int32_t *parents,
+                void *workspace, size_t workspace_bytes, void *stream);
+
+/* state_reorder: the state of beam j of request r becomes that of its beam
+ * parents[r][j] (int32 [requests][beams]), in place, all of a request's at
+ * once.  Beam j of request r has slot slots[r beams + j] (int32; NULL: slot
+ * r beams + j) of `states` [slots][H][dk][dv].  A negative parent, or a slot
+ * that is negative or does not exist, leaves its state as it was; a parent
+ * that does not exist (or whose slot does not) makes it NaN; of beams with one
+ * slot the last counts.  A request that has a slot of an earlier request of
+ * the call is left as it was.
+ * 1 <= beams <= BEAM_MAX; 1 <= dk, dv <= 256; requests and slots < 2^24. */
+typedef struct state_reorder_shape {
+    int64_t requests, beams, slots, H, dk, dv;
+} state_reorder_shape;
+int state_reorder(const state_reorder_shape *shape, const int32_t *parents, const int32_t *slots,
+                  float *states, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
