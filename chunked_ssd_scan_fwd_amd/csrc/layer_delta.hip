@@ -22,30 +22,43 @@ struct DeltaLds {
     static constexpr int PAD = sizeof(L) == 2 ? 16 : 4;
     static constexpr int LK = KP + PAD, LV = VT + PAD;
     static constexpr int PBYTES = PC::BYTES / PC::PARTS;
-    static constexpr bool T_HERE = C == 64;   // else the waves read T from memory themselves
     L q[2][C * LK], k[2][C * LK], v[2][C * LV];
-    char p[2][PBYTES], t[2][T_HERE ? PC::BYTES : 16];
+    alignas(16) char p[PBYTES], t[PC::BYTES];
+    // the next chunk's diagonal blocks of T, and A's tiles below, by lanes
+    alignas(16) f32x4 diag[PC::TT][64], low[PC::TT * (PC::TT - 1) / 2][64];
     Decays<C> dec[3];
+    alignas(16) float beta[3][C];
 };
+
+// f b + x of 16 x 16 matrices: lanes hold rows 4 g .. of column l % 16 of f^T, b and x.
+__device__ __forceinline__ f32x4 times(f32x4 f, f32x4 b, f32x4 x)
+{
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x = __builtin_amdgcn_mfma_f32_16x16x4f32(f[e], b[e], x, 0, 0, 0);
+    return x;
+}
 
 template <typename E, int KP, int VT>
 struct DeltaPerCu {
     static constexpr int n = VT == 64 && KP <= 128 && std::is_same<E, bf16>::value ? 2 : 1;
     static constexpr int C = n == 2 || sizeof(E) == 4 || KP > 128 || !std::is_same<E, bf16>::value ? 32 : 64;
+    // waves that hold S, and four more: with 64-row chunks all of them fetch and
+    // have rows of T, with 32-row ones two do either
+    static constexpr int waves = VT / 16, movers = C / 16, solvers = C / 16;
+    static constexpr int threads = 64 * (waves + 4), per_simd = n * threads / 256;
 };
 
 template <typename E, int KP, int VT, int C, bool VEC>
-__global__ __launch_bounds__(512)
-__attribute__((amdgpu_waves_per_eu(2 * DeltaPerCu<E, KP, VT>::n, 2 * DeltaPerCu<E, KP, VT>::n)))
-void k_delta_chunks(DeltaArgs a)
+__global__ __launch_bounds__((DeltaPerCu<E, KP, VT>::threads))
+__attribute__((amdgpu_waves_per_eu(DeltaPerCu<E, KP, VT>::per_simd, DeltaPerCu<E, KP, VT>::per_simd))) void k_delta_chunks(DeltaArgs a)
 {
     typedef DeltaLds<E, KP, VT, C> Lds;
     typedef typename Lds::L L;
     typedef Pieces<L, C> PC;
     constexpr int LK = Lds::LK, LV = Lds::LV;
-    constexpr int NT = VT / 64, MT = KP / 16, TT = C / 16, KS = KP / 32, TS = C / 32;
+    constexpr int WAVES = DeltaPerCu<E, KP, VT>::waves, NT = VT / 16 / WAVES, MT = KP / 16, TT = C / 16, KS = KP / 32, TS = C / 32;
     constexpr int PARTS = PC::PARTS, YU = PARTS == 3 ? 2 : 1;
-    constexpr int PT = 256;   // threads that fetch
+    constexpr int MOVERS = DeltaPerCu<E, KP, VT>::movers, PT = 64 * MOVERS;   // threads that fetch
     __shared__ __align__(16) Lds lds;
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -57,123 +70,228 @@ void k_delta_chunks(DeltaArgs a)
     const int g = h / (a.H / a.G), c0 = tile * VT, cols = min(VT, a.dv - c0);
     E *y = static_cast<E *>(a.y) + p.begin * a.st.y_t + h * a.st.y_h + c0;
     if (p.bad) {
-        for (int64_t e = threadIdx.x; e < (int64_t)p.rows * VT; e += 512)
+        for (int64_t e = threadIdx.x; e < (int64_t)p.rows * VT; e += DeltaPerCu<E, KP, VT>::threads)
             if (e % VT < cols) y[e / VT * a.st.y_t + e % VT] = from_f<E>(__builtin_nanf(""));
         return;
     }
     const int chunks = (p.rows + C - 1) / C;
-    const int first = p.begin - p.s * a.seg;   // of the sequence
-    const char *inv = a.inv + ((int64_t)chunk_number(p.n, first, p.s * a.seg, C) * a.H + h) * PC::BYTES;
-    const int64_t inv_step = (int64_t)a.H * PC::BYTES;
     const E *q = static_cast<const E *>(a.q) + p.begin * a.st.q_t + g * a.st.q_g;
     const E *k = static_cast<const E *>(a.k) + p.begin * a.st.k_t + g * a.st.k_g;
     const E *v = static_cast<const E *>(a.v) + p.begin * a.st.v_t + h * a.st.v_h + c0;
     const float *la = a.la + (a.la_t ? p.begin * a.la_t : 0) + h;
 
-    if (wave >= 4) {
-        // ---- fetches and scores
-        const int tid = threadIdx.x - 256, w = wave - 4;
-        constexpr int TU = PC::BYTES / 16, TPER = Lds::T_HERE ? (TU + PT - 1) / PT : 1;
+    // half j % 2 of a lane's 8 values of part u of piece (row block, j / 2)
+    typedef typename std::conditional<sizeof(L) == 2, bf16x4, f32x4>::type L4;
+    const auto put = [&](char *to, int parts, int row, int j, int u, L4 x) {
+        const int f = PC::at(row, j / 2) * parts + u;
+        *reinterpret_cast<L4 *>(to + (f * PC::UNITS * 64 + lane) * 16 + (j & 1) * (PC::UNITS == 2 ? 1024 : 8)) = x;
+    };
+
+    if (wave >= WAVES) {
+        // ---- fetches, and T of the next chunk
+        constexpr bool BOTH = MOVERS == 4;   // every wave does both
+        const int w = BOTH ? wave - WAVES : (wave - WAVES) & 1;
+        const bool mover = BOTH || wave < WAVES + MOVERS;
         Tile<E, C, KP, PT> tq, tk;
         Tile<E, C, VT, PT> tv;
-        u32x4 tt[TPER];
         const auto load = [&](int c) {
-            const int t0 = c * C, rows = p.rows - t0;
+            const int t0 = c * C, rows = p.rows - t0, tid = anew(threadIdx.x - 64 * WAVES);
             tq.template load<VEC>(q + t0 * a.st.q_t, a.st.q_t, min(C, rows), a.dk, tid);
             tk.template load<VEC>(k + t0 * a.st.k_t, a.st.k_t, min(C, rows), a.dk, tid);
             tv.template load<VEC>(v + t0 * a.st.v_t, a.st.v_t, min(C, rows), cols, tid);
-            if constexpr (Lds::T_HERE) {
-                const rsrc_t r = make_rsrc(inv + c * inv_step, rows > 0 ? PC::BYTES : 0);
-#pragma unroll
-                for (int u = 0; u < TPER; ++u)
-                    tt[u] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (u * PT + tid) * 16, 0, 0));
-            }
-        };
-        const auto log_decay = [&](int c) {
-            const int t = c * C + lane;
-            return lane < C && t < p.rows ? la[t * a.la_t] : 0.f;
         };
         const auto store = [&](int c) {
-            const int b = c & 1;
+            const int b = c & 1, tid = anew(threadIdx.x - 64 * WAVES);
             tq.template store<LK>(lds.q[b], tid);
             tk.template store<LK>(lds.k[b], tid);
             tv.template store<LV>(lds.v[b], tid);
-            if constexpr (Lds::T_HERE)
-#pragma unroll
-                for (int u = 0; u < TPER; ++u)
-                    if (TU % PT == 0 || u * PT + tid < TU) reinterpret_cast<u32x4 *>(lds.t[b])[u * PT + tid] = tt[u];
         };
-        // P: the 16 x 16 tiles on and below the diagonal, dealt to the four
-        // waves.  Formed as K Q^T, so that a lane holds 4 scores of one query.
-        const auto scores = [&](int c) {
-            const int b = c & 1;
-            const L *qs = lds.q[b], *ks = lds.k[b];
+        const float *beta = a.beta + p.begin * a.beta_t + h;
+        // a row's log decay (wave 0) or beta (wave 1), and what chunk c makes of them
+        const auto row_value = [&](int c) {
+            const int t = c * C + lane;
+            const bool on = w < 2 && lane < C && t < p.rows;
+            return on ? (w == 0 ? la[t * a.la_t] : beta[t * a.beta_t]) : 0.f;
+        };
+        const auto row_values = [&](int c, float x) {
+            if (w == 0) make_decays(lds.dec[c % 3], x, lane);
+            if (w == 1 && lane < C) lds.beta[c % 3][lane] = x;
+        };
+        // T in two steps, a row block of 16 to a wave.  First the tiles of
+        // A = diag(beta) M left of the diagonal, and the diagonal block's
+        // inverse X by substitution: a lane holds rows 4 g .. 4 g + 3 of column
+        // l % 16, so four rows at a time, which the lanes of the others then
+        // take off theirs.
+        const auto diagonal = [&](int c) {
+            const int lane = anew(threadIdx.x & 63), l16 = lane & 15, g4 = (lane >> 4) * 4;
+            const L *ks = lds.k[c & 1];
             const Decays<C> &d = lds.dec[c % 3];
-            constexpr int TILES = TT * (TT + 1) / 2;
-            const auto product = [&](int u) {
-                const int it = TT == 2 ? (u > 0) : (u > 0) + (u > 2) + (u > 5), jt = u - it * (it + 1) / 2;
-                f32x4 x = {};
+            const float *betas = lds.beta[c % 3];
+            Frag<L> fk[KS];
 #pragma unroll
-                for (int s = 0; s < KS; ++s)
-                    x = mma(frag8(ks + (16 * jt + l16) * LK + 32 * s + 2 * g4),
-                            frag8(qs + (16 * it + l16) * LK + 32 * s + 2 * g4), x);
-                return x;
+            for (int s = 0; s < KS; ++s) fk[s] = frag8(ks + (16 * w + l16) * LK + 32 * s + 2 * g4);
+            const f32x4 ih = *reinterpret_cast<const f32x4 *>(d.hi + 16 * w + g4);
+            const f32x4 il = *reinterpret_cast<const f32x4 *>(d.lo + 16 * w + g4);
+            const f32x4 bt = *reinterpret_cast<const f32x4 *>(betas + 16 * w + g4);
+            f32x4 m = {};
+#pragma unroll
+            for (int s = 0; s < KS; ++s) m = mma(fk[s], fk[s], m);
+            const auto scaled = [&](f32x4 &x, int j) {
+                const float jh = d.hi[16 * j + l16], jl = d.lo[16 * j + l16];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[e] *= bt[e] * __expf((ih[e] - jh) + (il[e] - jl));
             };
-            const auto masked = [&](int u, f32x4 x) {
-                const int it = TT == 2 ? (u > 0) : (u > 0) + (u > 2) + (u > 5), jt = u - it * (it + 1) / 2;
-                const int i = 16 * it + l16, j = 16 * jt + g4;
-                const float bh = d.hi[i], bl = d.lo[i];
-                const f32x4 jh = *reinterpret_cast<const f32x4 *>(d.hi + j);
-                const f32x4 jl = *reinterpret_cast<const f32x4 *>(d.lo + j);
-                float out[4];
+            scaled(m, w);
+            f32x4 X;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    out[e] = x[e] * __expf((bh - jh[e]) + (bl - jl[e]));
-                    if (j + e > i) out[e] = 0.f;
+            for (int e = 0; e < 4; ++e) {
+                if (l16 >= g4 + e) m[e] = 0.f;
+                X[e] = l16 == g4 + e ? 1.f : 0.f;
+            }
+            // the four rows' own block of A
+            const int own = 5 * g4;
+            const float a10 = __shfl(m[1], own), a20 = __shfl(m[2], own), a21 = __shfl(m[2], own + 1);
+            const float a30 = __shfl(m[3], own), a31 = __shfl(m[3], own + 1), a32 = __shfl(m[3], own + 2);
+            const auto rows4 = [&](auto which) {
+                constexpr int n = decltype(which)::value;
+                f32x4 y = X;
+                y[1] -= a10 * y[0];
+                y[2] -= a20 * y[0] + a21 * y[1];
+                y[3] -= a30 * y[0] + a31 * y[1] + a32 * y[2];
+                if (g4 == 4 * n) X = y;
+                if constexpr (n < 3) {
+                    const auto column = [&](int e, auto j) {   // A(g4 + e, 4 n + j)
+                        constexpr int ctrl = 0x150 + 4 * n + decltype(j)::value;   // row_newbcast
+                        return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(m[e]), ctrl, 0xf, 0xf, true));
+                    };
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) y[e] = __shfl(y[e], 16 * n + l16);
+                    f32x4 x = X;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        x[e] -= (column(e, ssd::IntC<0>{}) * y[0] + column(e, ssd::IntC<1>{}) * y[1]) +
+                                (column(e, ssd::IntC<2>{}) * y[2] + column(e, ssd::IntC<3>{}) * y[3]);
+                    if (g4 > 4 * n) X = x;
                 }
-                // half jt % 2 of the lane's 8 values
-                store4(reinterpret_cast<L *>(lds.p[b] + (PC::at(it, jt / 2) * PC::UNITS * 64 + lane) * 16 +
-                                             (jt % 2) * (PC::UNITS == 2 ? 1024 : 8)), out);
             };
-            if constexpr (TILES == 10) {
-                const f32x4 x0 = product(w), x1 = product(w + 4);
-                f32x4 x2 = {};
-                if (w < 2) x2 = product(w + 8);
-                masked(w, x0);
-                masked(w + 4, x1);
-                if (w < 2) masked(w + 8, x2);
-            } else {
+            rows4(ssd::IntC<0>{});
+            rows4(ssd::IntC<1>{});
+            rows4(ssd::IntC<2>{});
+            rows4(ssd::IntC<3>{});
+            lds.diag[w][lane] = X;
+#pragma unroll
+            for (int j = 0; j < TT - 1; ++j) {
+                if (j >= w) continue;
                 f32x4 x = {};
-                if (w < TILES) x = product(w);
-                if (w < TILES) masked(w, x);
+#pragma unroll
+                for (int s = 0; s < KS; ++s) x = mma(fk[s], frag8(ks + (16 * j + l16) * LK + 32 * s + 2 * g4), x);
+                scaled(x, j);
+                lds.low[w * (w - 1) / 2 + j][lane] = x;
             }
         };
-        // the scores above the diagonal that a piece on it holds stay 0
-        if (w < TT && w % 2 == 0) {
-            const float zero[4] = {};
+        // Then, from T (I + A) = I, T_ij = -(sum_m T_im A_mj) T_jj, j < m <= i.
+        // Held transposed, so that a sum comes out of the accumulators as the
+        // next product's operand, and T's rows as its pieces hold them; a block
+        // goes into all the sums that take it at once.
+        f32x4 T[TT];
+        const auto solve = [&](int c) {
+            const int lane = anew(threadIdx.x & 63), l16 = lane & 15, g4 = (lane >> 4) * 4;
+            const float *betas = lds.beta[c % 3];
+            f32x4 sum[TT] = {}, own;
+            {
+                const float *x = reinterpret_cast<const float *>(lds.diag[w]) + 64 * (l16 >> 2) + (l16 & 3);
 #pragma unroll
-            for (int b = 0; b < 2; ++b)
-                store4(reinterpret_cast<L *>(lds.p[b] + (PC::at(w, w / 2) * PC::UNITS * 64 + lane) * 16 +
-                                             (PC::UNITS == 2 ? 1024 : 8)), zero);
+                for (int e = 0; e < 4; ++e) own[e] = x[4 * (g4 + e)];
+            }
+#pragma unroll
+            for (int m = TT - 1; m >= 0; --m) {
+                if (m > w) continue;
+                T[m] = own;
+                if (m < w) T[m] = times(lds.diag[m][lane], -sum[m], f32x4{});
+                f32x4 f[TT];
+#pragma unroll
+                for (int j = 0; j < m; ++j) f[j] = lds.low[m * (m - 1) / 2 + j][lane];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+#pragma unroll
+                    for (int j = 0; j < m; ++j)
+                        sum[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(f[j][e], T[m][e], sum[j], 0, 0, 0);
+            }
+            // its columns times beta
+#pragma unroll
+            for (int j = 0; j < TT; ++j) T[j] *= *reinterpret_cast<const f32x4 *>(betas + 16 * j + g4);
+        };
+        const auto put_t = [&](int row, int j, f32x4 x) {
+            L4 parts[PARTS];
+            split4(parts, x);
+#pragma unroll
+            for (int u = 0; u < PARTS; ++u) put(lds.t, PARTS, row, j, u, parts[u]);
+        };
+        const auto write = [&]() {
+#pragma unroll
+            for (int j = 0; j < TT; ++j)
+                if (j <= w) put_t(w, j, T[j]);
+        };
+        // what a piece on the diagonal holds above it stays 0
+        if (w % 2 == 0 && (BOTH || !mover)) {
+            put(lds.p, 1, w, w + 1, 0, L4{});
+            put_t(w, w + 1, f32x4{});
         }
         // Without conditions: a chunk past the last one loads nothing and
         // leaves zeros in a buffer that is not read.
-        load(0);
-        if (w == 3) make_decays(lds.dec[0], log_decay(0), lane);
-        store(0);
-        load(1);
-        block_sync();
-        scores(0);
-        if (w == 3) make_decays(lds.dec[1], log_decay(1), lane);
-        block_sync();
-        for (int c = 0; c < chunks; ++c) {
-            const float la2 = log_decay(c + 2);
-            store(c + 1);
-            load(c + 2);
+        float next = 0.f;
+        const auto first_tiles = [&]() {
+            load(0);
+            store(0);
+            load(1);
+        };
+        const auto first_values = [&]() {
+            row_values(0, row_value(0));
+            next = row_value(1);
+        };
+        if (BOTH) {
+            first_values();
+            first_tiles();
             block_sync();
-            scores(c + 1);
-            if (w == 3) make_decays(lds.dec[(c + 2) % 3], la2, lane);
+            diagonal(0);
+            row_values(1, next);
             block_sync();
+            for (int c = 0; c < chunks; ++c) {
+                next = row_value(c + 2);
+                store(c + 1);
+                solve(c);
+                write();
+                block_sync();
+                load(c + 2);
+                diagonal(c + 1);
+                row_values(c + 2, next);
+                block_sync();
+            }
+        } else if (mover) {
+            first_tiles();
+            block_sync();
+            block_sync();
+            for (int c = 0; c < chunks; ++c) {
+                store(c + 1);
+                load(c + 2);
+                block_sync();
+                block_sync();
+            }
+        } else {
+            first_values();
+            block_sync();
+            diagonal(0);
+            row_values(1, next);
+            block_sync();
+            for (int c = 0; c < chunks; ++c) {
+                next = row_value(c + 2);
+                solve(c);
+                write();
+                block_sync();
+                diagonal(c + 1);
+                row_values(c + 2, next);
+                block_sync();
+            }
         }
         return;
     }
@@ -191,10 +309,10 @@ void k_delta_chunks(DeltaArgs a)
     // until it leaves 2^-16 .. 2^16.
     f32x4 S[MT][NT];
     float scale = 1.f;
-    const auto column = [&](int n) { return w0 + (NT == 2 ? 8 * (l16 >> 2) + 4 * n + (l16 & 3) : l16); };
-    const auto state_at = [&](int m, int n, int i) {
-        const int col = column(n);
-        const uint32_t base = col < cols ? (uint32_t)(2 * g4 * a.dv + c0 + col) * 4u : kOOB;
+    const auto column = [&](int n, int l16) { return w0 + (NT == 2 ? 8 * (l16 >> 2) + 4 * n + (l16 & 3) : l16); };
+    const auto state_at = [&](int m, int n, int i, int lane) {
+        const int col = column(n, lane & 15);
+        const uint32_t base = col < cols ? (uint32_t)((lane >> 4) * 8 * a.dv + c0 + col) * 4u : kOOB;
         return base + (uint32_t)(32 * (m / 2) + 4 * (m % 2) + i) * (uint32_t)a.dv * 4u;
     };
     {
@@ -205,7 +323,7 @@ void k_delta_chunks(DeltaArgs a)
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) S[m][n][i] = ssd::gload1(r, state_at(m, n, i));
+                for (int i = 0; i < 4; ++i) S[m][n][i] = ssd::gload1(r, state_at(m, n, i, lane));
     }
     block_sync();
     block_sync();
@@ -213,13 +331,29 @@ void k_delta_chunks(DeltaArgs a)
         const int b = c & 1, rows = min(C, p.rows - c * C);
         const Decays<C> &d = lds.dec[c % 3];
         const L *qs = lds.q[b], *ks = lds.k[b], *vs = lds.v[b];
-        const char *ts = Lds::T_HERE ? lds.t[b] : inv + c * inv_step;
-        Frag<L> own_t[Lds::T_HERE ? 1 : PC::N][PARTS];
-        if constexpr (!Lds::T_HERE)
+        // P's 16 x 16 tiles on and below the diagonal, dealt to the waves.
+        // Formed as K Q^T, so that a lane holds 4 scores of one query.
+        constexpr int TILES = TT * (TT + 1) / 2;
 #pragma unroll
-            for (int f = 0; f < PC::N; ++f)
+        for (int u0 = 0; u0 < TILES; u0 += WAVES) {
+            const int u = u0 + wave;
+            if (u >= TILES) continue;
+            const int it = TT == 2 ? (u > 0) : (u > 0) + (u > 2) + (u > 5), jt = u - it * (it + 1) / 2;
+            f32x4 x = {};
 #pragma unroll
-                for (int u = 0; u < PARTS; ++u) own_t[f][u] = piece<L, C>(ts, f, u, lane);
+            for (int s = 0; s < KS; ++s)
+                x = mma(frag8(ks + (16 * jt + l16) * LK + 32 * s + 2 * g4),
+                        frag8(qs + (16 * it + l16) * LK + 32 * s + 2 * g4), x);
+            const int i = 16 * it + l16, j = 16 * jt + g4;
+            const float bh = d.hi[i], bl = d.lo[i];
+            const f32x4 jh = *reinterpret_cast<const f32x4 *>(d.hi + j), jl = *reinterpret_cast<const f32x4 *>(d.lo + j);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                x[e] *= __expf((bh - jh[e]) + (bl - jl[e]));
+                if (j + e > i) x[e] = 0.f;
+            }
+            put(lds.p, 1, it, jt, 0, __builtin_convertvector(x, L4));
+        }
         // X = K S (rows: the chunk's, columns: of v), Y^T = S^T Q^T
         f32x4 X[NT][TT], Y[NT][TT];
 #pragma unroll
@@ -231,18 +365,23 @@ void k_delta_chunks(DeltaArgs a)
             Frag<L> fs[NT][PARTS];
 #pragma unroll
             for (int n = 0; n < NT; ++n) split(fs[n], S[2 * s][n], S[2 * s + 1][n]);
+            Frag<L> f[TT];
 #pragma unroll
-            for (int t = 0; t < TT; ++t) {
-                const Frag<L> fk = frag8(ks + (16 * t + l16) * LK + 32 * s + 2 * g4);
-                const Frag<L> fq = frag8(qs + (16 * t + l16) * LK + 32 * s + 2 * g4);
+            for (int t = 0; t < TT; ++t) f[t] = frag8(ks + (16 * t + l16) * LK + 32 * s + 2 * g4);
 #pragma unroll
-                for (int u = PARTS - 1; u >= 0; --u)
+            for (int u = PARTS - 1; u >= 0; --u)
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) X[n][t] = mma(fk, fs[n][u], X[n][t]);
+                for (int t = 0; t < TT; ++t)
 #pragma unroll
-                for (int n = 0; n < NT; ++n) Y[n][t] = mma(fs[n][0], fq, Y[n][t]);
-            }
+                    for (int n = 0; n < NT; ++n) X[n][t] = mma(f[t], fs[n][u], X[n][t]);
+#pragma unroll
+            for (int t = 0; t < TT; ++t) f[t] = frag8(qs + (16 * t + l16) * LK + 32 * s + 2 * g4);
+#pragma unroll
+            for (int t = 0; t < TT; ++t)
+#pragma unroll
+                for (int n = 0; n < NT; ++n) Y[n][t] = mma(fs[n][0], f[t], Y[n][t]);
         }
+        block_sync();   // P and T are there
         // U = (T diag(beta)) (V - diag(e^b) K S)
         f32x4 U[NT][TT];
         {
@@ -264,27 +403,23 @@ void k_delta_chunks(DeltaArgs a)
                 }
             }
 #pragma unroll
-            for (int t = 0; t < TT; ++t) {
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int n = 0; n < NT; ++n) U[n][t] = f32x4{};
+                for (int t = 0; t < TT; ++t) U[n][t] = f32x4{};
 #pragma unroll
-                for (int s = 0; s <= t / 2; ++s) {
-                    Frag<L> ft[PARTS];
+            for (int s = 0; s < TS; ++s)
 #pragma unroll
-                    for (int u = 0; u < PARTS; ++u) {
-                        if constexpr (Lds::T_HERE)
-                            ft[u] = piece<L, C>(ts, PC::at(t, s), u, lane);
-                        else
-                            ft[u] = own_t[PC::at(t, s)][u];
-                    }
+                for (int u = PARTS - 1; u >= 0; --u) {
+                    Frag<L> ft[TT];
 #pragma unroll
-                    for (int o = PARTS - 1; o >= 0; --o)   // the small products first
+                    for (int t = 2 * s; t < TT; ++t) ft[t] = piece<L, C>(lds.t, PC::at(t, s), u, lane);
 #pragma unroll
-                        for (int u = 0; u <= o; ++u)
+                    for (int o = PARTS - 1 - u; o >= 0; --o)
 #pragma unroll
-                            for (int n = 0; n < NT; ++n) U[n][t] = mma(ft[u], fg[s][n][o - u], U[n][t]);
+                        for (int t = 2 * s; t < TT; ++t)
+#pragma unroll
+                            for (int n = 0; n < NT; ++n) U[n][t] = mma(ft[t], fg[s][n][o], U[n][t]);
                 }
-            }
         }
         // An infinity or a NaN in k, v, beta, a decay or the state shows in U.
         float zero = 0.f;
@@ -295,8 +430,6 @@ void k_delta_chunks(DeltaArgs a)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) zero = __builtin_fmaf(U[n][t][i], 0.f, zero);
         const bool odd = __ballot(!(zero == 0.f)) != 0;
-        // the other waves' barrier between their tiles and their scores
-        block_sync();
         E *yc = y + c * C * a.st.y_t;
         if (__builtin_expect(odd, 0)) {
             // The products above would carry it to rows before its own, where T
@@ -306,6 +439,7 @@ void k_delta_chunks(DeltaArgs a)
 #pragma unroll
                 for (int n = 0; n < NT; ++n) S[m][n] *= scale;
             scale = 1.f;
+            const int ln = anew(lane), l16 = ln & 15, g4 = (ln >> 4) * 4;
 #pragma unroll 1
             for (int j = 0; j < rows; ++j) {
                 const float dec = __expf(clamp_decay(la[(c * C + j) * a.la_t]));
@@ -329,7 +463,7 @@ void k_delta_chunks(DeltaArgs a)
                 for (int n = 0; n < NT; ++n) {
                     dot[n] += __shfl_xor(dot[n], 16);
                     dot[n] += __shfl_xor(dot[n], 32);
-                    dot[n] = beta * (to_f(vs[j * LV + column(n)]) - dot[n]);
+                    dot[n] = beta * (to_f(vs[j * LV + column(n, l16)]) - dot[n]);
                 }
 #pragma unroll
                 for (int s = 0; s < KS; ++s) {
@@ -347,7 +481,7 @@ void k_delta_chunks(DeltaArgs a)
                 for (int n = 0; n < NT; ++n) {
                     out[n] += __shfl_xor(out[n], 16);
                     out[n] += __shfl_xor(out[n], 32);
-                    if (lane < 16 && column(n) < cols) yc[j * a.st.y_t + column(n)] = from_f<E>(out[n]);
+                    if (ln < 16 && column(n, l16) < cols) yc[j * a.st.y_t + column(n, l16)] = from_f<E>(out[n]);
                 }
             }
             block_sync();
@@ -376,28 +510,36 @@ void k_delta_chunks(DeltaArgs a)
             const f32x4 wb = *reinterpret_cast<const f32x4 *>(d.out + 32 * s + 16 + g4) * unscale;
 #pragma unroll
             for (int n = 0; n < NT; ++n) split(fu[n], U[n][2 * s], U[n][2 * s + 1]);
+            Frag<L> fp[TT];
 #pragma unroll
             for (int t = 2 * s; t < TT; ++t) {
-                Frag<L> fp;
-                char *to = reinterpret_cast<char *>(&fp);
+                char *to = reinterpret_cast<char *>(&fp[t]);
 #pragma unroll
                 for (int i = 0; i < PC::UNITS; ++i)
                     *reinterpret_cast<u32x4 *>(to + 16 * i) = *reinterpret_cast<const u32x4 *>(
-                        lds.p[b] + ((PC::at(t, s) * PC::UNITS + i) * 64 + lane) * 16);
-#pragma unroll
-                for (int u = YU - 1; u >= 0; --u)
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) Y[n][t] = mma(fu[n][u], fp, Y[n][t]);
+                        lds.p + ((PC::at(t, s) * PC::UNITS + i) * 64 + lane) * 16);
             }
 #pragma unroll
-            for (int n = 0; n < NT; ++n) split(fw[n], U[n][2 * s] * wa, U[n][2 * s + 1] * wb);
+            for (int u = YU - 1; u >= 0; --u)
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                const Frag<L> fk = frag_col<LK, true>(ks + 32 * s * LK, 32 * (m / 2) + 4 * (m % 2), lane);
+                for (int t = 2 * s; t < TT; ++t)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) Y[n][t] = mma(fu[n][u], fp[t], Y[n][t]);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) split(fw[n], U[n][2 * s] * wa, U[n][2 * s + 1] * wb);
+            // four accumulators' rows at a time: as many products that do not wait for each other
+#pragma unroll
+            for (int m0 = 0; m0 < MT; m0 += 4) {
+                Frag<L> fk[4];
+#pragma unroll
+                for (int m = 0; m < 4; ++m)
+                    fk[m] = frag_col<LK, true>(ks + 32 * s * LK, 32 * ((m0 + m) / 2) + 4 * (m % 2), lane);
 #pragma unroll
                 for (int u = PARTS - 1; u >= 0; --u)
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) S[m][n] = mma(fk, fw[n][u], S[m][n]);
+                    for (int m = 0; m < 4; ++m)
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) S[m0 + m][n] = mma(fk[m], fw[n][u], S[m0 + m][n]);
             }
         }
         {
@@ -434,69 +576,35 @@ void k_delta_chunks(DeltaArgs a)
     }
 
     const rsrc_t r = make_rsrc(pool, pool ? state * 4 : 0);
+    const int at = anew(lane);
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) ssd::gstore1(r, state_at(m, n, i), S[m][n][i] * scale);
+            for (int i = 0; i < 4; ++i) ssd::gstore1(r, state_at(m, n, i, at), S[m][n][i] * scale);
 }
 
 // ---- host side
 
 static int col_tile(int64_t dk, int64_t dv) { return dk > 128 || dv <= 64 ? 64 : 128; }
 
-// Rows of a chunk (DeltaPerCu).
-static int chunk_rows(int dtype, int64_t dk, int64_t dv)
-{
-    return dtype == LAYER_BF16 && dk <= 128 && col_tile(dk, dv) == 128 ? 64 : 32;
-}
-
-struct DeltaPlan {
-    int64_t ids = 0;     // chunk numbers
-    size_t total = 0;    // bytes of the workspace
-};
-
-static DeltaPlan plan_delta(const lin_shape &s, int dtype)
-{
-    DeltaPlan P;
-    const int C = chunk_rows(dtype, s.dk, s.dv);
-    P.ids = s.T / C + s.N;
-    const int64_t image = dtype == LAYER_BF16 ? (C == 64 ? Pieces<bf16, 64>::BYTES : Pieces<bf16, 32>::BYTES)
-                                              : Pieces<float, 32>::BYTES;
-    P.total = (size_t)(P.ids * s.H) * (size_t)image;
-    return P;
-}
-
-// The workspace for any element type.
-static size_t delta_workspace(const lin_shape &s)
-{
-    const size_t a = plan_delta(s, LAYER_BF16).total, b = plan_delta(s, LAYER_F32).total;
-    return a > b ? a : b;
-}
-
 template <typename E, int KP, int VT, bool VEC>
-static int run_delta(DeltaArgs &a, int64_t ids, hipStream_t st)
+static int run_delta(DeltaArgs &a, hipStream_t st)
 {
     constexpr int C = DeltaPerCu<E, KP, VT>::C;
-    if (ids > 0 && a.T > 0) {
-        DeltaArgs c = a;
-        c.seg = C;
-        c.ids = (int)ids;
-        k_delta_inverse<E, KP, C, VEC, false><<<dim3((unsigned)(ids * a.H)), dim3(4 * C), 0, st>>>(c);
-    }
     const int64_t grid = (int64_t)a.ids * a.H * a.tiles;
-    k_delta_chunks<E, KP, VT, C, VEC><<<dim3((unsigned)grid), dim3(512), 0, st>>>(a);
+    k_delta_chunks<E, KP, VT, C, VEC><<<dim3((unsigned)grid), dim3(DeltaPerCu<E, KP, VT>::threads), 0, st>>>(a);
     return launch_status();
 }
 
 template <typename E, bool VEC>
-static int dispatch_delta(DeltaArgs &a, int64_t ids, hipStream_t st)
+static int dispatch_delta(DeltaArgs &a, hipStream_t st)
 {
     const bool wide = col_tile(a.dk, a.dv) == 128;
-    if (a.dk > 128) return run_delta<E, 256, 64, VEC>(a, ids, st);
-    if (a.dk > 64) return wide ? run_delta<E, 128, 128, VEC>(a, ids, st) : run_delta<E, 128, 64, VEC>(a, ids, st);
-    return wide ? run_delta<E, 64, 128, VEC>(a, ids, st) : run_delta<E, 64, 64, VEC>(a, ids, st);
+    if (a.dk > 128) return run_delta<E, 256, 64, VEC>(a, st);
+    if (a.dk > 64) return wide ? run_delta<E, 128, 128, VEC>(a, st) : run_delta<E, 128, 64, VEC>(a, st);
+    return wide ? run_delta<E, 64, 128, VEC>(a, st) : run_delta<E, 64, 64, VEC>(a, st);
 }
 
 }  // namespace layer
@@ -506,7 +614,7 @@ using namespace layer;
 extern "C" size_t delta_prefill_workspace_size(const lin_shape *shape, int64_t max_seqlen)
 {
     if (check_delta(shape, false) != SSD_OK || max_seqlen < 0) return (size_t)-1;
-    return delta_workspace(*shape);
+    return 0;
 }
 
 extern "C" int delta_prefill(const lin_shape *shape, int dtype, const lin_strides *strides, const void *q,
@@ -533,7 +641,7 @@ extern "C" int delta_prefill(const lin_shape *shape, int dtype, const lin_stride
         misaligned(beta, 4) || misaligned(slots, 4) || misaligned(states, 4) || misaligned(cu_seqlens, 4) ||
         misaligned(carry, 4))
         return SSD_ERR_ALIGN;
-    const size_t need = delta_workspace(s);
+    const size_t need = 0;
     if (workspace_bytes < need) return SSD_ERR_WORKSPACE;
     if (need > 0 && !workspace) return SSD_ERR_NULL;
     if (need > 0 && misaligned(workspace, 16)) return SSD_ERR_ALIGN;
@@ -550,7 +658,6 @@ extern "C" int delta_prefill(const lin_shape *shape, int dtype, const lin_stride
     a.states = states;
     a.y = y;
     a.ends = a.segdec = nullptr;
-    a.inv = static_cast<char *>(workspace);
     a.T = (int)s.T;
     a.N = (int)s.N;
     a.G = (int)s.G;
@@ -563,14 +670,13 @@ extern "C" int delta_prefill(const lin_shape *shape, int dtype, const lin_stride
     a.seg = 0;
     a.ids = (int)s.N;
     a.shift = -1;
-    const int64_t ids = plan_delta(s, dtype).ids;
     const auto rows16 = [&](const void *ptr, int64_t row, int64_t head, int64_t d) {
         return !misaligned(ptr, 16) && row * e % 16 == 0 && head * e % 16 == 0 && d * e % 16 == 0 && row >= d;
     };
     const bool vec = rows16(q, a.st.q_t, a.st.q_g, s.dk) && rows16(k, a.st.k_t, a.st.k_g, s.dk) &&
                      rows16(v, a.st.v_t, a.st.v_h, s.dv) && rows16(y, a.st.y_t, a.st.y_h, s.dv);
     hipStream_t st = static_cast<hipStream_t>(stream);
-    if (dtype == LAYER_BF16) return vec ? dispatch_delta<bf16, true>(a, ids, st) : dispatch_delta<bf16, false>(a, ids, st);
-    if (dtype == LAYER_F16) return vec ? dispatch_delta<f16, true>(a, ids, st) : dispatch_delta<f16, false>(a, ids, st);
-    return vec ? dispatch_delta<float, true>(a, ids, st) : dispatch_delta<float, false>(a, ids, st);
+    if (dtype == LAYER_BF16) return vec ? dispatch_delta<bf16, true>(a, st) : dispatch_delta<bf16, false>(a, st);
+    if (dtype == LAYER_F16) return vec ? dispatch_delta<f16, true>(a, st) : dispatch_delta<f16, false>(a, st);
+    return vec ? dispatch_delta<float, true>(a, st) : dispatch_delta<float, false>(a, st);
 }

@@ -28,6 +28,7 @@ constexpr int CW = 32;   // rows of a chunk of the walks
 
 struct DeltaBackArgs : DeltaArgs {
     const void *dy;
+    char *inv;                     // the walk chunks' T~, T^T and P^T, [chunk][H]
     const float *dlast;            // gradients of the last states, or null
     float *zrec, *grec;            // [walk chunk][H][CW][dvp]
     float *srec, *arec;            // [chunk of CB][H][dk][dvp]

@@ -38,6 +38,15 @@ struct PrefillArgs {
     int shift;     // lengths >> shift order the segments; -1: as they come
 };
 
+// x, as a value that the compiler does not know: what is computed from it is
+// computed where it stands, not ahead of a loop and kept in registers that the
+// loop does not have.
+__device__ __forceinline__ int anew(int x)
+{
+    asm volatile("" : "+v"(x));
+    return x;
+}
+
 // ---- fragments of the matrix products
 //
 // A fragment is the 8 values a lane holds of a 16 x 32 operand: its row (or
@@ -187,6 +196,30 @@ __device__ __forceinline__ void split(Frag<float> (&f)[PARTS], f32x4 a, f32x4 b)
     frag_acc(f[0], a, b);
 }
 
+// Four values in PARTS summands of type L.
+template <int PARTS>
+__device__ __forceinline__ void split4(bf16x4 (&f)[PARTS], f32x4 x)
+{
+    const bf16x2 first = pair_of(0x0000bf80u), second = pair_of(0xbf800000u);
+#pragma unroll
+    for (int e = 0; e < 4; e += 2)
+#pragma unroll
+        for (int u = 0; u < PARTS; ++u) {
+            const bf16x2 r = __builtin_convertvector((f32x2{x[e], x[e + 1]}), bf16x2);
+            f[u][e] = r[0];
+            f[u][e + 1] = r[1];
+            if (u + 1 < PARTS) {
+                x[e] = __builtin_amdgcn_fdot2_f32_bf16(r, first, x[e], false);
+                x[e + 1] = __builtin_amdgcn_fdot2_f32_bf16(r, second, x[e + 1], false);
+            }
+        }
+}
+template <int PARTS>
+__device__ __forceinline__ void split4(f32x4 (&f)[PARTS], f32x4 x)
+{
+    f[0] = x;
+}
+
 __device__ __forceinline__ void store4(bf16 *p, const float (&x)[4])
 {
     *reinterpret_cast<bf16x4 *>(p) = __builtin_convertvector((f32x4{x[0], x[1], x[2], x[3]}), bf16x4);
@@ -230,12 +263,15 @@ struct Tile {
         const int64_t bytes = rows > 0 ? ((rows - 1) * ld + cols) * (int64_t)sizeof(E) : 0;
         if constexpr (VEC) {
             const rsrc_t r = make_rsrc(base, bytes);
+            // pieces of a thread lie PT VE / COLS rows apart
+            static_assert(PT * VE % COLS == 0, "whole rows between a thread's pieces");
+            const int row = tid * VE / COLS, col = tid * VE % COLS;
+            const uint32_t step = (uint32_t)(PT * VE / COLS * (int)ld) * (uint32_t)sizeof(E);
+            uint32_t off = col < cols ? (uint32_t)(row * (int)ld + col) * (uint32_t)sizeof(E) : kOOB;
 #pragma unroll
             for (int u = 0; u < PER; ++u) {
-                const int e = (u * PT + tid) * VE, row = e / COLS, col = e % COLS;
-                const uint32_t off =
-                    has(u, tid) && col < cols ? (uint32_t)(row * (int)ld + col) * (uint32_t)sizeof(E) : kOOB;
-                buf[u] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+                buf[u] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, has(u, tid) ? off : kOOB, 0, 0));
+                off += step;
             }
         } else {
             const rsrc_t r = make_rsrc(base, bytes);
