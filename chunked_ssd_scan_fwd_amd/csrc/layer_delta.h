@@ -23,6 +23,8 @@ namespace layer {
 struct DeltaArgs : PrefillArgs {
     const float *beta;
     int64_t beta_t;
+    float *maps;    // segments' transitions, [id][H][dk][dk]
+    int map_tiles;  // blocks for the columns of one
 };
 
 // Chunk number of row `begin` + `at` of sequence n, for chunks of C rows.

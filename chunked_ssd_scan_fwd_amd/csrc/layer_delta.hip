@@ -48,7 +48,11 @@ struct DeltaPerCu {
     static constexpr int threads = 64 * (waves + 4), per_simd = n * threads / 256;
 };
 
-template <typename E, int KP, int VT, int C, bool VEC>
+// OUT: y and the last state, from the state that enters the segment.  Otherwise
+// the map from the state that enters it to the one that leaves it, S' = M S + B:
+// B as the state that the segment makes from zero, and further blocks for the
+// columns of M, which is what it makes of the identity with v = 0.
+template <typename E, int KP, int VT, int C, bool OUT, bool VEC>
 __global__ __launch_bounds__((DeltaPerCu<E, KP, VT>::threads))
 __attribute__((amdgpu_waves_per_eu(DeltaPerCu<E, KP, VT>::per_simd, DeltaPerCu<E, KP, VT>::per_simd))) void k_delta_chunks(DeltaArgs a)
 {
@@ -63,13 +67,17 @@ __attribute__((amdgpu_waves_per_eu(DeltaPerCu<E, KP, VT>::per_simd, DeltaPerCu<E
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int l16 = lane & 15, g4 = (lane >> 4) * 4;
-    const int tile = blockIdx.x % a.tiles, h = blockIdx.x / a.tiles % a.H;
-    int id = blockIdx.x / (a.tiles * a.H);
+    const int tiles = OUT ? a.tiles : a.tiles + a.map_tiles;
+    const int tile = blockIdx.x % tiles, h = blockIdx.x / tiles % a.H;
+    int id = blockIdx.x / (tiles * a.H);
     Place p;
     if (!find(a, id, p)) return;
-    const int g = h / (a.H / a.G), c0 = tile * VT, cols = min(VT, a.dv - c0);
+    if (!OUT && (p.s + 1 >= p.segs || p.bad)) return;   // nothing follows the last segment
+    const bool map = !OUT && tile >= a.tiles;
+    const int width = map ? a.dk : a.dv;
+    const int g = h / (a.H / a.G), c0 = (map ? tile - a.tiles : tile) * VT, cols = min(VT, width - c0);
     E *y = static_cast<E *>(a.y) + p.begin * a.st.y_t + h * a.st.y_h + c0;
-    if (p.bad) {
+    if (OUT && p.bad) {
         for (int64_t e = threadIdx.x; e < (int64_t)p.rows * VT; e += DeltaPerCu<E, KP, VT>::threads)
             if (e % VT < cols) y[e / VT * a.st.y_t + e % VT] = from_f<E>(__builtin_nanf(""));
         return;
@@ -77,7 +85,7 @@ __attribute__((amdgpu_waves_per_eu(DeltaPerCu<E, KP, VT>::per_simd, DeltaPerCu<E
     const int chunks = (p.rows + C - 1) / C;
     const E *q = static_cast<const E *>(a.q) + p.begin * a.st.q_t + g * a.st.q_g;
     const E *k = static_cast<const E *>(a.k) + p.begin * a.st.k_t + g * a.st.k_g;
-    const E *v = static_cast<const E *>(a.v) + p.begin * a.st.v_t + h * a.st.v_h + c0;
+    const E *v = static_cast<const E *>(a.v) + p.begin * a.st.v_t + h * a.st.v_h + (map ? 0 : c0);
     const float *la = a.la + (a.la_t ? p.begin * a.la_t : 0) + h;
 
     // half j % 2 of a lane's 8 values of part u of piece (row block, j / 2)
@@ -96,13 +104,13 @@ __attribute__((amdgpu_waves_per_eu(DeltaPerCu<E, KP, VT>::per_simd, DeltaPerCu<E
         Tile<E, C, VT, PT> tv;
         const auto load = [&](int c) {
             const int t0 = c * C, rows = p.rows - t0, tid = anew(threadIdx.x - 64 * WAVES);
-            tq.template load<VEC>(q + t0 * a.st.q_t, a.st.q_t, min(C, rows), a.dk, tid);
+            if (OUT) tq.template load<VEC>(q + t0 * a.st.q_t, a.st.q_t, min(C, rows), a.dk, tid);
             tk.template load<VEC>(k + t0 * a.st.k_t, a.st.k_t, min(C, rows), a.dk, tid);
-            tv.template load<VEC>(v + t0 * a.st.v_t, a.st.v_t, min(C, rows), cols, tid);
+            tv.template load<VEC>(v + t0 * a.st.v_t, a.st.v_t, map ? 0 : min(C, rows), cols, tid);
         };
         const auto store = [&](int c) {
             const int b = c & 1, tid = anew(threadIdx.x - 64 * WAVES);
-            tq.template store<LK>(lds.q[b], tid);
+            if (OUT) tq.template store<LK>(lds.q[b], tid);
             tk.template store<LK>(lds.k[b], tid);
             tv.template store<LV>(lds.v[b], tid);
         };
@@ -298,8 +306,9 @@ __attribute__((amdgpu_waves_per_eu(DeltaPerCu<E, KP, VT>::per_simd, DeltaPerCu<E
 
     // ---- states and outputs
     __builtin_amdgcn_s_setprio(1);
-    const int64_t state = (int64_t)a.dk * a.dv;
+    const int64_t state = (int64_t)a.dk * width;
     float *pool = p.slot < 0 ? nullptr : a.states + ((int64_t)p.slot * a.H + h) * state;
+    float *ends = (map ? a.maps : a.ends) + ((int64_t)id * a.H + h) * state;
     const int w0 = 16 * NT * wave;   // this wave's columns of the tile
 
     // S: value i of accumulator m, n is row 32 (m / 2) + 2 g4 + 4 (m % 2) + i,
@@ -312,18 +321,21 @@ __attribute__((amdgpu_waves_per_eu(DeltaPerCu<E, KP, VT>::per_simd, DeltaPerCu<E
     const auto column = [&](int n, int l16) { return w0 + (NT == 2 ? 8 * (l16 >> 2) + 4 * n + (l16 & 3) : l16); };
     const auto state_at = [&](int m, int n, int i, int lane) {
         const int col = column(n, lane & 15);
-        const uint32_t base = col < cols ? (uint32_t)((lane >> 4) * 8 * a.dv + c0 + col) * 4u : kOOB;
-        return base + (uint32_t)(32 * (m / 2) + 4 * (m % 2) + i) * (uint32_t)a.dv * 4u;
+        const uint32_t base = col < cols ? (uint32_t)((lane >> 4) * 8 * width + c0 + col) * 4u : kOOB;
+        return base + (uint32_t)(32 * (m / 2) + 4 * (m % 2) + i) * (uint32_t)width * 4u;
     };
     {
-        const float *from = p.carry ? pool : nullptr;
+        const float *from = !OUT ? nullptr : p.segs > 1 ? ends : p.carry ? pool : nullptr;
         const rsrc_t r = make_rsrc(from, from ? state * 4 : 0);   // zeros where nothing enters
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) S[m][n][i] = ssd::gload1(r, state_at(m, n, i, lane));
+                for (int i = 0; i < 4; ++i) {
+                    S[m][n][i] = OUT ? ssd::gload1(r, state_at(m, n, i, lane)) : 0.f;
+                    if (map && 32 * (m / 2) + 2 * g4 + 4 * (m % 2) + i == c0 + column(n, l16)) S[m][n][i] = 1.f;
+                }
     }
     block_sync();
     block_sync();
@@ -333,7 +345,7 @@ __attribute__((amdgpu_waves_per_eu(DeltaPerCu<E, KP, VT>::per_simd, DeltaPerCu<E
         const L *qs = lds.q[b], *ks = lds.k[b], *vs = lds.v[b];
         // P's 16 x 16 tiles on and below the diagonal, dealt to the waves.
         // Formed as K Q^T, so that a lane holds 4 scores of one query.
-        constexpr int TILES = TT * (TT + 1) / 2;
+        constexpr int TILES = OUT ? TT * (TT + 1) / 2 : 0;
 #pragma unroll
         for (int u0 = 0; u0 < TILES; u0 += WAVES) {
             const int u = u0 + wave;
@@ -374,6 +386,7 @@ __attribute__((amdgpu_waves_per_eu(DeltaPerCu<E, KP, VT>::per_simd, DeltaPerCu<E
                 for (int t = 0; t < TT; ++t)
 #pragma unroll
                     for (int n = 0; n < NT; ++n) X[n][t] = mma(f[t], fs[n][u], X[n][t]);
+            if (!OUT) continue;
 #pragma unroll
             for (int t = 0; t < TT; ++t) f[t] = frag8(qs + (16 * t + l16) * LK + 32 * s + 2 * g4);
 #pragma unroll
@@ -430,7 +443,7 @@ __attribute__((amdgpu_waves_per_eu(DeltaPerCu<E, KP, VT>::per_simd, DeltaPerCu<E
 #pragma unroll
                 for (int i = 0; i < 4; ++i) zero = __builtin_fmaf(U[n][t][i], 0.f, zero);
         const bool odd = __ballot(!(zero == 0.f)) != 0;
-        E *yc = y + c * C * a.st.y_t;
+        E *yc = OUT ? y + c * C * a.st.y_t : nullptr;
         if (__builtin_expect(odd, 0)) {
             // The products above would carry it to rows before its own, where T
             // and P are 0: the recurrence itself, row by row.
@@ -481,7 +494,7 @@ __attribute__((amdgpu_waves_per_eu(DeltaPerCu<E, KP, VT>::per_simd, DeltaPerCu<E
                 for (int n = 0; n < NT; ++n) {
                     out[n] += __shfl_xor(out[n], 16);
                     out[n] += __shfl_xor(out[n], 32);
-                    if (ln < 16 && column(n, l16) < cols) yc[j * a.st.y_t + column(n, l16)] = from_f<E>(out[n]);
+                    if (OUT && ln < 16 && column(n, l16) < cols) yc[j * a.st.y_t + column(n, l16)] = from_f<E>(out[n]);
                 }
             }
             block_sync();
@@ -508,8 +521,9 @@ __attribute__((amdgpu_waves_per_eu(DeltaPerCu<E, KP, VT>::per_simd, DeltaPerCu<E
             Frag<L> fu[NT][YU], fw[NT][PARTS];
             const f32x4 wa = *reinterpret_cast<const f32x4 *>(d.out + 32 * s + g4) * unscale;
             const f32x4 wb = *reinterpret_cast<const f32x4 *>(d.out + 32 * s + 16 + g4) * unscale;
+            if constexpr (OUT) {
 #pragma unroll
-            for (int n = 0; n < NT; ++n) split(fu[n], U[n][2 * s], U[n][2 * s + 1]);
+                for (int n = 0; n < NT; ++n) split(fu[n], U[n][2 * s], U[n][2 * s + 1]);
             Frag<L> fp[TT];
 #pragma unroll
             for (int t = 2 * s; t < TT; ++t) {
@@ -525,6 +539,7 @@ __attribute__((amdgpu_waves_per_eu(DeltaPerCu<E, KP, VT>::per_simd, DeltaPerCu<E
                 for (int t = 2 * s; t < TT; ++t)
 #pragma unroll
                     for (int n = 0; n < NT; ++n) Y[n][t] = mma(fu[n][u], fp[t], Y[n][t]);
+            }
 #pragma unroll
             for (int n = 0; n < NT; ++n) split(fw[n], U[n][2 * s] * wa, U[n][2 * s + 1] * wb);
             // four accumulators' rows at a time: as many products that do not wait for each other
@@ -542,7 +557,7 @@ __attribute__((amdgpu_waves_per_eu(DeltaPerCu<E, KP, VT>::per_simd, DeltaPerCu<E
                         for (int n = 0; n < NT; ++n) S[m0 + m][n] = mma(fk[m], fw[n][u], S[m0 + m][n]);
             }
         }
-        {
+        if constexpr (OUT) {
             const rsrc_t r = make_rsrc(yc, ((rows - 1) * a.st.y_t + cols) * (int64_t)sizeof(E));
             const int col = w0 + NT * g4;   // 4 NT columns from here on
             constexpr int W = 4 * NT, PIECE = 16 / (int)sizeof(E) < W ? 16 / (int)sizeof(E) : W;
@@ -575,7 +590,8 @@ __attribute__((amdgpu_waves_per_eu(DeltaPerCu<E, KP, VT>::per_simd, DeltaPerCu<E
         block_sync();
     }
 
-    const rsrc_t r = make_rsrc(pool, pool ? state * 4 : 0);
+    float *to = OUT ? (p.s + 1 == p.segs ? pool : nullptr) : ends;
+    const rsrc_t r = make_rsrc(to, to ? state * 4 : 0);
     const int at = anew(lane);
 #pragma unroll
     for (int m = 0; m < MT; ++m)
@@ -585,16 +601,156 @@ __attribute__((amdgpu_waves_per_eu(DeltaPerCu<E, KP, VT>::per_simd, DeltaPerCu<E
             for (int i = 0; i < 4; ++i) ssd::gstore1(r, state_at(m, n, i, at), S[m][n][i] * scale);
 }
 
+// The states that enter the segments of a sequence that was cut, in place of
+// the states that the segments make from zero: S_{s+1} = M_s S_s + B_s, in
+// float32.  A block has 16 columns of one head's states; a wave has 16 rows of
+// M (twice where dk is over 128) and the next segment's on their way, and the
+// state goes round the waves through LDS, transposed.
+template <int KP>
+struct CarryWaves {
+    static constexpr int n = KP / 16 < 8 ? KP / 16 : 8;
+};
+template <int KP>
+__global__ __launch_bounds__(64 * CarryWaves<KP>::n) void k_delta_carry(DeltaArgs a)
+{
+    constexpr int WAVES = CarryWaves<KP>::n, NR = KP / 16 / WAVES, KS = KP / 16, LS = KP + 4;
+    __shared__ __align__(16) float St[2][16 * LS];
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int l16 = lane & 15, g4 = (lane >> 4) * 4;
+    const int h = blockIdx.x % a.H, col = blockIdx.y * 16 + l16;
+    Place p;
+    int begin, end;
+    about(a, blockIdx.x / a.H, p, begin, end);
+    if (p.segs <= 1 || p.bad) return;
+    const int64_t id0 = begin / a.seg + p.n, state = (int64_t)a.dk * a.dv, map = (int64_t)a.dk * a.dk;
+    float *ends = a.ends + (id0 * a.H + h) * state;
+    const float *maps = a.maps + (id0 * a.H + h) * map;
+    // rows 16 (n WAVES + w) + g4 + i of column col; M's rows 16 (n WAVES + w) + l16, columns 16 s + g4 ..
+    const auto at = [&](int n, int i) {
+        const int row = 16 * (n * WAVES + w) + g4 + i;
+        return col < a.dv && row < a.dk ? (uint32_t)(row * a.dv + col) * 4u : kOOB;
+    };
+    f32x4 M[NR][KS], B[NR], S[NR];
+    const auto load = [&](int s) {
+        const rsrc_t rm = make_rsrc(maps + s * (a.H * map), map * 4), rb = make_rsrc(ends + s * (a.H * state), state * 4);
+#pragma unroll
+        for (int n = 0; n < NR; ++n) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) B[n][i] = ssd::gload1(rb, at(n, i));
+            const int row = 16 * (n * WAVES + w) + l16;
+#pragma unroll
+            for (int x = 0; x < KS; ++x)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int c = 16 * x + g4 + i;
+                    M[n][x][i] = ssd::gload1(rm, row < a.dk && c < a.dk ? (uint32_t)(row * a.dk + c) * 4u : kOOB);
+                }
+        }
+    };
+    {
+        const float *from = p.carry ? a.states + ((int64_t)p.slot * a.H + h) * state : nullptr;
+        const rsrc_t r = make_rsrc(from, from ? state * 4 : 0);
+#pragma unroll
+        for (int n = 0; n < NR; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) S[n][i] = ssd::gload1(r, at(n, i));
+    }
+    load(0);
+    for (int s = 0; s < p.segs; ++s) {
+        float *st = St[s & 1];
+        const rsrc_t r = make_rsrc(ends + s * (a.H * state), state * 4);
+#pragma unroll
+        for (int n = 0; n < NR; ++n) {
+            *reinterpret_cast<f32x4 *>(st + l16 * LS + 16 * (n * WAVES + w) + g4) = S[n];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) ssd::gstore1(r, at(n, i), S[n][i]);   // after this lane's B was read
+        }
+        if (s + 1 == p.segs) break;
+        block_sync();
+        f32x4 sum[NR][2];
+#pragma unroll
+        for (int n = 0; n < NR; ++n) {
+            sum[n][0] = B[n];
+            sum[n][1] = f32x4{};
+        }
+#pragma unroll
+        for (int x = 0; x < KS; ++x) {
+            const f32x4 f = *reinterpret_cast<const f32x4 *>(st + l16 * LS + 16 * x + g4);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+                for (int n = 0; n < NR; ++n)
+                    sum[n][x & 1] = __builtin_amdgcn_mfma_f32_16x16x4f32(M[n][x][e], f[e], sum[n][x & 1], 0, 0, 0);
+        }
+#pragma unroll
+        for (int n = 0; n < NR; ++n) S[n] = sum[n][0] + sum[n][1];
+        if (s + 2 < p.segs) load(s + 1);   // the last segment made none
+    }
+}
+
 // ---- host side
 
 static int col_tile(int64_t dk, int64_t dv) { return dk > 128 || dv <= 64 ? 64 : 128; }
 
+struct DeltaPlan {
+    int seg = 0, ids = 0, map_tiles = 0;
+    size_t ends = 0, maps = 0, total = 0;
+};
+
+// Sequences are cut where that is faster by an estimate: into segments of a
+// length that makes about one block for each place on a CU out of the batch's
+// rows, at least 256.  Whole, the longest one's chain of chunks counts, or all
+// rows over the places; cut, the output pass's rows and, for 0.7 of its time
+// each, those of the blocks for B and M, with 1.2 us for each segment that the
+// carry pass joins and 15 us for two launches more.
+static DeltaPlan plan_delta(const lin_shape &s, int dtype, int64_t max_seqlen, int cus)
+{
+    DeltaPlan P;
+    const int64_t longest = max_seqlen > 0 && max_seqlen < s.T ? max_seqlen : s.T;
+    const int64_t vt = col_tile(s.dk, s.dv), tiles = (s.dv + vt - 1) / vt, map_tiles = (s.dk + vt - 1) / vt;
+    const int64_t places = (vt == 64 && s.dk <= 128 && dtype == LAYER_BF16 ? 2 : 1) * (int64_t)cus;
+    P.ids = (int)s.N;
+    P.map_tiles = (int)map_tiles;
+    int64_t seg = ((s.T * s.H * tiles + places - 1) / places + 63) / 64 * 64;
+    if (seg < 256) seg = 256;
+    const double row = dtype == LAYER_BF16 ? 0.1 : 0.2;   // us
+    const double all = (double)s.T * (double)(s.H * tiles) / (double)places;
+    const double whole = row * (all > (double)longest ? all : (double)longest);
+    const double cut = row * ((double)seg + 0.7 * (double)seg * (double)(tiles + map_tiles) / (double)tiles) +
+                       1.2 * (double)longest / (double)seg + 15.0;
+    if (longest <= seg || whole <= cut) return P;
+    // and no more of them than a launch has blocks for
+    const int64_t most = max_blocks(1024) / (s.H * (tiles + map_tiles)) - s.N;
+    if (most < 1) return P;
+    if (s.T / seg > most) seg = (s.T / most + 64) / 64 * 64;
+    if (longest <= seg || seg >= (int64_t(1) << 30)) return P;
+    P.seg = (int)seg;
+    P.ids = (int)(s.T / seg + s.N);
+    P.ends = 0;
+    P.maps = ((size_t)(P.ids * s.H * s.dk * s.dv) * sizeof(float) + 255) / 256 * 256;
+    P.total = P.maps + (size_t)(P.ids * s.H * s.dk * s.dk) * sizeof(float);
+    return P;
+}
+
+// The workspace for any element type.
+static size_t delta_workspace(const lin_shape &s, int64_t max_seqlen, int cus)
+{
+    const size_t a = plan_delta(s, LAYER_BF16, max_seqlen, cus).total, b = plan_delta(s, LAYER_F32, max_seqlen, cus).total;
+    return a > b ? a : b;
+}
+
 template <typename E, int KP, int VT, bool VEC>
 static int run_delta(DeltaArgs &a, hipStream_t st)
 {
-    constexpr int C = DeltaPerCu<E, KP, VT>::C;
+    constexpr int C = DeltaPerCu<E, KP, VT>::C, threads = DeltaPerCu<E, KP, VT>::threads;
+    if (a.seg > 0) {
+        const int64_t grid = (int64_t)a.ids * a.H * (a.tiles + a.map_tiles);
+        k_delta_chunks<E, KP, VT, C, false, VEC><<<dim3((unsigned)grid), dim3(threads), 0, st>>>(a);
+        const dim3 carry((unsigned)(a.N * a.H), (unsigned)((a.dv + 15) / 16));
+        k_delta_carry<KP><<<carry, dim3(64 * CarryWaves<KP>::n), 0, st>>>(a);
+    }
     const int64_t grid = (int64_t)a.ids * a.H * a.tiles;
-    k_delta_chunks<E, KP, VT, C, VEC><<<dim3((unsigned)grid), dim3(DeltaPerCu<E, KP, VT>::threads), 0, st>>>(a);
+    k_delta_chunks<E, KP, VT, C, true, VEC><<<dim3((unsigned)grid), dim3(threads), 0, st>>>(a);
     return launch_status();
 }
 
@@ -614,7 +770,7 @@ using namespace layer;
 extern "C" size_t delta_prefill_workspace_size(const lin_shape *shape, int64_t max_seqlen)
 {
     if (check_delta(shape, false) != SSD_OK || max_seqlen < 0) return (size_t)-1;
-    return 0;
+    return delta_workspace(*shape, max_seqlen, ssd::device_cus());
 }
 
 extern "C" int delta_prefill(const lin_shape *shape, int dtype, const lin_strides *strides, const void *q,
@@ -641,7 +797,9 @@ extern "C" int delta_prefill(const lin_shape *shape, int dtype, const lin_stride
         misaligned(beta, 4) || misaligned(slots, 4) || misaligned(states, 4) || misaligned(cu_seqlens, 4) ||
         misaligned(carry, 4))
         return SSD_ERR_ALIGN;
-    const size_t need = 0;
+    const int cus = ssd::device_cus();
+    const DeltaPlan P = plan_delta(s, dtype, max_seqlen, cus);
+    const size_t need = delta_workspace(s, max_seqlen, cus);
     if (workspace_bytes < need) return SSD_ERR_WORKSPACE;
     if (need > 0 && !workspace) return SSD_ERR_NULL;
     if (need > 0 && misaligned(workspace, 16)) return SSD_ERR_ALIGN;
@@ -657,7 +815,10 @@ extern "C" int delta_prefill(const lin_shape *shape, int dtype, const lin_stride
     a.carry = carry;
     a.states = states;
     a.y = y;
-    a.ends = a.segdec = nullptr;
+    a.ends = reinterpret_cast<float *>(static_cast<char *>(workspace) + P.ends);
+    a.maps = reinterpret_cast<float *>(static_cast<char *>(workspace) + P.maps);
+    a.segdec = nullptr;
+    a.map_tiles = P.map_tiles;
     a.T = (int)s.T;
     a.N = (int)s.N;
     a.G = (int)s.G;
@@ -667,8 +828,8 @@ extern "C" int delta_prefill(const lin_shape *shape, int dtype, const lin_stride
     a.nslots = (int)s.slots;
     const int vt = col_tile(s.dk, s.dv);
     a.tiles = (a.dv + vt - 1) / vt;
-    a.seg = 0;
-    a.ids = (int)s.N;
+    a.seg = P.seg;
+    a.ids = P.ids;
     a.shift = -1;
     const auto rows16 = [&](const void *ptr, int64_t row, int64_t head, int64_t d) {
         return !misaligned(ptr, 16) && row * e % 16 == 0 && head * e % 16 == 0 && d * e % 16 == 0 && row >= d;

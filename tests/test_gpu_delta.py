@@ -73,6 +73,28 @@ def test_prefill_slices_of_a_projection(heads, dtype):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("lens,max_seqlen", [([4500], 0), ([3000, 17, 0, 1400], 0), ([2500], 5), ([1024, 2048, 512], 0)])
+def test_prefill_long(lens, max_seqlen, dtype):
+    """Cut over the length: with no bound given, with the right one, and with one that is too small."""
+    carry = [1] * (len(lens) - 1) + [0] if len(lens) > 1 else None
+    for heads, per_token in (((1, 1, 128, 128), True), ((1, 2, 64, 48), False)):
+        check_prefill("long", heads, dtype, lens, per_token=per_token, max_seqlen=max_seqlen, seed=5, carry=carry, mu=-6.0)
+
+
+@pytest.mark.parametrize("heads,dtype", [((1, 1, 256, 130), BF), ((1, 2, 96, 200), F16), ((1, 1, 33, 17), F32),
+                                         ((2, 2, 64, 64), BF), ((1, 1, 20, 256), BF), ((1, 1, 256, 64), F32)])
+def test_prefill_cut_at_other_heads(heads, dtype):
+    check_prefill("cut", heads, dtype, [1500, 1700], carry=[0, 1], slots=[2, 0], npool=3, tail=2, seed=13, mu=-6.0)
+
+
+def test_prefill_long_runs_are_cut():
+    """The shapes above do run cut: they ask for a workspace."""
+    for shape in ((4500, 1, 1, 1, 128, 128, 1), (4417, 4, 1, 2, 64, 48, 4), (3202, 2, 1, 1, 256, 130, 3),
+                  (3202, 2, 1, 1, 33, 17, 3)):
+        assert ssd.layer.delta_prefill_workspace_size(*shape) > 0, shape
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
 @pytest.mark.parametrize("near", [0.5, 0.9, 1.0])
 def test_prefill_near_keys(near, dtype):
     """Keys that are nearly or quite the same: the inverse's powers would be huge."""
@@ -134,11 +156,11 @@ def test_prefill_empty_and_missing(dtype):
 @pytest.mark.parametrize("bad", [NAN, INF])
 def test_prefill_infinities_and_nan(where, bad, dtype):
     """They reach the rows after them, in v only their column."""
-    for heads in ((1, 2, 128, 128), (1, 2, 64, 64)):
+    for heads, T in (((1, 2, 128, 128), 200), ((1, 2, 64, 64), 200), ((1, 2, 128, 64), 3000)):   # the last one cut
         G, H, dk, dv = heads
-        q, k, v, ld, beta, S = ref.inputs(200, G, H, dk, dv, dtype, True, 9, 2)
+        q, k, v, ld, beta, S = ref.inputs(T, G, H, dk, dv, dtype, True, 9, 2)
         clean = [dev(t) for t in (q, k, v, ld, beta)], dev(S)
-        want = ssd.delta_prefill(*clean[0], ids([0, 90, 200]), clean[1])
+        want = ssd.delta_prefill(*clean[0], ids([0, 90, T]), clean[1])
         row, col = 131, 7
         t = {"q": q, "k": k, "v": v, "beta": beta, "decay": ld, "state": S}[where]
         if where in ("q", "k"):
@@ -151,7 +173,7 @@ def test_prefill_infinities_and_nan(where, bad, dtype):
             t[row, 1] = bad
         say(f"delta_prefill {where} {bad} {heads} {dtype}")
         pool = dev(S)
-        y = ssd.delta_prefill(*(dev(x) for x in (q, k, v, ld, beta)), ids([0, 90, 200]), pool)
+        y = ssd.delta_prefill(*(dev(x) for x in (q, k, v, ld, beta)), ids([0, 90, T]), pool)
         y, want = y.cpu(), want.cpu()
         assert torch.equal(y[:90], want[:90])
         if where in ("v", "state"):
