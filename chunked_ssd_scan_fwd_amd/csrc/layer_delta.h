@@ -23,8 +23,8 @@ namespace layer {
 struct DeltaArgs : PrefillArgs {
     const float *beta;
     int64_t beta_t;
-    float *maps;    // segments' transitions, [id][H][dk][dk]
-    int map_tiles;  // blocks for the columns of one
+    float *maps;    // segments' transitions, [id][H][dk][map_cols]
+    int map_cols, map_tiles;   // dk rounded up to a multiple of 4, and blocks for as many columns
 };
 
 // Chunk number of row `begin` + `at` of sequence n, for chunks of C rows.

@@ -74,7 +74,7 @@ __attribute__((amdgpu_waves_per_eu(DeltaPerCu<E, KP, VT>::per_simd, DeltaPerCu<E
     if (!find(a, id, p)) return;
     if (!OUT && (p.s + 1 >= p.segs || p.bad)) return;   // nothing follows the last segment
     const bool map = !OUT && tile >= a.tiles;
-    const int width = map ? a.dk : a.dv;
+    const int width = map ? a.map_cols : a.dv;
     const int g = h / (a.H / a.G), c0 = (map ? tile - a.tiles : tile) * VT, cols = min(VT, width - c0);
     E *y = static_cast<E *>(a.y) + p.begin * a.st.y_t + h * a.st.y_h + c0;
     if (OUT && p.bad) {
@@ -604,16 +604,17 @@ __attribute__((amdgpu_waves_per_eu(DeltaPerCu<E, KP, VT>::per_simd, DeltaPerCu<E
 // The states that enter the segments of a sequence that was cut, in place of
 // the states that the segments make from zero: S_{s+1} = M_s S_s + B_s, in
 // float32.  A block has 16 columns of one head's states; a wave has 16 rows of
-// M (twice where dk is over 128) and the next segment's on their way, and the
+// M (twice where dk is over 128) and the next segments' on their way, and the
 // state goes round the waves through LDS, transposed.
 template <int KP>
 struct CarryWaves {
-    static constexpr int n = KP / 16 < 8 ? KP / 16 : 8;
+    static constexpr int n = KP / 16 < 8 ? KP / 16 : 8, ahead = KP == 256 ? 1 : 3;
 };
 template <int KP>
 __global__ __launch_bounds__(64 * CarryWaves<KP>::n) void k_delta_carry(DeltaArgs a)
 {
     constexpr int WAVES = CarryWaves<KP>::n, NR = KP / 16 / WAVES, KS = KP / 16, LS = KP + 4;
+    constexpr int AHEAD = CarryWaves<KP>::ahead;
     __shared__ __align__(16) float St[2][16 * LS];
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int l16 = lane & 15, g4 = (lane >> 4) * 4;
@@ -622,7 +623,7 @@ __global__ __launch_bounds__(64 * CarryWaves<KP>::n) void k_delta_carry(DeltaArg
     int begin, end;
     about(a, blockIdx.x / a.H, p, begin, end);
     if (p.segs <= 1 || p.bad) return;
-    const int64_t id0 = begin / a.seg + p.n, state = (int64_t)a.dk * a.dv, map = (int64_t)a.dk * a.dk;
+    const int64_t id0 = begin / a.seg + p.n, state = (int64_t)a.dk * a.dv, map = (int64_t)a.dk * a.map_cols;
     float *ends = a.ends + (id0 * a.H + h) * state;
     const float *maps = a.maps + (id0 * a.H + h) * map;
     // rows 16 (n WAVES + w) + g4 + i of column col; M's rows 16 (n WAVES + w) + l16, columns 16 s + g4 ..
@@ -630,23 +631,25 @@ __global__ __launch_bounds__(64 * CarryWaves<KP>::n) void k_delta_carry(DeltaArg
         const int row = 16 * (n * WAVES + w) + g4 + i;
         return col < a.dv && row < a.dk ? (uint32_t)(row * a.dv + col) * 4u : kOOB;
     };
-    f32x4 M[NR][KS], B[NR], S[NR];
-    const auto load = [&](int s) {
+    struct Step {
+        f32x4 M[NR][KS], B[NR];
+    };
+    const auto load = [&](Step &x, int s) {
         const rsrc_t rm = make_rsrc(maps + s * (a.H * map), map * 4), rb = make_rsrc(ends + s * (a.H * state), state * 4);
 #pragma unroll
         for (int n = 0; n < NR; ++n) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) B[n][i] = ssd::gload1(rb, at(n, i));
-            const int row = 16 * (n * WAVES + w) + l16;
+            for (int i = 0; i < 4; ++i) x.B[n][i] = ssd::gload1(rb, at(n, i));
+            const int row = 16 * (n * WAVES + w) + l16;   // past dk: past the end
 #pragma unroll
-            for (int x = 0; x < KS; ++x)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int c = 16 * x + g4 + i;
-                    M[n][x][i] = ssd::gload1(rm, row < a.dk && c < a.dk ? (uint32_t)(row * a.dk + c) * 4u : kOOB);
-                }
+            for (int k = 0; k < KS; ++k) {
+                const int c = 16 * k + g4;
+                const uint32_t o = c < a.map_cols ? (uint32_t)(row * a.map_cols + c) * 4u : kOOB;
+                x.M[n][k] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rm, o, 0, 0));
+            }
         }
     };
+    f32x4 S[NR];
     {
         const float *from = p.carry ? a.states + ((int64_t)p.slot * a.H + h) * state : nullptr;
         const rsrc_t r = make_rsrc(from, from ? state * 4 : 0);
@@ -655,37 +658,52 @@ __global__ __launch_bounds__(64 * CarryWaves<KP>::n) void k_delta_carry(DeltaArg
 #pragma unroll
             for (int i = 0; i < 4; ++i) S[n][i] = ssd::gload1(r, at(n, i));
     }
-    load(0);
-    for (int s = 0; s < p.segs; ++s) {
+    // leaves S in place of B; false where that was the last
+    const auto enter = [&](int s) {
         float *st = St[s & 1];
         const rsrc_t r = make_rsrc(ends + s * (a.H * state), state * 4);
 #pragma unroll
         for (int n = 0; n < NR; ++n) {
             *reinterpret_cast<f32x4 *>(st + l16 * LS + 16 * (n * WAVES + w) + g4) = S[n];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) ssd::gstore1(r, at(n, i), S[n][i]);   // after this lane's B was read
+            for (int i = 0; i < 4; ++i) ssd::gstore1(r, at(n, i), S[n][i]);
         }
-        if (s + 1 == p.segs) break;
-        block_sync();
-        f32x4 sum[NR][2];
+        return s + 1 < p.segs;
+    };
+    const auto join = [&](const Step &x, int s) {
+        const float *st = St[s & 1];
+        f32x4 sum[NR][4];   // chains that do not wait for each other
 #pragma unroll
         for (int n = 0; n < NR; ++n) {
-            sum[n][0] = B[n];
-            sum[n][1] = f32x4{};
+            sum[n][0] = x.B[n];
+            sum[n][1] = sum[n][2] = sum[n][3] = f32x4{};
         }
 #pragma unroll
-        for (int x = 0; x < KS; ++x) {
-            const f32x4 f = *reinterpret_cast<const f32x4 *>(st + l16 * LS + 16 * x + g4);
+        for (int k = 0; k < KS; ++k) {
+            const f32x4 f = *reinterpret_cast<const f32x4 *>(st + l16 * LS + 16 * k + g4);
 #pragma unroll
             for (int e = 0; e < 4; ++e)
 #pragma unroll
                 for (int n = 0; n < NR; ++n)
-                    sum[n][x & 1] = __builtin_amdgcn_mfma_f32_16x16x4f32(M[n][x][e], f[e], sum[n][x & 1], 0, 0, 0);
+                    sum[n][e] = __builtin_amdgcn_mfma_f32_16x16x4f32(x.M[n][k][e], f[e], sum[n][e], 0, 0, 0);
         }
 #pragma unroll
-        for (int n = 0; n < NR; ++n) S[n] = sum[n][0] + sum[n][1];
-        if (s + 2 < p.segs) load(s + 1);   // the last segment made none
-    }
+        for (int n = 0; n < NR; ++n) S[n] = (sum[n][0] + sum[n][1]) + (sum[n][2] + sum[n][3]);
+    };
+    // the maps of AHEAD segments in flight; the last segment made none, and the
+    // loads past it are of the one before
+    const int last = p.segs - 2;
+    Step x[AHEAD];
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u) load(x[u], min(u, last));
+    for (int s0 = 0;; s0 += AHEAD)
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u) {
+            if (!enter(s0 + u)) return;
+            block_sync();
+            join(x[u], s0 + u);
+            load(x[u], min(s0 + u + AHEAD, last));
+        }
 }
 
 // ---- host side
@@ -693,7 +711,7 @@ __global__ __launch_bounds__(64 * CarryWaves<KP>::n) void k_delta_carry(DeltaArg
 static int col_tile(int64_t dk, int64_t dv) { return dk > 128 || dv <= 64 ? 64 : 128; }
 
 struct DeltaPlan {
-    int seg = 0, ids = 0, map_tiles = 0;
+    int seg = 0, ids = 0, map_cols = 0, map_tiles = 0;
     size_t ends = 0, maps = 0, total = 0;
 };
 
@@ -710,6 +728,7 @@ static DeltaPlan plan_delta(const lin_shape &s, int dtype, int64_t max_seqlen, i
     const int64_t vt = col_tile(s.dk, s.dv), tiles = (s.dv + vt - 1) / vt, map_tiles = (s.dk + vt - 1) / vt;
     const int64_t places = (vt == 64 && s.dk <= 128 && dtype == LAYER_BF16 ? 2 : 1) * (int64_t)cus;
     P.ids = (int)s.N;
+    P.map_cols = (int)((s.dk + 3) / 4 * 4);
     P.map_tiles = (int)map_tiles;
     int64_t seg = ((s.T * s.H * tiles + places - 1) / places + 63) / 64 * 64;
     if (seg < 256) seg = 256;
@@ -728,7 +747,7 @@ static DeltaPlan plan_delta(const lin_shape &s, int dtype, int64_t max_seqlen, i
     P.ids = (int)(s.T / seg + s.N);
     P.ends = 0;
     P.maps = ((size_t)(P.ids * s.H * s.dk * s.dv) * sizeof(float) + 255) / 256 * 256;
-    P.total = P.maps + (size_t)(P.ids * s.H * s.dk * s.dk) * sizeof(float);
+    P.total = P.maps + (size_t)(P.ids * s.H * s.dk * P.map_cols) * sizeof(float);
     return P;
 }
 
@@ -818,6 +837,7 @@ extern "C" int delta_prefill(const lin_shape *shape, int dtype, const lin_stride
     a.ends = reinterpret_cast<float *>(static_cast<char *>(workspace) + P.ends);
     a.maps = reinterpret_cast<float *>(static_cast<char *>(workspace) + P.maps);
     a.segdec = nullptr;
+    a.map_cols = P.map_cols;
     a.map_tiles = P.map_tiles;
     a.T = (int)s.T;
     a.N = (int)s.N;
