@@ -36,6 +36,7 @@ struct DeltaBackArgs : DeltaArgs {
     void *dq, *dk_out, *dv_out;
     float *dla, *dla_rows, *dbeta, *dfirst;
     int dvp, cb;
+    bool clear;                    // zeros for the gradients of rows of no sequence
 };
 
 // ---- T~ = (I + M diag(beta))^-1, T^T and P^T of a chunk of 32 rows, in pieces
@@ -269,15 +270,11 @@ __device__ __forceinline__ void walk(const DeltaBackArgs &a, WalkLds<E, KP> &lds
 #pragma unroll
             for (int i = 0; i < 4; ++i) S[m][i] = ssd::gload1(r, state_at(m, i, a.dv));
     }
-    block_sync();
-    for (int c = 0; c < chunks; ++c) {
-        const int b = c & 1, cc = chunk(c);
-        const Decays<C> &d = lds.dec[c % 3];
-        const float *betas = lds.beta[c % 3];
-        const L *qs = lds.q[b], *ks = lds.k[b], *vs = lds.v[b];
-        const int64_t id = (id0 + cc) * a.H + h;
-        const char *image = a.inv + id * 3 * PC::BYTES;
-        Frag<L> ft[2][PARTS], fp[2][PARTS];
+    // the pieces of T~, or of T^T and P^T: a chunk's are on their way while the
+    // chunk before it ends
+    Frag<L> ft[2][PARTS], fp[2][PARTS];
+    const auto load_pieces = [&](int c) {
+        const char *image = a.inv + ((id0 + chunk(min(c, chunks - 1))) * a.H + h) * 3 * PC::BYTES;
 #pragma unroll
         for (int f = 0; f < 2; ++f)
 #pragma unroll
@@ -285,6 +282,15 @@ __device__ __forceinline__ void walk(const DeltaBackArgs &a, WalkLds<E, KP> &lds
                 if (BACK) fp[f][u] = piece<L, C>(image + 2 * PC::BYTES, f, u, lane);
                 ft[f][u] = piece<L, C>(image + (BACK ? PC::BYTES : 0), f, u, lane);
             }
+    };
+    if (chunks > 0) load_pieces(0);
+    block_sync();
+    for (int c = 0; c < chunks; ++c) {
+        const int b = c & 1, cc = chunk(c);
+        const Decays<C> &d = lds.dec[c % 3];
+        const float *betas = lds.beta[c % 3];
+        const L *qs = lds.q[b], *ks = lds.k[b], *vs = lds.v[b];
+        const int64_t id = (id0 + cc) * a.H + h;
         // the state that enters the chunk of cb rows, or the gradient of the one that leaves it
         if (BACK ? (cc + 1) % (a.cb / C) == 0 || cc + 1 == chunks : cc % (a.cb / C) == 0) {
             float *to = (BACK ? a.arec : a.srec) + ((int64_t)chunk_number(n, begin, cc * C, a.cb) * a.H + h) * rec;
@@ -294,18 +300,26 @@ __device__ __forceinline__ void walk(const DeltaBackArgs &a, WalkLds<E, KP> &lds
 #pragma unroll
                 for (int i = 0; i < 4; ++i) ssd::gstore1(r, state_at(m, i, a.dvp), S[m][i]);
         }
-        f32x4 X[2] = {};
+        f32x4 X[2], part[2][PARTS] = {};   // chains that do not wait for each other
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
             Frag<L> fs[PARTS];
             split(fs, S[2 * s], S[2 * s + 1]);
+            const Frag<L> fk0 = frag8(ks + l16 * LK + 32 * s + 2 * g4), fk1 = frag8(ks + (16 + l16) * LK + 32 * s + 2 * g4);
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                const Frag<L> fk = frag8(ks + (16 * t + l16) * LK + 32 * s + 2 * g4);
-#pragma unroll
-                for (int u = PARTS - 1; u >= 0; --u) X[t] = mma(fk, fs[u], X[t]);
+            for (int u = PARTS - 1; u >= 0; --u) {
+                part[0][u] = mma(fk0, fs[u], part[0][u]);
+                part[1][u] = mma(fk1, fs[u], part[1][u]);
             }
         }
+        const auto summed = [&](int t) {
+            f32x4 x = part[t][PARTS - 1];
+#pragma unroll
+            for (int u = PARTS - 2; u >= 0; --u) x += part[t][u];
+            return x;
+        };
+        X[0] = summed(0);
+        X[1] = summed(1);
         const f32x4 ea = *reinterpret_cast<const f32x4 *>(d.in + g4), eb = *reinterpret_cast<const f32x4 *>(d.in + 16 + g4);
         const f32x4 wa = *reinterpret_cast<const f32x4 *>(d.out + g4), wb = *reinterpret_cast<const f32x4 *>(d.out + 16 + g4);
         const f32x4 ba = *reinterpret_cast<const f32x4 *>(betas + g4), bb = *reinterpret_cast<const f32x4 *>(betas + 16 + g4);
@@ -323,18 +337,25 @@ __device__ __forceinline__ void walk(const DeltaBackArgs &a, WalkLds<E, KP> &lds
 #pragma unroll
             for (int u = PARTS - 1; u >= 0; --u)
 #pragma unroll
-                for (int t = 0; t < 2; ++t) X[t] = mma(fp[t][u], fv, X[t]);
-            split(fx, X[0], X[1]);
+                for (int t = 0; t < 2; ++t) part[t][u] = mma(fp[t][u], fv, f32x4{});
+            split(fx, X[0] + summed(0), X[1] + summed(1));
         } else {
             split(fx, va - ea * X[0], vb - eb * X[1]);
         }
-        f32x4 R[2] = {};   // Z, or dG
+        f32x4 R[2];   // Z, or dG
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int u = 0; u < PARTS; ++u) part[t][u] = f32x4{};
 #pragma unroll
         for (int o = PARTS - 1; o >= 0; --o)
 #pragma unroll
             for (int u = 0; u <= o; ++u)
 #pragma unroll
-                for (int t = 0; t < 2; ++t) R[t] = mma(ft[t][u], fx[o - u], R[t]);
+                for (int t = 0; t < 2; ++t) part[t][o] = mma(ft[t][u], fx[o - u], part[t][o]);
+        R[0] = summed(0);
+        R[1] = summed(1);
+        load_pieces(c + 1);
         {
             float *to = (BACK ? a.grec : a.zrec) + id * C * a.dvp;
             const rsrc_t r = make_rsrc(to, (int64_t)C * a.dvp * 4);
@@ -380,6 +401,27 @@ template <typename E, int KP, bool VEC>
 __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_delta_walk(DeltaBackArgs a)
 {
     __shared__ __align__(16) WalkLds<E, KP> lds;
+    if (a.clear) {
+        int b0, b1, e0, e1;
+        rows_of(a, 0, b0, e0);
+        rows_of(a, a.N - 1, b1, e1);
+        for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+            if (t >= b0 && t < e1) {
+                t += (e1 - 1 - t) / gridDim.x * gridDim.x;   // the last of these that is a sequence's
+                continue;
+            }
+            const int qk = a.G * a.dk, hv = a.H * a.dv;
+            for (int i = threadIdx.x; i < qk; i += 512) {
+                static_cast<E *>(a.dq)[t * qk + i] = (E)0.f;
+                static_cast<E *>(a.dk_out)[t * qk + i] = (E)0.f;
+            }
+            for (int i = threadIdx.x; i < hv; i += 512) static_cast<E *>(a.dv_out)[t * hv + i] = (E)0.f;
+            for (int i = threadIdx.x; i < a.H; i += 512) {
+                a.dbeta[t * a.H + i] = 0.f;
+                a.dla_rows[t * a.H + i] = 0.f;
+            }
+        }
+    }
     const int tile = blockIdx.x % a.tiles, h = blockIdx.x / a.tiles % a.H;
     const int n = blockIdx.x / (a.tiles * a.H) % a.N;
     if (blockIdx.x / (a.tiles * a.H) < (unsigned)a.N)
@@ -827,7 +869,8 @@ extern "C" int delta_bwd(const lin_shape *shape, int dtype, const lin_strides *s
                          const void *v, const float *log_decay, int64_t decay_stride, const float *beta,
                          int64_t beta_stride, const int32_t *cu_seqlens, const float *states, const void *dy,
                          const float *dstates_last, void *dq, void *dk, void *dv, float *dlog_decay, int decay_by_row,
-                         float *dbeta, float *dstates, void *workspace, size_t workspace_bytes, void *stream)
+                         float *dbeta, float *dstates, int clear, void *workspace, size_t workspace_bytes,
+                         void *stream)
 {
     int rc = check_delta_bwd(shape);
     if (rc == SSD_OK) rc = check_dtype(dtype);
@@ -886,6 +929,7 @@ extern "C" int delta_bwd(const lin_shape *shape, int dtype, const lin_strides *s
     a.dfirst = dstates;
     a.dvp = P.dvp;
     a.cb = P.cb;
+    a.clear = clear != 0;
     a.T = (int)s.T;
     a.N = (int)s.N;
     a.G = (int)s.G;

@@ -68,7 +68,7 @@ def declare(lib):
     lib.delta_bwd_workspace_size.argtypes = [lp]
     lib.delta_bwd_workspace_size.restype = _sz
     lib.delta_bwd.argtypes = [lp, _int, tp, _vp, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
-                              _int, _vp, _vp, _vp, _sz, _vp]
+                              _int, _vp, _vp, _int, _vp, _sz, _vp]
     for fn in (lib.gn_fwd_workspace_size, lib.gn_bwd_workspace_size):
         fn.argtypes = [gp]
         fn.restype = _sz
@@ -369,8 +369,8 @@ def delta_bwd(q, k, v, log_decay, beta, cu_seqlens, dy, *, states=None, dstates=
     sp, dsp = (None if t is None else _dense(t, name, st, _torch.float32, dev)
                for t, name in ((states, "states"), (dstates, "dstates")))
     if out is None:
-        # rows of no sequence get no gradient; where the last offset ends is known on the device alone
-        new = v.new_zeros
+        # rows of no sequence get zeros, from the kernels: where the last offset ends is known on the device alone
+        new = v.new_empty if N else v.new_zeros
         dq, dk_, dv_ = new((T, G, dk)), new((T, G, dk)), new((T, H, dv))
         dla = new(log_decay.shape, dtype=_torch.float32)
         dbeta = new((T, H), dtype=_torch.float32)
@@ -389,7 +389,7 @@ def delta_bwd(q, k, v, log_decay, beta, cu_seqlens, dy, *, states=None, dstates=
     strides = _arg(LinStridesArg, *_rows(q, "q"), *_rows(k, "k"), *_rows(v, "v"), *_rows(dy, "dy"))
     _call(lib.delta_bwd, "delta_bwd", dev, s, code, strides, q.data_ptr() or None, k.data_ptr() or None,
           v.data_ptr() or None, log_decay.data_ptr() or None, ld, bp, lb, cu, sp, dy.data_ptr() or None, dsp, *ptrs[:4],
-          int(by_row), ptrs[4], d0p, wp, wn)
+          int(by_row), ptrs[4], d0p, int(out is None), wp, wn)
     return dq, dk_, dv_, dla, dbeta, d0
 
 

@@ -482,7 +482,8 @@ int delta_step(const lin_shape *shape, int dtype, const lin_strides *strides,
  * fixed order); dbeta [T][H]; dstates [N][H][dk][dv], or NULL if not wanted.
  * states and dstates_last are float32 [N][H][dk][dv] or NULL; the strides of
  * y are dy's, and may be 0 here.  shape->slots is not read.  Rows of no
- * sequence are not read, and their gradients are left as they were.
+ * sequence are not read; their gradients are left as they were, or, where
+ * `clear` is not 0 and there is a sequence, set to zero.
  * Every sum and every value between is float32, or three bfloat16 numbers
  * that hold one; nothing of a forward call is needed.  The states of every
  * 64th row (32nd for dk over 128) are kept in the workspace meanwhile, twice.
@@ -498,7 +499,7 @@ int delta_bwd(const lin_shape *shape, int dtype, const lin_strides *strides,
               const float *beta, int64_t beta_stride, const int32_t *cu_seqlens,
               const float *states, const void *dy, const float *dstates_last,
               void *dq, void *dk, void *dv, float *dlog_decay, int decay_by_row,
-              float *dbeta, float *dstates,
+              float *dbeta, float *dstates, int clear,
               void *workspace, size_t workspace_bytes, void *stream);
 
 /* Group norm, channels last, with an activation.  x is N samples of L rows

@@ -38,7 +38,7 @@ def call(shape, which, dtype=1, strides=None, ptr=P, ld=0, lb=8, max_len=0, ws=B
         return lib.delta_prefill(s, dtype, st, p["q"], p["k"], p["v"], p["la"], ld, p["beta"], lb, p["cu"], p["slots"],
                                  p["carry"], max_len, p["states"], p["y"], *ws, None)
     return lib.delta_bwd(s, dtype, st, p["q"], p["k"], p["v"], p["la"], ld, p["beta"], lb, p["cu"], p["states"], p["dy"],
-                         p["dlast"], p["dq"], p["dk"], p["dv"], p["dla"], by_row, p["dbeta"], p["d0"], *ws, None)
+                         p["dlast"], p["dq"], p["dk"], p["dv"], p["dla"], by_row, p["dbeta"], p["d0"], 0, *ws, None)
 
 
 @pytest.mark.parametrize("which", ["prefill", "step", "bwd"])
@@ -98,7 +98,7 @@ def test_null_shapes_and_sizes():
     lib = ssd.library()
     assert lib.delta_prefill(None, 0, None, *[None] * 4, 0, None, 0, *[None] * 3, 0, *[None] * 3, 0, None) == NULL
     assert lib.delta_step(None, 0, None, *[None] * 4, 0, None, 0, *[None] * 4) == NULL
-    assert lib.delta_bwd(None, 0, None, *[None] * 4, 0, None, 0, *[None] * 8, 0, *[None] * 3, 0, None) == NULL
+    assert lib.delta_bwd(None, 0, None, *[None] * 4, 0, None, 0, *[None] * 8, 0, None, None, 0, None, 0, None) == NULL
     with pytest.raises(ValueError):
         ssd.layer.delta_prefill_workspace_size(5, 2, 3, 4, 8, 8, 4)
     with pytest.raises(ValueError):
