@@ -430,6 +430,15 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
         walk<E, KP, VEC, false>(a, lds, n, h, tile);
 }
 
+// The sum over 16 lanes that follow one another, in all of them.
+__device__ __forceinline__ float sum16(float x)
+{
+    x = ssd::dpp_add<ssd::kRowRor + 8>(x);
+    x = ssd::dpp_add<ssd::kRowRor + 4>(x);
+    x = ssd::dpp_add<ssd::kRowRor + 2>(x);
+    return ssd::dpp_add<ssd::kRowRor + 1>(x);
+}
+
 // ---- the products inside a chunk of CB rows
 //
 // All on fp32 MFMA.  A wave has 16 columns of dQ and dK (two times 16 where dk
@@ -597,8 +606,7 @@ __global__ __launch_bounds__(64 * GradsLds<KP>::WAVES) void k_delta_grads(DeltaB
             if (!isP) v = -v;
             float n = j < i ? v * s[e] : 0.f;   // the diagonal depends on no decay
             by_col += n;
-#pragma unroll
-            for (int o = 1; o < 16; o *= 2) n += __shfl_xor(n, o);
+            n = sum16(n);
             if (l16 == 0) lds.rowsum[u][g4 + e] = n;
             if (isP) {
                 lds.pair.dp[i * LP + j] = v;
@@ -670,9 +678,7 @@ __global__ __launch_bounds__(64 * GradsLds<KP>::WAVES) void k_delta_grads(DeltaB
         for (int t = 0; t < TT; ++t)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                float s = sums[x][t][e];
-#pragma unroll
-                for (int o = 1; o < 16; o *= 2) s += __shfl_xor(s, o);
+                const float s = sum16(sums[x][t][e]);
                 if (l16 == 0) lds.sums[x][w][16 * t + g4 + e] = s;
             }
 #pragma unroll
@@ -709,6 +715,356 @@ __global__ __launch_bounds__(64 * GradsLds<KP>::WAVES) void k_delta_grads(DeltaB
         const double pre = scan64(lane > 0 ? before : 0.), post = __shfl(scan64(__shfl(f, 63 - lane)), 63 - lane);
         const double r = post + pre + (double)d.all * all;
         if (lane < p.rows && lane < CB) a.dla_rows[(row0 + lane) * a.H + h] = (float)r;
+    }
+}
+
+// The same for bfloat16 calls with dk up to 128, on bf16 MFMA: whatever enters
+// dlog_decay or dbeta as a sum of three bfloat16 numbers, split once on its way
+// to LDS (six products for two such operands, the ones of 2^-24 and less left
+// out), dP and dM, which meet K and Q for dQ and dK alone, of two.
+//
+// S, A, dR, U and dY pass through LDS 32 columns at a time, S and A one after
+// the other in one place, and q and k take it over after them, so that two
+// blocks share a CU and fill each other's waits.
+template <int KP>
+struct GradsBfLds {
+    static constexpr int CB = 64, WAVES = 4, SL = 32, TT = 4, TILES = 10;
+    static constexpr int LK = KP + 16, LS = SL + 16, LP = CB + 16, NS = KP / 16 / WAVES;
+    union {
+        struct {
+            alignas(16) bf16 dy[CB * LS], u[3][CB * LS], dr[3][CB * LS], s[3][KP * LS];
+        } in;
+        struct {
+            alignas(16) bf16 q[CB * LK], k[CB * LK];
+            union {
+                struct {
+                    alignas(16) bf16 dp[2][CB * LP], dm[2][CB * LP];
+                };
+                float sums[3][WAVES][CB];   // after them
+            };
+            float rowsum[2 * TILES][16], colsum[2 * TILES][16];
+        } pair;
+    };
+    Decays<CB> dec;
+    alignas(16) float beta[CB];
+    float dot[WAVES];
+};
+
+template <int KP, bool VEC>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_delta_grads_bf(DeltaBackArgs a)
+{
+    typedef GradsBfLds<KP> Lds;
+    typedef bf16 E;
+    constexpr int CB = Lds::CB, WAVES = Lds::WAVES, SL = Lds::SL, TT = Lds::TT, TILES = Lds::TILES, NS = Lds::NS;
+    constexpr int LK = Lds::LK, LS = Lds::LS, LP = Lds::LP, PT = 256, KS = KP / 32, RROWS = PT / 8;
+    constexpr int TS = CB / 32, PAIRS = (2 * TILES + WAVES - 1) / WAVES, RPER = CB / RROWS, SPER = KP / RROWS;
+    __shared__ Lds lds;
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int l16 = lane & 15, g4 = (lane >> 4) * 4;
+    const int h = blockIdx.x % a.H;
+    int id = blockIdx.x / a.H;
+    Place p;
+    if (!find(a, id, p) || p.rows <= 0) return;
+    const int g = h / (a.H / a.G);
+    const int first = p.begin - p.s * CB;
+    const int64_t row0 = p.begin, idw = chunk_number(p.n, first, p.s * CB, CW);
+    const float *srec = a.srec + ((int64_t)id * a.H + h) * a.dk * a.dvp;
+    const float *arec = a.arec + ((int64_t)id * a.H + h) * a.dk * a.dvp;
+    const int64_t rec_step = (int64_t)a.H * CW * a.dvp;
+    const float *zrec = a.zrec + (idw * a.H + h) * CW * a.dvp, *grec = a.grec + (idw * a.H + h) * CW * a.dvp;
+    const E *dy = static_cast<const E *>(a.dy) + row0 * a.st.y_t + h * a.st.y_h;
+
+    // a thread's four columns, of RPER rows of Z and dG and of SPER rows of S and A
+    const int row = tid / 8, col8 = tid % 8 * 4;
+    Tile<E, CB, SL, PT> ty;
+    f32x4 tz[RPER], tg[RPER], ts[SPER], ta[SPER];
+    const auto load = [&](int c0) {
+        ty.template load<VEC>(dy + c0, a.st.y_t, c0 < a.dv ? p.rows : 0, min(SL, a.dv - c0), tid);
+        const int col = c0 + col8;
+#pragma unroll
+        for (int u = 0; u < RPER; ++u) {
+            const int r = u * RROWS + row;
+            const bool on = r < p.rows && col < a.dvp;
+            const int64_t at = r / CW * rec_step + (int64_t)(r % CW) * a.dvp + col;
+            tz[u] = on ? *reinterpret_cast<const f32x4 *>(zrec + at) : f32x4{};
+            tg[u] = on ? *reinterpret_cast<const f32x4 *>(grec + at) : f32x4{};
+        }
+#pragma unroll
+        for (int u = 0; u < SPER; ++u) {
+            const int r = u * RROWS + row;
+            const bool live = r < a.dk && col < a.dvp;
+            ts[u] = live ? *reinterpret_cast<const f32x4 *>(srec + (int64_t)r * a.dvp + col) : f32x4{};
+            ta[u] = live ? *reinterpret_cast<const f32x4 *>(arec + (int64_t)r * a.dvp + col) : f32x4{};
+        }
+    };
+    const auto put = [&](auto &to, int r, f32x4 x) {
+        bf16x4 parts[3];
+        split4(parts, x);
+#pragma unroll
+        for (int u = 0; u < 3; ++u) *reinterpret_cast<bf16x4 *>(to[u] + r * LS + col8) = parts[u];
+    };
+    load(0);
+    {
+        const bool on = lane < p.rows;
+        if (w == 0) make_decays(lds.dec, on ? a.la[(a.la_t ? (row0 + lane) * a.la_t : 0) + h] : 0.f, lane);
+        if (w == 1) lds.beta[lane] = on ? a.beta[(row0 + lane) * a.beta_t + h] : 0.f;
+    }
+    block_sync();
+    f32x4 dyS[NS][TT] = {}, dRS[NS][TT] = {}, UA[NS][TT] = {}, pair[PAIRS] = {};
+    float dbeta[RPER] = {}, dot = 0.f;
+    for (int c0 = 0; c0 < a.dv; c0 += SL) {
+        ty.template store<LS>(lds.in.dy, tid);
+#pragma unroll
+        for (int u = 0; u < RPER; ++u) {
+            const int r = u * RROWS + row;
+            const float bt = lds.beta[r];
+            const f32x4 dr = tg[u] * bt;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) dbeta[u] += tg[u][i] * tz[u][i];
+            put(lds.in.u, r, tz[u] * bt);
+            put(lds.in.dr, r, dr);
+            if (r < p.rows) {
+                E *to = static_cast<E *>(a.dv_out) + ((row0 + r) * a.H + h) * a.dv + c0 + col8;
+                if (VEC && c0 + col8 < a.dv) {
+                    *reinterpret_cast<bf16x4 *>(to) = __builtin_convertvector(dr, bf16x4);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (c0 + col8 + i < a.dv) to[i] = from_f<E>(dr[i]);
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < SPER; ++u) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) dot += ts[u][i] * ta[u][i];
+            put(lds.in.s, u * RROWS + row, ts[u]);
+        }
+        block_sync();
+        {
+            Frag<bf16> fs[NS][3];
+#pragma unroll
+            for (int n = 0; n < NS; ++n)
+#pragma unroll
+                for (int u = 0; u < 3; ++u) fs[n][u] = frag8(lds.in.s[u] + (16 * (n * WAVES + w) + l16) * LS + 2 * g4);
+#pragma unroll
+            for (int t = 0; t < TT; ++t) {
+                const int at = (16 * t + l16) * LS + 2 * g4;
+                const Frag<bf16> fy = frag8(lds.in.dy + at);
+                Frag<bf16> fr[3];
+#pragma unroll
+                for (int u = 0; u < 3; ++u) fr[u] = frag8(lds.in.dr[u] + at);
+#pragma unroll
+                for (int o = 2; o >= 0; --o)   // the small products first
+#pragma unroll
+                    for (int n = 0; n < NS; ++n) {
+                        dyS[n][t] = mma(fy, fs[n][o], dyS[n][t]);
+#pragma unroll
+                        for (int u = 0; u <= o; ++u) dRS[n][t] = mma(fr[u], fs[n][o - u], dRS[n][t]);
+                    }
+            }
+        }
+        // U dY^T and U dR^T: lane holds rows j of U, column i of dY or dR
+#pragma unroll
+        for (int x = 0; x < PAIRS; ++x) {
+            const int u = x * WAVES + w, f = u < TILES ? u : u - TILES;
+            if (u >= 2 * TILES) continue;
+            const int it = (f > 0) + (f > 2) + (f > 5), jt = f - it * (it + 1) / 2;
+            const int ai = (16 * it + l16) * LS + 2 * g4, aj = (16 * jt + l16) * LS + 2 * g4;
+            if (u < TILES) {
+                const Frag<bf16> fy = frag8(lds.in.dy + ai);
+#pragma unroll
+                for (int o = 2; o >= 0; --o) pair[x] = mma(frag8(lds.in.u[o] + aj), fy, pair[x]);
+            } else {
+                Frag<bf16> fr[3], fu[3];
+#pragma unroll
+                for (int o = 0; o < 3; ++o) {
+                    fr[o] = frag8(lds.in.dr[o] + ai);
+                    fu[o] = frag8(lds.in.u[o] + aj);
+                }
+#pragma unroll
+                for (int o = 2; o >= 0; --o)
+#pragma unroll
+                    for (int z = 0; z <= o; ++z) pair[x] = mma(fu[z], fr[o - z], pair[x]);
+            }
+        }
+        block_sync();
+#pragma unroll
+        for (int u = 0; u < SPER; ++u) put(lds.in.s, u * RROWS + row, ta[u]);   // A in S's place
+        block_sync();
+        load(c0 + SL);
+        {
+            Frag<bf16> fa[NS][3];
+#pragma unroll
+            for (int n = 0; n < NS; ++n)
+#pragma unroll
+                for (int u = 0; u < 3; ++u) fa[n][u] = frag8(lds.in.s[u] + (16 * (n * WAVES + w) + l16) * LS + 2 * g4);
+#pragma unroll
+            for (int t = 0; t < TT; ++t) {
+                Frag<bf16> fu[3];
+#pragma unroll
+                for (int u = 0; u < 3; ++u) fu[u] = frag8(lds.in.u[u] + (16 * t + l16) * LS + 2 * g4);
+#pragma unroll
+                for (int o = 2; o >= 0; --o)
+#pragma unroll
+                    for (int u = 0; u <= o; ++u)
+#pragma unroll
+                        for (int n = 0; n < NS; ++n) UA[n][t] = mma(fu[u], fa[n][o - u], UA[n][t]);
+            }
+        }
+        block_sync();
+    }
+    {
+        Tile<E, CB, KP, PT> tk, tq;
+        tk.template load<VEC>(static_cast<const E *>(a.k) + row0 * a.st.k_t + g * a.st.k_g, a.st.k_t, p.rows, a.dk, tid);
+        tq.template load<VEC>(static_cast<const E *>(a.q) + row0 * a.st.q_t + g * a.st.q_g, a.st.q_t, p.rows, a.dk, tid);
+        tk.template store<LK>(lds.pair.k, tid);
+        tq.template store<LK>(lds.pair.q, tid);
+    }
+    block_sync();
+    const Decays<CB> &d = lds.dec;
+    // dP and dM below the diagonal, their columns in the order in which the
+    // products take them, and N's sums by rows and columns
+#pragma unroll
+    for (int x = 0; x < PAIRS; ++x) {
+        const int u = x * WAVES + w, f = u < TILES ? u : u - TILES;
+        if (u >= 2 * TILES) continue;
+        const bool isP = u < TILES;
+        const int it = (f > 0) + (f > 2) + (f > 5), jt = f - it * (it + 1) / 2;
+        const bf16 *rows = isP ? lds.pair.q : lds.pair.k;
+        f32x4 s = {};
+#pragma unroll
+        for (int m = 0; m < KS; ++m)
+            s = mma(frag8(lds.pair.k + (16 * jt + l16) * LK + 32 * m + 2 * g4), frag8(rows + (16 * it + l16) * LK + 32 * m + 2 * g4),
+                    s);
+        const f32x4 jh = *reinterpret_cast<const f32x4 *>(d.hi + 16 * jt + g4);
+        const f32x4 jl = *reinterpret_cast<const f32x4 *>(d.lo + 16 * jt + g4);
+        const int i = 16 * it + l16;
+        const float ih = d.hi[i], il = d.lo[i];
+        float by_row = 0.f;
+        f32x4 v;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int j = 16 * jt + g4 + e;
+            v[e] = pair[x][e] * __expf((ih - jh[e]) + (il - jl[e]));
+            if (isP ? j > i : j >= i) v[e] = 0.f;
+            if (!isP) v[e] = -v[e];
+            float n = j < i ? v[e] * s[e] : 0.f;   // the diagonal depends on no decay
+            by_row += n;
+            n = sum16(n);
+            if (l16 == 0) lds.pair.colsum[u][g4 + e] = n;
+        }
+        by_row += __shfl_xor(by_row, 16);
+        by_row += __shfl_xor(by_row, 32);
+        if (lane < 16) lds.pair.rowsum[u][lane] = by_row;
+        bf16x4 parts[2];
+        split4(parts, v);
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+            bf16 *to = (isP ? lds.pair.dp[z] : lds.pair.dm[z]) + i * LP + 32 * (jt / 2) + 2 * g4;
+            *reinterpret_cast<bf16x4 *>(to + 4 * (jt % 2)) = parts[z];
+            // right of a tile on the diagonal, what the same pieces hold
+            if (it == jt && it % 2 == 0) *reinterpret_cast<bf16x4 *>(to + 4) = bf16x4{};
+        }
+    }
+    block_sync();
+    float sums[3][TT][4] = {};   // of f's two terms and of e, over this lane's columns
+#pragma unroll
+    for (int n = 0; n < NS; ++n) {
+        const int c16 = 16 * (n * WAVES + w), col = c16 + l16;
+        Frag<bf16> kc[TS], qc[TS];
+#pragma unroll
+        for (int s = 0; s < TS; ++s) {
+            kc[s] = frag_col<LK, false>(lds.pair.k + 32 * s * LK, c16, lane);
+            qc[s] = frag_col<LK, false>(lds.pair.q + 32 * s * LK, c16, lane);
+        }
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+            const f32x4 eb = *reinterpret_cast<const f32x4 *>(d.in + 16 * t + g4);
+            const f32x4 wb = *reinterpret_cast<const f32x4 *>(d.out + 16 * t + g4);
+            f32x4 gq = dyS[n][t] * eb, gr = dRS[n][t] * eb, gu = UA[n][t] * wb;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int at = (16 * t + g4 + e) * LK + col;
+                const float qv = to_f(lds.pair.q[at]), kv = to_f(lds.pair.k[at]);
+                sums[0][t][e] += qv * gq[e];
+                sums[1][t][e] += kv * gr[e];
+                sums[2][t][e] += kv * gu[e];
+            }
+            f32x4 gk = gu - gr;
+            // rows of dP and dM, and of their transposes
+#pragma unroll
+            for (int s = 0; s < TS; ++s)
+#pragma unroll
+                for (int z = 1; z >= 0; --z) {
+                    if (s <= t / 2) {
+                        const int at = (16 * t + l16) * LP + 32 * s + 2 * g4;
+                        gq = mma(frag8(lds.pair.dp[z] + at), kc[s], gq);
+                        gk = mma(frag8(lds.pair.dm[z] + at), kc[s], gk);
+                    }
+                    if (s >= t / 2) {
+                        const int c = 32 * (t / 2) + 4 * (t % 2);
+                        gk = mma(frag_col<LP, true>(lds.pair.dp[z] + 32 * s * LP, c, lane), qc[s], gk);
+                        gk = mma(frag_col<LP, true>(lds.pair.dm[z] + 32 * s * LP, c, lane), kc[s], gk);
+                    }
+                }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int r = 16 * t + g4 + e;
+                if (r >= p.rows || col >= a.dk) continue;
+                if (a.G == a.H) {
+                    const int64_t at = ((row0 + r) * a.G + g) * a.dk + col;
+                    static_cast<E *>(a.dq)[at] = from_f<E>(gq[e]);
+                    static_cast<E *>(a.dk_out)[at] = from_f<E>(gk[e]);
+                } else {
+                    const int64_t at = ((row0 + r) * a.H + h) * a.dk + col;
+                    a.dq_head[at] = gq[e];
+                    a.dk_head[at] = gk[e];
+                }
+            }
+        }
+    }
+    block_sync();   // the sums take the place of dP and dM
+#pragma unroll
+    for (int x = 0; x < 3; ++x)
+#pragma unroll
+        for (int t = 0; t < TT; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float s = sum16(sums[x][t][e]);
+                if (l16 == 0) lds.pair.sums[x][w][16 * t + g4 + e] = s;
+            }
+#pragma unroll
+    for (int o = 1; o < 64; o *= 2) dot += __shfl_xor(dot, o);
+    if (lane == 0) lds.dot[w] = dot;
+#pragma unroll
+    for (int u = 0; u < RPER; ++u) {
+        const int r = u * RROWS + row;
+#pragma unroll
+        for (int o = 1; o < 8; o *= 2) dbeta[u] += __shfl_xor(dbeta[u], o);
+        if (col8 == 0 && r < p.rows) a.dbeta[(row0 + r) * a.H + h] = dbeta[u];
+    }
+    block_sync();
+    if (w == 0) {
+        double f = 0., e = 0., all = 0.;
+#pragma unroll
+        for (int x = 0; x < WAVES; ++x) {
+            f += (double)lds.pair.sums[0][x][lane] - (double)lds.pair.sums[1][x][lane];
+            e += (double)lds.pair.sums[2][x][lane];
+            all += (double)lds.dot[x];
+        }
+        const int t = lane / 16;   // N's tiles of row block t, and of column block t
+#pragma unroll
+        for (int x = 0; x < TILES; ++x) {
+            const int it = (x > 0) + (x > 2) + (x > 5), jt = x - it * (it + 1) / 2;
+            if (it == t) e -= (double)lds.pair.rowsum[x][lane % 16] + (double)lds.pair.rowsum[TILES + x][lane % 16];
+            if (jt == t) e += (double)lds.pair.colsum[x][lane % 16] + (double)lds.pair.colsum[TILES + x][lane % 16];
+        }
+        // the rows before, and the rows from its own on: no sum is taken back
+        const double before = __shfl_up(e, 1);
+        const double pre = scan64(lane > 0 ? before : 0.), post = __shfl(scan64(__shfl(f, 63 - lane)), 63 - lane);
+        const double r = post + pre + (double)d.all * all;
+        if (lane < p.rows) a.dla_rows[(row0 + lane) * a.H + h] = (float)r;
     }
 }
 
@@ -832,7 +1188,11 @@ static int run_back(DeltaBackArgs &a, const DeltaBackPlan &P, hipStream_t st)
         DeltaBackArgs c = a;
         c.seg = GradsLds<KP>::CB;
         c.ids = (int)P.ids;
-        k_delta_grads<E, KP, VEC><<<dim3((unsigned)(P.ids * a.H)), dim3(64 * GradsLds<KP>::WAVES), 0, st>>>(c);
+        const dim3 grid((unsigned)(P.ids * a.H));
+        if constexpr (std::is_same<E, bf16>::value && KP <= 128)
+            k_delta_grads_bf<KP, VEC><<<grid, dim3(256), 0, st>>>(c);
+        else
+            k_delta_grads<E, KP, VEC><<<grid, dim3(64 * GradsLds<KP>::WAVES), 0, st>>>(c);
     }
     if (a.G != a.H) {
         const int v = a.dk % 4 == 0 ? 4 : 1;
