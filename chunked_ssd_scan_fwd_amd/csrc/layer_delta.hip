@@ -104,15 +104,15 @@ __attribute__((amdgpu_waves_per_eu(DeltaPerCu<E, KP, VT>::per_simd, DeltaPerCu<E
         Tile<E, C, VT, PT> tv;
         const auto load = [&](int c) {
             const int t0 = c * C, rows = p.rows - t0, tid = anew(threadIdx.x - 64 * WAVES);
-            if (OUT) tq.template load<VEC>(q + t0 * a.st.q_t, a.st.q_t, min(C, rows), a.dk, tid);
-            tk.template load<VEC>(k + t0 * a.st.k_t, a.st.k_t, min(C, rows), a.dk, tid);
-            tv.template load<VEC>(v + t0 * a.st.v_t, a.st.v_t, map ? 0 : min(C, rows), cols, tid);
+            if (OUT) tq.template fetch<VEC>(q + t0 * a.st.q_t, a.st.q_t, min(C, rows), a.dk, tid);
+            tk.template fetch<VEC>(k + t0 * a.st.k_t, a.st.k_t, min(C, rows), a.dk, tid);
+            tv.template fetch<VEC>(v + t0 * a.st.v_t, a.st.v_t, map ? 0 : min(C, rows), cols, tid);
         };
         const auto store = [&](int c) {
             const int b = c & 1, tid = anew(threadIdx.x - 64 * WAVES);
-            if (OUT) tq.template store<LK>(lds.q[b], tid);
-            tk.template store<LK>(lds.k[b], tid);
-            tv.template store<LV>(lds.v[b], tid);
+            if (OUT) tq.template place<VEC, LK>(lds.q[b], q + c * C * a.st.q_t, a.st.q_t, a.dk, tid);
+            tk.template place<VEC, LK>(lds.k[b], k + c * C * a.st.k_t, a.st.k_t, a.dk, tid);
+            tv.template place<VEC, LV>(lds.v[b], v + c * C * a.st.v_t, a.st.v_t, cols, tid);
         };
         const float *beta = a.beta + p.begin * a.beta_t + h;
         // a row's log decay (wave 0) or beta (wave 1), and what chunk c makes of them

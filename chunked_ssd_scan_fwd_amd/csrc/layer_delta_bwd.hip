@@ -60,17 +60,17 @@ __global__ __launch_bounds__(256) void k_delta_back_inverse(DeltaBackArgs a)
     const int g = h / (a.H / a.G);
     {
         Tile<E, CW, KP, PT> tk, tq;
-        tk.template load<VEC>(static_cast<const E *>(a.k) + p.begin * a.st.k_t + g * a.st.k_g, a.st.k_t, p.rows, a.dk,
-                              tid);
-        tq.template load<VEC>(static_cast<const E *>(a.q) + p.begin * a.st.q_t + g * a.st.q_g, a.st.q_t, p.rows, a.dk,
-                              tid);
+        const E *k = static_cast<const E *>(a.k) + p.begin * a.st.k_t + g * a.st.k_g;
+        const E *q = static_cast<const E *>(a.q) + p.begin * a.st.q_t + g * a.st.q_g;
+        tk.template fetch<VEC>(k, a.st.k_t, p.rows, a.dk, tid);
+        tq.template fetch<VEC>(q, a.st.q_t, p.rows, a.dk, tid);
         const int64_t row = p.begin + lane;
         const bool on = lane < p.rows;
         const float la = on ? a.la[(a.la_t ? row * a.la_t : 0) + h] : 0.f;
         if (w == 0) make_decays(d, la, lane);
         if (w == 1 && lane < CW) betas[lane] = on ? a.beta[row * a.beta_t + h] : 0.f;
-        tk.template store<LK>(ks, tid);
-        tq.template store<LK>(qs, tid);
+        tk.template place<VEC, LK>(ks, k, a.st.k_t, a.dk, tid);
+        tq.template place<VEC, LK>(qs, q, a.st.q_t, a.dk, tid);
     }
     block_sync();
     const auto product = [&](const L *rows, int i, int j) {   // rows_i k_j^T
@@ -221,9 +221,9 @@ __device__ __forceinline__ void walk(const DeltaBackArgs &a, WalkLds<E, KP> &lds
             const int64_t t0 = (int64_t)chunk(c) * C;
             const int left = c < chunks ? min(C, (int)(rows - t0)) : 0;
             const int64_t at = c < chunks ? t0 : 0;
-            if (BACK) tq.template load<VEC>(q + at * a.st.q_t, a.st.q_t, left, a.dk, tid);
-            tk.template load<VEC>(k + at * a.st.k_t, a.st.k_t, left, a.dk, tid);
-            tv.template load<VEC>(v + at * v_t, v_t, left, cols, tid);
+            if (BACK) tq.template fetch<VEC>(q + at * a.st.q_t, a.st.q_t, left, a.dk, tid);
+            tk.template fetch<VEC>(k + at * a.st.k_t, a.st.k_t, left, a.dk, tid);
+            tv.template fetch<VEC>(v + at * v_t, v_t, left, cols, tid);
         };
         const auto decays = [&](int c) {   // two waves: the log decays, and beta
             const int t = chunk(c) * C + lane;
@@ -233,9 +233,10 @@ __device__ __forceinline__ void walk(const DeltaBackArgs &a, WalkLds<E, KP> &lds
         };
         const auto store = [&](int c) {
             const int b = c & 1;
-            if (BACK) tq.template store<LK>(lds.q[b], tid);
-            tk.template store<LK>(lds.k[b], tid);
-            tv.template store<LV>(lds.v[b], tid);
+            const int64_t at = c < chunks ? (int64_t)chunk(c) * C : 0;
+            if (BACK) tq.template place<VEC, LK>(lds.q[b], q + at * a.st.q_t, a.st.q_t, a.dk, tid);
+            tk.template place<VEC, LK>(lds.k[b], k + at * a.st.k_t, a.st.k_t, a.dk, tid);
+            tv.template place<VEC, LV>(lds.v[b], v + at * v_t, v_t, cols, tid);
         };
         load(0);
         decays(0);
@@ -489,7 +490,7 @@ __global__ __launch_bounds__(64 * GradsLds<KP>::WAVES) void k_delta_grads(DeltaB
     Tile<E, CB, SL, PT> ty;
     f32x4 tz[RPER], tg[RPER], ts[SPER], ta[SPER];
     const auto load = [&](int c0) {
-        ty.template load<VEC>(dy + c0, a.st.y_t, c0 < a.dv ? p.rows : 0, min(SL, a.dv - c0), tid);
+        ty.template fetch<VEC>(dy + c0, a.st.y_t, c0 < a.dv ? p.rows : 0, min(SL, a.dv - c0), tid);
 #pragma unroll
         for (int u = 0; u < RPER; ++u) {
             const int e = u * PT + tid, row = e / 8, col = c0 + e % 8 * 4;
@@ -509,10 +510,12 @@ __global__ __launch_bounds__(64 * GradsLds<KP>::WAVES) void k_delta_grads(DeltaB
     load(0);
     {
         Tile<E, CB, KP, PT> t;
-        t.template load<VEC>(static_cast<const E *>(a.k) + row0 * a.st.k_t + g * a.st.k_g, a.st.k_t, p.rows, a.dk, tid);
-        t.template store<LK>(lds.k, tid);
-        t.template load<VEC>(static_cast<const E *>(a.q) + row0 * a.st.q_t + g * a.st.q_g, a.st.q_t, p.rows, a.dk, tid);
-        t.template store<LK>(lds.q, tid);
+        const E *k = static_cast<const E *>(a.k) + row0 * a.st.k_t + g * a.st.k_g;
+        const E *q = static_cast<const E *>(a.q) + row0 * a.st.q_t + g * a.st.q_g;
+        t.template fetch<VEC>(k, a.st.k_t, p.rows, a.dk, tid);
+        t.template place<VEC, LK>(lds.k, k, a.st.k_t, a.dk, tid);
+        t.template fetch<VEC>(q, a.st.q_t, p.rows, a.dk, tid);
+        t.template place<VEC, LK>(lds.q, q, a.st.q_t, a.dk, tid);
         const bool on = lane < p.rows && lane < CB;
         if (w == 0) make_decays(lds.dec, on ? a.la[(a.la_t ? (row0 + lane) * a.la_t : 0) + h] : 0.f, lane);
         if (w == 1 && lane < CB) lds.beta[lane] = on ? a.beta[(row0 + lane) * a.beta_t + h] : 0.f;
@@ -521,7 +524,7 @@ __global__ __launch_bounds__(64 * GradsLds<KP>::WAVES) void k_delta_grads(DeltaB
     f32x4 dyS[NS][TT] = {}, dRS[NS][TT] = {}, UA[NS][TT] = {}, pair[PAIRS] = {};
     float dbeta[RPER] = {}, dot = 0.f;
     for (int c0 = 0; c0 < a.dv; c0 += SL) {
-        ty.template store<LS>(lds.in.dy, tid);
+        ty.template place<VEC, LS>(lds.in.dy, dy + c0, a.st.y_t, min(SL, a.dv - c0), tid);
 #pragma unroll
         for (int u = 0; u < RPER; ++u) {
             const int e = u * PT + tid, row = e / 8, col = e % 8 * 4;
@@ -779,7 +782,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     Tile<E, CB, SL, PT> ty;
     f32x4 tz[RPER], tg[RPER], ts[SPER], ta[SPER];
     const auto load = [&](int c0) {
-        ty.template load<VEC>(dy + c0, a.st.y_t, c0 < a.dv ? p.rows : 0, min(SL, a.dv - c0), tid);
+        ty.template fetch<VEC>(dy + c0, a.st.y_t, c0 < a.dv ? p.rows : 0, min(SL, a.dv - c0), tid);
         const int col = c0 + col8;
 #pragma unroll
         for (int u = 0; u < RPER; ++u) {
@@ -813,7 +816,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     f32x4 dyS[NS][TT] = {}, dRS[NS][TT] = {}, UA[NS][TT] = {}, pair[PAIRS] = {};
     float dbeta[RPER] = {}, dot = 0.f;
     for (int c0 = 0; c0 < a.dv; c0 += SL) {
-        ty.template store<LS>(lds.in.dy, tid);
+        ty.template place<VEC, LS>(lds.in.dy, dy + c0, a.st.y_t, min(SL, a.dv - c0), tid);
 #pragma unroll
         for (int u = 0; u < RPER; ++u) {
             const int r = u * RROWS + row;
@@ -916,10 +919,12 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     }
     {
         Tile<E, CB, KP, PT> tk, tq;
-        tk.template load<VEC>(static_cast<const E *>(a.k) + row0 * a.st.k_t + g * a.st.k_g, a.st.k_t, p.rows, a.dk, tid);
-        tq.template load<VEC>(static_cast<const E *>(a.q) + row0 * a.st.q_t + g * a.st.q_g, a.st.q_t, p.rows, a.dk, tid);
-        tk.template store<LK>(lds.pair.k, tid);
-        tq.template store<LK>(lds.pair.q, tid);
+        const E *k = static_cast<const E *>(a.k) + row0 * a.st.k_t + g * a.st.k_g;
+        const E *q = static_cast<const E *>(a.q) + row0 * a.st.q_t + g * a.st.q_g;
+        tk.template fetch<VEC>(k, a.st.k_t, p.rows, a.dk, tid);
+        tq.template fetch<VEC>(q, a.st.q_t, p.rows, a.dk, tid);
+        tk.template place<VEC, LK>(lds.pair.k, k, a.st.k_t, a.dk, tid);
+        tq.template place<VEC, LK>(lds.pair.q, q, a.st.q_t, a.dk, tid);
     }
     block_sync();
     const Decays<CB> &d = lds.dec;

@@ -294,6 +294,58 @@ struct Tile {
         }
     }
 
+    // The same tile for rows on any alignment, kept as the words that hold it
+    // until `place` writes it: an element of 2 bytes may begin in the middle of
+    // one, so a piece is five words.  The first and the last of a tile may hold
+    // two bytes that are not its own, and no element of any.  (Loads of 2 bytes
+    // into halves of registers, eight to a piece, came out of this compiler
+    // with halves lost where it ran out of registers.)
+    unsigned fifth[PER];
+    template <bool VEC>
+    __device__ __forceinline__ void fetch(const E *base, int64_t ld, int rows, int cols, int tid)
+    {
+        if constexpr (VEC || sizeof(E) != 2) {
+            load<VEC>(base, ld, rows, cols, tid);
+        } else {
+            const uintptr_t at = reinterpret_cast<uintptr_t>(base);
+            const uint32_t skip = (uint32_t)(at & 2);
+            const int64_t bytes = rows > 0 ? (((rows - 1) * ld + cols) * 2 + skip + 3) / 4 * 4 : 0;
+            const rsrc_t r = make_rsrc(reinterpret_cast<const void *>(at - skip), bytes);
+            const int row0 = tid * VE / COLS, col = tid * VE % COLS;
+#pragma unroll
+            for (int u = 0; u < PER; ++u) {
+                const int row = row0 + u * (PT * VE / COLS);
+                const uint32_t first = ((uint32_t)(row * (int)ld + col) * 2u + skip) & ~3u;
+                const uint32_t off = has(u, tid) && row < rows && col < cols ? first : kOOB;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) buf[u][i] = __builtin_amdgcn_raw_buffer_load_b32(r, off + 4 * i, 0, 0);
+                fifth[u] = __builtin_amdgcn_raw_buffer_load_b32(r, off + 16, 0, 0);
+            }
+        }
+    }
+    // What `fetch` with the same base, ld, cols and tid got, to LDS.
+    template <bool VEC, int LD, typename L>
+    __device__ __forceinline__ void place(L *lds, const E *base, int64_t ld, int cols, int tid)
+    {
+        if constexpr (!VEC && sizeof(E) == 2) {
+            const uint32_t skip = (uint32_t)(reinterpret_cast<uintptr_t>(base) >> 1);
+            const int row0 = tid * VE / COLS, col = tid * VE % COLS;
+#pragma unroll
+            for (int u = 0; u < PER; ++u) {
+                const uint32_t odd = (skip + (uint32_t)((row0 + u * (PT * VE / COLS)) * (int)ld + col)) & 1u;
+                unsigned w[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const unsigned next = i < 3 ? buf[u][i + 1 < 4 ? i + 1 : 3] : fifth[u];
+                    w[i] = __builtin_amdgcn_alignbit(next, buf[u][i], odd * 16);
+                    w[i] = col + 2 * i + 1 < cols ? w[i] : col + 2 * i < cols ? w[i] & 0xffffu : 0u;
+                }
+                buf[u] = u32x4{w[0], w[1], w[2], w[3]};
+            }
+        }
+        store<LD>(lds, tid);
+    }
+
     // 0, or NaN where one of the thread's elements is an infinity or a NaN: the
     // sum of 0 times each, in four chains that do not wait for each other.
     __device__ __forceinline__ float zero_times() const

@@ -49,7 +49,8 @@ def check_prefill(name, heads, dtype, lens, per_token=True, carry=None, slots=No
 
 
 HEADS = [(1, 1, 128, 128), (2, 4, 48, 40), (2, 8, 128, 128), (1, 6, 128, 64), (3, 3, 64, 64), (1, 2, 256, 128),
-         (1, 2, 64, 256), (1, 1, 256, 256), (1, 2, 1, 1), (1, 3, 33, 97), (2, 2, 5, 200), (1, 1, 200, 3), (1, 1, 130, 129)]
+         (1, 2, 64, 256), (1, 1, 256, 256), (1, 2, 1, 1), (1, 3, 33, 97), (2, 2, 5, 200), (1, 1, 200, 3), (1, 1, 130, 129),
+         (1, 2, 100, 33), (2, 2, 77, 127), (1, 3, 63, 31)]
 
 
 @pytest.mark.parametrize("dtype", [F32, BF, F16])
