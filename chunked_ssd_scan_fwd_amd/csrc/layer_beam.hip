@@ -1,7 +1,7 @@
 // Beam search over a pool of states: the best continuations of each request's
 // beams, and the states of the beams that go on.
 #include "layer_device.h"
-#include "ssd_internal.h"
+#include "ssd_device.h"
 
 namespace layer {
 
@@ -13,26 +13,51 @@ constexpr int TILE = 64 * PER;          // logits of a wave's tile
 //
 // A key orders candidates: the greater is the better, and no two are equal.
 
+// The value of lane `lane ^ J`: within 16 lanes by DPP, which costs no trip
+// through LDS.
+template <int J>
+__device__ __forceinline__ int across(int x)
+{
+    constexpr int ror8 = ssd::kRowRor + 8, half_mirror = 0x141;
+    if constexpr (J == 1) return __builtin_amdgcn_update_dpp(0, x, 0xb1, 0xf, 0xf, true);
+    if constexpr (J == 2) return __builtin_amdgcn_update_dpp(0, x, 0x4e, 0xf, 0xf, true);
+    if constexpr (J == 4) {   // 7 - i after 3 - i
+        const int y = __builtin_amdgcn_update_dpp(0, x, 0x1b, 0xf, 0xf, true);
+        return __builtin_amdgcn_update_dpp(0, y, half_mirror, 0xf, 0xf, true);
+    }
+    if constexpr (J == 8) return __builtin_amdgcn_update_dpp(0, x, ror8, 0xf, 0xf, true);
+    if constexpr (J == 16) return __builtin_amdgcn_ds_swizzle(x, 0x10 << 10 | 0x1f);
+    return __shfl_xor(x, 32);
+}
+// The value of the lane before (lane 0: its own place is never asked).
+__device__ __forceinline__ int lane_before(int x)
+{
+    return __builtin_amdgcn_update_dpp(0, x, ssd::kWaveShr1, 0xf, 0xf, true);
+}
+
 // A logit and its place: its bits in an order, then the lower place first.
 struct LogitKey {
-    unsigned long long k;
-    __device__ __forceinline__ bool operator>(const LogitKey &o) const { return k > o.k; }
-    __device__ __forceinline__ LogitKey from(int lane) const { return {(unsigned long long)__shfl((long long)k, lane)}; }
-    __device__ __forceinline__ LogitKey across(int mask) const { return {(unsigned long long)__shfl_xor((long long)k, mask)}; }
-    __device__ __forceinline__ LogitKey up() const { return {(unsigned long long)__shfl_up((long long)k, 1)}; }
-    static __device__ __forceinline__ LogitKey least() { return {0}; }
+    unsigned v, p;   // p: ~place
+    __device__ __forceinline__ bool operator>(const LogitKey &o) const { return v > o.v || (v == o.v && p > o.p); }
+    __device__ __forceinline__ LogitKey at(int lane) const   // the same lane for all
+    {
+        return {(unsigned)__builtin_amdgcn_readlane((int)v, lane), (unsigned)__builtin_amdgcn_readlane((int)p, lane)};
+    }
+    __device__ __forceinline__ LogitKey from(int lane) const { return {(unsigned)__shfl((int)v, lane), (unsigned)__shfl((int)p, lane)}; }
+    template <int J>
+    __device__ __forceinline__ LogitKey other() const { return {(unsigned)across<J>((int)v), (unsigned)across<J>((int)p)}; }
+    __device__ __forceinline__ LogitKey before() const { return {(unsigned)lane_before((int)v), (unsigned)lane_before((int)p)}; }
+    static __device__ __forceinline__ LogitKey least() { return {0, 0}; }
 };
-__device__ __forceinline__ LogitKey logit_key(float x, unsigned place)
+__device__ __forceinline__ unsigned ordered(float x)
 {
     const unsigned u = __float_as_uint(x + 0.f);   // -0 is 0
-    return {(unsigned long long)(u & 0x80000000u ? ~u : u | 0x80000000u) << 32 | (unsigned)~place};
+    return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
-__device__ __forceinline__ float logit_of(LogitKey k)
+__device__ __forceinline__ float unordered(unsigned v)
 {
-    const unsigned u = (unsigned)(k.k >> 32);
-    return __uint_as_float(u & 0x80000000u ? u & 0x7fffffffu : ~u);
+    return __uint_as_float(v & 0x80000000u ? v & 0x7fffffffu : ~v);
 }
-__device__ __forceinline__ unsigned place_of(LogitKey k) { return ~(unsigned)k.k; }
 
 // A score in 64 bits, and its place among the request's candidates.
 struct ScoreKey {
@@ -42,28 +67,47 @@ struct ScoreKey {
     {
         return c > o.c || (c == o.c && place < o.place);
     }
-    __device__ __forceinline__ ScoreKey from(int lane) const { return {__shfl(c, lane), (unsigned)__shfl((int)place, lane)}; }
-    __device__ __forceinline__ ScoreKey across(int mask) const
+    template <typename F>
+    __device__ __forceinline__ ScoreKey moved(const F &f) const
     {
-        return {__shfl_xor(c, mask), (unsigned)__shfl_xor((int)place, mask)};
+        const unsigned long long u = __builtin_bit_cast(unsigned long long, c);
+        const unsigned lo = (unsigned)f((int)(unsigned)u), hi = (unsigned)f((int)(unsigned)(u >> 32));
+        return {__builtin_bit_cast(double, (unsigned long long)hi << 32 | lo), (unsigned)f((int)place)};
     }
-    __device__ __forceinline__ ScoreKey up() const { return {__shfl_up(c, 1), (unsigned)__shfl_up((int)place, 1)}; }
+    __device__ __forceinline__ ScoreKey from(int lane) const
+    {
+        return moved([&](int x) { return __shfl(x, lane); });
+    }
+    __device__ __forceinline__ ScoreKey at(int lane) const { return from(lane); }
+    template <int J>
+    __device__ __forceinline__ ScoreKey other() const { return moved([](int x) { return across<J>(x); }); }
+    __device__ __forceinline__ ScoreKey before() const { return moved([](int x) { return lane_before(x); }); }
     static __device__ __forceinline__ ScoreKey least() { return {-__builtin_inf(), 0xffffffffu}; }
 };
 
 // Falling order over the lanes.
-template <typename K>
-__device__ __forceinline__ void keep(K &x, int lane, int j, bool falling)
+template <int J, typename K>
+__device__ __forceinline__ void keep(K &x, int lane, bool falling)
 {
-    const K y = x.across(j);
-    const bool low = (lane & j) == 0;
+    const K y = x.template other<J>();
+    const bool low = (lane & J) == 0;
     if ((y > x) == (low == falling)) x = y;
+}
+template <int J, typename K>
+__device__ __forceinline__ void merge(K &x, int lane, bool falling)   // of two orders that meet
+{
+    keep<J>(x, lane, falling);
+    if constexpr (J > 1) merge<J / 2>(x, lane, falling);
 }
 template <typename K>
 __device__ __forceinline__ K sorted(K x, int lane)
 {
-    for (int k = 2; k <= 64; k *= 2)
-        for (int j = k / 2; j > 0; j /= 2) keep(x, lane, j, (lane & k) == 0);
+    merge<1>(x, lane, (lane & 2) == 0);
+    merge<2>(x, lane, (lane & 4) == 0);
+    merge<4>(x, lane, (lane & 8) == 0);
+    merge<8>(x, lane, (lane & 16) == 0);
+    merge<16>(x, lane, (lane & 32) == 0);
+    merge<32>(x, lane, true);
     return x;
 }
 template <typename K>
@@ -71,26 +115,29 @@ struct Best {
     K list, last;   // lane i: the i-th best so far; the n-th of them
     int n;
     __device__ __forceinline__ explicit Best(int n_) : list(K::least()), last(K::least()), n(n_) {}
+    __device__ __forceinline__ void insert(K y, int lane)   // y: the same for all lanes
+    {
+        const int at = __popcll(__ballot(list > y));
+        const K shifted = list.before();
+        if (lane > at) list = shifted;
+        if (lane == at) list = y;
+    }
     // Candidates x of the lanes in `on`: few one by one, many sorted and merged.
     __device__ __forceinline__ void take(K x, bool on, int lane)
     {
         unsigned long long m = __ballot(on && x > last);
         if (m == 0) return;
-        if (__popcll(m) > 12) {
-            K y = sorted(on ? x : K::least(), lane).from(63 - lane);
-            if (y > list) list = y;
-            for (int j = 32; j > 0; j /= 2) keep(list, lane, j, true);
-        } else {
-            while (m != 0) {
-                const K y = x.from(__ffsll(m) - 1);
-                m &= m - 1;
-                const int at = __popcll(__ballot(list > y));
-                const K shifted = list.up();
-                if (lane == at) list = y;
-                if (lane > at) list = shifted;
-            }
-        }
-        last = list.from(n - 1);
+        if (__popcll(m) > 12) return join(sorted(on ? x : K::least(), lane), lane);
+        for (; m != 0; m &= m - 1) insert(x.at(__ffsll(m) - 1), lane);
+        last = list.at(n - 1);
+    }
+    // A list in falling order.
+    __device__ __forceinline__ void join(K x, int lane)
+    {
+        const K y = x.from(63 - lane);
+        if (y > list) list = y;
+        merge<32>(list, lane, true);
+        last = list.at(n - 1);
     }
 };
 
@@ -102,7 +149,7 @@ struct BeamArgs {
     int R, K, V, n, tiles, pieces;   // tiles of a piece, pieces of a row
     int end;
     float *stat;           // [R K][pieces][2]: the piece's largest logit m and sum of e^{x - m}
-    unsigned long long *top;   // [R K][pieces][n]: its best
+    LogitKey *top;         // [R K][pieces][n]: its best, or keys of 0
     float *out;
     int32_t *tokens, *parents;
 };
@@ -115,13 +162,17 @@ __device__ __forceinline__ bool goes_on(const BeamArgs &a, int row)
 // The largest logit, the sum of exponentials and the n best of a piece of a
 // row, in one pass: a wave to a piece, 2048 logits at a time in registers.
 //
-// A lane offers its best logit, then, where that was among the wave's n best
-// so far, its next one.
+// Memory bounds it, with about 5 vector instructions a logit beside it, one of
+// them an exponential at a quarter of the rate.  So the candidates have to
+// cost next to nothing: a logit is compared once, with the n-th best so far.
+// For the first 2048 that is the n-th largest of the lanes' own largest ones
+// (at least n logits reach it); the few that reach it go into the list one by
+// one.
 template <typename T, bool VEC>
 __global__ __launch_bounds__(BT) void k_beam_rows(BeamArgs a)
 {
     const int lane = threadIdx.x & 63;
-    const int64_t at = (int64_t)blockIdx.x * BW + (threadIdx.x >> 6);
+    const int64_t at = (int64_t)blockIdx.x * BW + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if (at >= (int64_t)a.R * a.K * a.pieces) return;
     const int row = (int)(at / a.pieces), piece = (int)(at % a.pieces);
     if (!goes_on(a, row)) return;
@@ -130,12 +181,12 @@ __global__ __launch_bounds__(BT) void k_beam_rows(BeamArgs a)
     constexpr int VE = VEC ? 16 / (int)sizeof(T) : 1;
     typedef Vec<T, VE> V;
     // place of a lane's value i within a tile
-    const auto place = [&](int i) { return (i / VE * 64 + lane) * VE + i % VE; };
+    const auto place = [](int lane, int i) { return (i / VE * 64 + lane) * VE + i % VE; };
     V next[PER / VE];
     const auto load = [&](int t0) {
 #pragma unroll
         for (int u = 0; u < PER / VE; ++u) {
-            const int p = t0 + place(u * VE);
+            const int p = t0 + place(lane, u * VE);
             // whole vectors: VEC rows hold a whole number of them
             if (p < end)
                 next[u] = *reinterpret_cast<const V *>(x0 + p);
@@ -145,23 +196,23 @@ __global__ __launch_bounds__(BT) void k_beam_rows(BeamArgs a)
         }
     };
     Best<LogitKey> best(a.n);
-    float m = -__builtin_inff(), s = 0.f;
+    float m = -__builtin_inff(), s = 0.f, reach = -__builtin_inff();
     load(first);
     for (int t0 = first; t0 < end; t0 += TILE) {
         float x[PER];
 #pragma unroll
         for (int i = 0; i < PER; ++i) x[i] = to_f(next[i / VE].v[i % VE]);
         if (t0 + TILE < end) load(t0 + TILE);
-        float big = x[0], nan = 0.f;
-        int of = 0;
+        float big = x[0];
 #pragma unroll
-        for (int i = 1; i < PER; ++i) {
-            of = x[i] > big ? i : of;
-            big = fmaxf(big, x[i]);
-        }
+        for (int i = 1; i < PER; ++i) big = fmaxf(big, x[i]);
         float top = big;
-#pragma unroll
-        for (int d = 1; d < 64; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
+        top = fmaxf(top, __int_as_float(across<1>(__float_as_int(top))));
+        top = fmaxf(top, __int_as_float(across<2>(__float_as_int(top))));
+        top = fmaxf(top, __int_as_float(across<4>(__float_as_int(top))));
+        top = fmaxf(top, __int_as_float(across<8>(__float_as_int(top))));
+        top = fmaxf(top, __int_as_float(across<16>(__float_as_int(top))));
+        top = fmaxf(top, __int_as_float(across<32>(__float_as_int(top))));
         const float M = fmaxf(m, top);
         if (M > -__builtin_inff()) {
             float sum[4] = {};
@@ -171,26 +222,29 @@ __global__ __launch_bounds__(BT) void k_beam_rows(BeamArgs a)
             m = M;
         } else {   // nothing but -infinity, or NaN
 #pragma unroll
-            for (int i = 0; i < PER; ++i) nan += x[i] == x[i] ? 0.f : x[i];
-            s += nan;
+            for (int i = 0; i < PER; ++i) s += x[i] == x[i] ? 0.f : x[i];
+            continue;
         }
-        LogitKey key = logit_key(big, t0 + place(of));
-        bool on = true;
-        while (true) {
-            best.take(key, on, lane);
-            // the lanes whose offer is among the best have another one
-            on = on && !(best.last > key);
-            if (__ballot(on) == 0) break;
-            LogitKey lower = LogitKey::least();
+        if (t0 == first) {
+            // (a lane's largest may be -infinity or come from a NaN's place: then fewer are passed over)
+            const LogitKey own = {ordered(big), (unsigned)lane};
+            reach = unordered(sorted(own, lane).at(a.n - 1).v);
+        }
+        if (__ballot(big >= reach) == 0) continue;
 #pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                const LogitKey y = logit_key(x[i], t0 + place(i));
-                if (key > y && y > lower) lower = y;
+        for (int i = 0; i < PER; ++i) {
+            unsigned long long c = __ballot(x[i] >= reach);
+            if (c == 0) continue;
+            const LogitKey key = {ordered(x[i]), ~(unsigned)(t0 + place(lane, i))};
+            for (c &= __ballot(key > best.last); c != 0; c &= c - 1) {
+                const LogitKey y = key.at(__ffsll(c) - 1);
+                if (y > best.last) {
+                    best.insert(y, lane);
+                    best.last = best.list.at(a.n - 1);
+                }
             }
-            key = lower;
-            on = on && key > best.last;
-            if (__ballot(on) == 0) break;
         }
+        if (best.last.v != 0) reach = fmaxf(reach, unordered(best.last.v));
     }
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) s += __shfl_xor(s, d);
@@ -198,7 +252,7 @@ __global__ __launch_bounds__(BT) void k_beam_rows(BeamArgs a)
         a.stat[at * 2] = m;
         a.stat[at * 2 + 1] = s;
     }
-    if (lane < a.n) a.top[at * a.n + lane] = best.list.k;
+    if (lane < a.n) a.top[at * a.n + lane] = best.list;
 }
 
 // The n best of a request, out of its beams' pieces: a block to a request.
@@ -233,10 +287,10 @@ __global__ __launch_bounds__(BT) void k_beam_join(BeamArgs a)
         ScoreKey key = ScoreKey::least();
         bool on = e < all && lse[k] == lse[k];
         if (on) {
-            const LogitKey y = {a.top[((int64_t)r * a.K + k) * per + e % per]};
-            const double c = (double)a.scores[r * a.K + k] + ((double)logit_of(y) - lse[k]);
-            on = y.k != 0 && c > -__builtin_inf();
-            key = {c, (unsigned)k * (unsigned)a.V + place_of(y)};
+            const LogitKey y = a.top[((int64_t)r * a.K + k) * per + e % per];
+            const double c = (double)a.scores[r * a.K + k] + ((double)unordered(y.v) - lse[k]);
+            on = y.v != 0 && c > -__builtin_inf();
+            key = {c, (unsigned)k * (unsigned)a.V + ~y.p};
         }
         best.take(key, on, lane);
     }
@@ -249,10 +303,7 @@ __global__ __launch_bounds__(BT) void k_beam_join(BeamArgs a)
     lists[w][lane] = best.list;
     __syncthreads();
     if (w != 0) return;
-    for (int x = 1; x < BW; ++x) {
-        const ScoreKey key = lists[x][lane];
-        best.take(key, key.place != 0xffffffffu, lane);
-    }
+    for (int x = 1; x < BW; ++x) best.join(lists[x][lane], lane);
     if (lane < a.n) {
         const ScoreKey key = best.list;
         const bool none = key.place == 0xffffffffu;
@@ -339,7 +390,7 @@ static BeamPlan plan_beam(const beam_shape &s, int cus)
     P.tiles = (int)tiles;
     P.pieces = (int)((all + tiles - 1) / tiles);
     P.top = ((size_t)(rows * P.pieces) * 2 * sizeof(float) + 255) / 256 * 256;
-    P.total = P.top + (size_t)(rows * P.pieces * s.n) * sizeof(unsigned long long);
+    P.total = P.top + (size_t)(rows * P.pieces * s.n) * sizeof(LogitKey);
     return P;
 }
 
@@ -388,7 +439,7 @@ extern "C" int beam_select(const beam_shape *shape, int dtype, const void *logit
     a.pieces = P.pieces;
     a.end = end_token;
     a.stat = static_cast<float *>(workspace);
-    a.top = reinterpret_cast<unsigned long long *>(static_cast<char *>(workspace) + P.top);
+    a.top = reinterpret_cast<LogitKey *>(static_cast<char *>(workspace) + P.top);
     a.out = out_scores;
     a.tokens = tokens;
     a.parents = parents;
