@@ -453,13 +453,13 @@ int lin_step(const lin_shape *shape, int dtype, const lin_strides *strides,
  *                 are the caller's risk.
  * Rounding: q, k and v in float32 are rounded nowhere.  bfloat16 calls hold
  * the state, u and all that they come from to float32's accuracy; in y the
- * masked scores and the copy of the state that meets q are rounded to
- * bfloat16 too.
+ * masked scores are rounded to bfloat16 too, and the copies of the state and
+ * of u that meet q and them are sums of two bfloat16 numbers.
  * Infinite and NaN values of a row reach, as in the recurrence, only it and
  * the rows after it in its sequence, and one in v no column but its own; a
  * sequence that holds them is slow from there on, where they reached a state
  * to its end.  Where the recurrence gives an infinity, NaN may stand.
- * (T / 32 + N) H < 2^24 besides, and workspaces for every call. */
+ * (T / 32 + N) H < 2^24 besides. */
 size_t delta_prefill_workspace_size(const lin_shape *shape, int64_t max_seqlen);
 int delta_prefill(const lin_shape *shape, int dtype, const lin_strides *strides,
                   const void *q, const void *k, const void *v,

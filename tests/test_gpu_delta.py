@@ -421,3 +421,214 @@ def test_bwd_out_and_rows_of_no_sequence():
             assert bool((b[:5] == 7).all()) and bool((b[80:] == 7).all())
         else:
             assert torch.equal(a, b)
+
+
+# ---- as they are used
+
+
+def problem(dtype, lens, heads=(2, 4, 64, 64), seed=0, slots=None):
+    G, H, dk, dv = heads
+    T = sum(lens)
+    q, k, v, ld, beta, S = (dev(t) for t in ref.inputs(T, G, H, dk, dv, dtype, True, seed, slots or len(lens)))
+    dy = dev(torch.randn(T, H, dv, generator=torch.Generator().manual_seed(seed + 9)).to(dtype))
+    return q, k, v, ld, beta, ids(offsets(lens)), S, dy
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_training_step_of_a_layer(dtype):
+    """The forward over a batch, the norm of its heads, and both gradients, chained as a training step does."""
+    q, k, v, ld, beta, cu, S, _ = problem(dtype, [70, 58], seed=3)
+    T, H, dv = v.shape
+    pool = torch.zeros_like(S)
+    y = ssd.delta_prefill(q, k, v, ld, beta, cu, pool, carry=ids([0, 0]))
+    w, b = torch.ones(H * dv, device="cuda"), torch.zeros(H * dv, device="cuda")
+    z, stats = ssd.gn_fwd(y.flatten(1), w, b, H, act="none")
+    dz = torch.randn(T, H * dv, device="cuda", generator=torch.Generator("cuda").manual_seed(1)).to(dtype)
+    dy, dw, db, _ = ssd.gn_bwd(y.flatten(1), w, b, H, stats, dz, act="none")
+    got = ssd.delta_bwd(q, k, v, ld, beta, cu, dy.view(T, H, dv))
+    want, err = ref.gradients(q, k, v, ld, beta, cu.tolist(), dy.view(T, H, dv))
+    for n, t in zip(("dq", "dk", "dv", "dlog_decay", "dbeta"), got):
+        kind = dtype if n in ("dq", "dk", "dv") else F32
+        assert beyond(t, want[n], ref.gradient_bound(kind, want[n], err[n])) <= 1, n
+
+
+def test_beam_search_over_recurrent_states():
+    """A prompt, then steps in which beams are selected, their states reordered and stepped, against one state for each
+    history that is stepped by itself."""
+    G, H, dk, dv, K, V, steps = 1, 2, 32, 16, 4, 101, 6
+    g = torch.Generator("cuda").manual_seed(5)
+    r = lambda *s: torch.randn(*s, device="cuda", generator=g)   # noqa: E731
+    emb = [r(V, G, dk), r(V, G, dk), r(V, H, dv)]
+    emb[0], emb[1] = (torch.nn.functional.normalize(x, dim=-1) for x in emb[:2])
+    out = r(H * dv, V)
+    ld, beta = -0.1 * torch.rand(H, device="cuda", generator=g), torch.full((1, H), 0.7, device="cuda")
+    prompt = torch.randint(0, V, (9,), device="cuda", generator=g)
+
+    def run(tokens):   # logits after these tokens, from nothing
+        pool = torch.zeros(1, H, dk, dv, device="cuda")
+        q, k, v = (x[tokens] for x in emb)
+        y = ssd.delta_prefill(q, k, v, ld, beta.expand(len(tokens), H), ids([0, len(tokens)]), pool, carry=ids([0]))
+        return y[-1].flatten() @ out
+
+    pool = torch.zeros(7, H, dk, dv, device="cuda")
+    slots = ids([5, 1, 6, 2])
+    q, k, v = (x[prompt].repeat(K, 1, 1) for x in emb)
+    y = ssd.delta_prefill(q, k, v, ld, beta.expand(9 * K, H), ids([0, 9, 18, 27, 36]), pool, slots=slots, carry=ids([0] * K))
+    logits = (y[8::9].flatten(1) @ out).view(1, K, V)
+    scores = torch.tensor([[0.0, -INF, -INF, -INF]], device="cuda")
+    history = [prompt.tolist()] * K
+    for _ in range(steps):
+        scores, tokens, parents = ssd.beam_select(logits, scores, K)
+        ssd.state_reorder(pool, parents, slots=slots)
+        history = [history[p] + [t] for p, t in zip(parents[0].tolist(), tokens[0].tolist())]
+        q, k, v = (x[tokens[0].long()] for x in emb)
+        y = ssd.delta_step(q, k, v, ld, beta.expand(K, H), pool, slots=slots)
+        logits = (y.flatten(1) @ out).view(1, K, V)
+        for j in range(K):
+            want = run(torch.tensor(history[j], device="cuda"))
+            assert torch.allclose(logits[0, j], want, rtol=1e-3, atol=1e-3)
+    assert len(set(map(tuple, history))) == K
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_same_results_on_any_workspace_and_every_run(dtype):
+    for lens, heads in (([2000, 300], (1, 1, 128, 128)), ([130, 70], (2, 4, 48, 40))):
+        q, k, v, ld, beta, cu, S, dy = problem(dtype, lens, heads, seed=7)
+        args = (q, k, v, ld, beta, cu)
+        T, N, (G, H, dk, dv) = sum(lens), len(lens), heads
+        first = None
+        for fill in (0, 255, 127):
+            n = ssd.layer.delta_prefill_workspace_size(T, N, G, H, dk, dv, N)
+            ws = torch.full((max(n, 16),), fill, dtype=torch.uint8, device="cuda")
+            pool = S.clone()
+            y = ssd.delta_prefill(*args, pool, workspace=ws)
+            wb = torch.full((ssd.layer.delta_bwd_workspace_size(T, N, G, H, dk, dv),), fill, dtype=torch.uint8, device="cuda")
+            all_ = [y, pool, *ssd.delta_bwd(*args, dy, states=S, dstates=S, workspace=wb)]
+            torch.cuda.synchronize()
+            first = first or all_
+            assert all(torch.equal(a, b) for a, b in zip(all_, first))
+    x = torch.randn(3, 4, 5001, device="cuda").to(dtype)
+    sc = -torch.rand(3, 4, device="cuda")
+    n = ssd.layer.beam_select_workspace_size(3, 4, 5001, 8)
+    res = [ssd.beam_select(x, sc, 8, workspace=torch.full((n,), f, dtype=torch.uint8, device="cuda")) for f in (0, 255, 127)]
+    assert all(torch.equal(a, b) for r in res[1:] for a, b in zip(r, res[0]))
+
+
+def test_two_streams_at_once():
+    """Two batches on streams of their own, each with its own workspace, give what each gives alone."""
+    sets = [problem(BF, [2100, 65], (1, 2, 128, 64), seed=s) for s in (1, 2)]
+    alone = []
+    for q, k, v, ld, beta, cu, S, dy in sets:
+        pool = S.clone()
+        alone.append([ssd.delta_prefill(q, k, v, ld, beta, cu, pool), pool,
+                      *ssd.delta_bwd(q, k, v, ld, beta, cu, dy, states=S)])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [None, None]
+    pools = [s[6].clone() for s in sets]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for i, (q, k, v, ld, beta, cu, S, dy) in enumerate(sets):
+            with torch.cuda.stream(streams[i]):
+                pools[i].copy_(S)
+                got[i] = [ssd.delta_prefill(q, k, v, ld, beta, cu, pools[i]), pools[i],
+                          *ssd.delta_bwd(q, k, v, ld, beta, cu, dy, states=S)]
+    torch.cuda.synchronize()
+    for a, b in zip(alone, got):
+        assert all(torch.equal(x, y) for x, y in zip(a, b) if x is not None)
+
+
+def test_captured_calls_replayed():
+    """Every call in two graphs, replayed in turn with eager work between, against the eager results."""
+    def run(x):
+        q, k, v, ld, beta, cu, S, dy, pool, logits, scores, parents = x
+        pool.copy_(S)
+        y = ssd.delta_prefill(q, k, v, ld, beta, cu, pool)
+        z = ssd.delta_step(q[:2], k[:2], v[:2], ld[:2], beta[:2], pool)
+        sel = ssd.beam_select(logits, scores, 2)
+        ssd.state_reorder(pool, parents)
+        return [y, z, pool, *sel, *ssd.delta_bwd(q, k, v, ld, beta, cu, dy, states=S)]
+
+    sets = []
+    for s in (1, 2):
+        p = problem(BF, [1700, 40], (1, 2, 128, 64), seed=s)
+        g = torch.Generator("cuda").manual_seed(s)
+        sets.append([*p, p[6].clone(), torch.randn(1, 2, 3000, device="cuda", generator=g),
+                     torch.zeros(1, 2, device="cuda"), ids([[1, 0]])])
+    eager = [[t.clone() for t in run(x)] for x in sets]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    graphs, outs = [], []
+    with torch.cuda.stream(side):
+        for x in sets:
+            run(x)
+            torch.cuda.synchronize()
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=side):
+                outs.append(run(x))
+            graphs.append(graph)
+    torch.cuda.synchronize()
+    for rep in range(3):
+        for i in (0, 1, 1, 0):
+            with torch.cuda.stream(side):
+                for t in outs[i]:
+                    t.fill_(0) if t.dtype != torch.bfloat16 else t.zero_()
+                graphs[i].replay()
+            torch.cuda.synchronize()
+            run(sets[1 - i])   # eager work between
+            torch.cuda.synchronize()
+            for j, (a, b) in enumerate(zip(outs[i], eager[i])):
+                assert torch.equal(a, b), (rep, i, j)
+
+
+def test_offsets_past_32_bits():
+    """Rows of v whose elements lie past 2^31, states past 2^32 bytes, beams whose states do."""
+    H, dk, dv = 1, 8, 8
+    big = 1 << 23                                        # row stride
+    rows = 300
+    base = torch.zeros(rows * big, dtype=BF, device="cuda")
+    q, k, v, ld, beta, S = ref.inputs(rows, 1, H, dk, dv, BF, True, 4, 1)
+    far = torch.as_strided(base, (rows, H, dv), (big, dv, 1))
+    far.copy_(v)
+    pool = dev(S)
+    y = ssd.delta_prefill(dev(q), dev(k), far, dev(ld), dev(beta), ids([0, rows]), pool)
+    want, S1, ye, Se, ym = ref.rule(q, k, v, ld, beta, [0, rows], S)
+    assert beyond(y, want, ref.y_bound(BF, want, ye, ym)) <= 1 and beyond(pool, S1, Se + 1e-30) <= 1
+    dy = torch.ones(rows, H, dv, dtype=BF, device="cuda")
+    got = ssd.delta_bwd(dev(q), dev(k), far, dev(ld), dev(beta), ids([0, rows]), dy, states=dev(S))
+    near = ssd.delta_bwd(dev(q), dev(k), dev(v), dev(ld), dev(beta), ids([0, rows]), dy, states=dev(S))
+    assert all(torch.equal(a, b) for a, b in zip(got, near))
+    del base, far
+    slots = (1 << 32) // (128 * 128 * 4) + 3             # the last states begin past 2^32 bytes
+    q, k, v, ld, beta, S = ref.inputs(2, 1, 1, 128, 128, BF, True, 4, 2)
+    pool = torch.zeros(slots, 1, 128, 128, device="cuda")
+    pool[-2:] = dev(S)
+    ssd.delta_step(dev(q), dev(k), dev(v), dev(ld), dev(beta), pool, slots=ids([slots - 2, slots - 1]))
+    want, S1, ye, Se, ym = ref.rule(q, k, v, ld, beta, [0, 1, 2], S)
+    assert beyond(pool[-2:], S1, Se + 1e-30) <= 1
+    before = pool[-2:].clone()
+    ssd.state_reorder(pool, ids([[1, 0]]), slots=ids([slots - 2, slots - 1]))
+    assert torch.equal(pool[-2:], before.flip(0)) and not bool(pool[:-2].any())
+
+
+def test_another_streams_and_devices_tensors_are_refused_or_served():
+    q, k, v, ld, beta, cu, S, dy = problem(F32, [20])
+    with pytest.raises(ValueError):
+        ssd.delta_prefill(q, k.cpu(), v, ld, beta, cu, S)
+    with pytest.raises(ValueError):
+        ssd.delta_prefill(q, k, v, ld, beta.cpu(), cu, S)
+    with pytest.raises(TypeError):
+        ssd.delta_prefill(q, k, v, ld, beta.double(), cu, S)
+    with pytest.raises(ValueError):
+        ssd.delta_bwd(q, k, v, ld, beta, cu, dy[:-1])
+    with pytest.raises(ValueError):
+        ssd.delta_bwd(q, k, v, ld, beta, cu, dy, states=S[:, :, :, :-1])
+    with pytest.raises(ValueError):
+        ssd.beam_select(torch.zeros(1, 2, 9, device="cuda"), torch.zeros(1, 2), 2)
+    with pytest.raises(ValueError):
+        ssd.beam_select(torch.zeros(1, 2, 9, device="cuda"), torch.zeros(1, 2, device="cuda"), 2,
+                        ended=torch.zeros(1, 2, dtype=torch.uint8, device="cuda"), end_token=9)
+    with pytest.raises(ValueError):
+        ssd.state_reorder(S, ids([[0, 1, 2]]).flatten())
+    with pytest.raises(ssd.SsdError):
+        ssd.state_reorder(S, ids([[0, 1, 2]]))   # more beams than slots
