@@ -39,6 +39,17 @@ __device__ __forceinline__ f32x4 times(f32x4 f, f32x4 b, f32x4 x)
     return x;
 }
 
+// Row N of 16 lanes in place of all four.
+template <int N>
+__device__ __forceinline__ float row_of_lanes(float x)
+{
+    // rows 0, 0, 2, 2 and 1, 1, 3, 3; then one half of them twice
+    const unsigned u = __float_as_uint(x);
+    const auto pairs = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    const auto halves = __builtin_amdgcn_permlane32_swap(pairs[N & 1], pairs[N & 1], false, false);
+    return __uint_as_float(halves[N >> 1]);
+}
+
 template <typename E, int KP, int VT>
 struct DeltaPerCu {
     static constexpr int n = VT == 64 && KP <= 128 && std::is_same<E, bf16>::value ? 2 : 1;
@@ -95,6 +106,27 @@ __attribute__((amdgpu_waves_per_eu(DeltaPerCu<E, KP, VT>::per_simd, DeltaPerCu<E
         const int f = PC::at(row, j / 2) * parts + u;
         *reinterpret_cast<L4 *>(to + (f * PC::UNITS * 64 + lane) * 16 + (j & 1) * (PC::UNITS == 2 ? 1024 : 8)) = x;
     };
+
+    // A tile of P, 16 x 16, on or below the diagonal.  Formed as K Q^T, so that a
+    // lane holds 4 scores of one query.
+    const auto scores = [&](const Decays<C> &d, const L *qs, const L *ks, int it, int jt, int lane) {
+        const int l16 = lane & 15, g4 = (lane >> 4) * 4;
+        f32x4 x = {};
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+            x = mma(frag8(ks + (16 * jt + l16) * LK + 32 * s + 2 * g4), frag8(qs + (16 * it + l16) * LK + 32 * s + 2 * g4),
+                    x);
+        const int i = 16 * it + l16, j = 16 * jt + g4;
+        const float bh = d.hi[i], bl = d.lo[i];
+        const f32x4 jh = *reinterpret_cast<const f32x4 *>(d.hi + j), jl = *reinterpret_cast<const f32x4 *>(d.lo + j);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            x[e] *= __expf((bh - jh[e]) + (bl - jl[e]));
+            if (j + e > i) x[e] = 0.f;
+        }
+        return x;
+    };
+    const auto put_scores = [&](int it, int jt, f32x4 x) { put(lds.p, 1, it, jt, 0, __builtin_convertvector(x, L4)); };
 
     if (wave >= WAVES) {
         // ---- fetches, and T of the next chunk
@@ -174,7 +206,7 @@ __attribute__((amdgpu_waves_per_eu(DeltaPerCu<E, KP, VT>::per_simd, DeltaPerCu<E
                         return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(m[e]), ctrl, 0xf, 0xf, true));
                     };
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) y[e] = __shfl(y[e], 16 * n + l16);
+                    for (int e = 0; e < 4; ++e) y[e] = row_of_lanes<n>(y[e]);
                     f32x4 x = X;
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
@@ -276,29 +308,44 @@ __attribute__((amdgpu_waves_per_eu(DeltaPerCu<E, KP, VT>::per_simd, DeltaPerCu<E
                 row_values(c + 2, next);
                 block_sync();
             }
-        } else if (mover) {
+        } else if (mover) {   // the decays and P are its own too: wave 0 has P's tile (1, 0), wave 1 those on the diagonal
+            f32x4 P0 = {}, P1 = {};
+            const auto make_scores = [&](int c) {
+                if (!OUT) return;
+                const int lane = anew(threadIdx.x & 63), b = c & 1;
+                P0 = scores(lds.dec[c % 3], lds.q[b], lds.k[b], 1, w, lane);
+                if (w == 1) P1 = scores(lds.dec[c % 3], lds.q[b], lds.k[b], 0, 0, lane);
+            };
+            const auto write_scores = [&]() {
+                if (!OUT) return;
+                put_scores(1, w, P0);
+                if (w == 1) put_scores(0, 0, P1);
+            };
+            first_values();
             first_tiles();
             block_sync();
-            block_sync();
-            for (int c = 0; c < chunks; ++c) {
-                store(c + 1);
-                load(c + 2);
-                block_sync();
-                block_sync();
-            }
-        } else {
-            first_values();
-            block_sync();
-            diagonal(0);
+            make_scores(0);
             row_values(1, next);
             block_sync();
             for (int c = 0; c < chunks; ++c) {
                 next = row_value(c + 2);
+                write_scores();
+                store(c + 1);
+                load(c + 2);
+                block_sync();
+                make_scores(c + 1);
+                row_values(c + 2, next);
+                block_sync();
+            }
+        } else {
+            block_sync();
+            diagonal(0);
+            block_sync();
+            for (int c = 0; c < chunks; ++c) {
                 solve(c);
                 write();
                 block_sync();
                 diagonal(c + 1);
-                row_values(c + 2, next);
                 block_sync();
             }
         }
@@ -344,29 +391,14 @@ __attribute__((amdgpu_waves_per_eu(DeltaPerCu<E, KP, VT>::per_simd, DeltaPerCu<E
         const int b = c & 1, rows = min(C, p.rows - c * C);
         const Decays<C> &d = lds.dec[c % 3];
         const L *qs = lds.q[b], *ks = lds.k[b], *vs = lds.v[b];
-        // P's 16 x 16 tiles on and below the diagonal, dealt to the waves.
-        // Formed as K Q^T, so that a lane holds 4 scores of one query.
-        constexpr int TILES = OUT ? TT * (TT + 1) / 2 : 0;
+        // P, dealt to the waves (where no other has the time)
+        constexpr int TILES = OUT && MOVERS == 4 ? TT * (TT + 1) / 2 : 0;
 #pragma unroll
-        for (int u0 = 0; u0 < TILES; u0 += WAVES) {
-            const int u = u0 + wave;
-            if (u >= TILES) continue;
-            const int it = TT == 2 ? (u > 0) : (u > 0) + (u > 2) + (u > 5), jt = u - it * (it + 1) / 2;
-            f32x4 x = {};
-#pragma unroll
-            for (int s = 0; s < KS; ++s)
-                x = mma(frag8(ks + (16 * jt + l16) * LK + 32 * s + 2 * g4),
-                        frag8(qs + (16 * it + l16) * LK + 32 * s + 2 * g4), x);
-            const int i = 16 * it + l16, j = 16 * jt + g4;
-            const float bh = d.hi[i], bl = d.lo[i];
-            const f32x4 jh = *reinterpret_cast<const f32x4 *>(d.hi + j), jl = *reinterpret_cast<const f32x4 *>(d.lo + j);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                x[e] *= __expf((bh - jh[e]) + (bl - jl[e]));
-                if (j + e > i) x[e] = 0.f;
+        for (int u0 = 0; u0 < TILES; u0 += WAVES)
+            if (u0 + wave < TILES) {
+                const int u = u0 + wave, it = (u > 0) + (u > 2) + (u > 5), jt = u - it * (it + 1) / 2;
+                put_scores(it, jt, scores(d, qs, ks, it, jt, lane));
             }
-            put(lds.p, 1, it, jt, 0, __builtin_convertvector(x, L4));
-        }
         // X = K S (rows: the chunk's, columns: of v), Y^T = S^T Q^T
         f32x4 X[NT][TT], Y[NT][TT];
 #pragma unroll
