@@ -7,6 +7,9 @@
 // two dependent loads (slot, then state).  u needs all of a column before any
 // of it can be written, so a block keeps its columns in registers, and y is
 // taken from the same pass over them: S'^T q = a S^T q + (k . q) u.
+//
+// 256 rows of 16 heads of 128 x 128 (537 MB): 110 us, 4.9 TB/s; one row of 8
+// heads 5.1 us.
 #include "layer_device.h"
 #include "ssd_internal.h"
 
@@ -144,6 +147,8 @@ static void launch_rows(DeltaStepArgs &a, hipStream_t st)
         k_delta_step<T, VEC, CL, 256 / R, STREAM><<<grid, dim3(DT), 0, st>>>(a);
 }
 
+// Columns of a block as for lin_step: 64 where that makes a block for every
+// CU, else 32; states of more than 128 MiB in a call go past the caches.
 template <typename T>
 static void launch_delta_step(DeltaStepArgs &a, int cus, hipStream_t st)
 {
