@@ -385,6 +385,9 @@ struct BeamPlan {
     size_t top = 0, total = 0;
 };
 
+// Tiles of a wave: as many as leave 16 waves for every CU, 8 at most.  (256 rows
+// of 131072 logits: 35 us, one each 46; 4 of 32001: one each 18 us, 8 each 34,
+// for a wave's tiles come one after the other.)
 static BeamPlan plan_beam(const beam_shape &s, int cus)
 {
     BeamPlan P;

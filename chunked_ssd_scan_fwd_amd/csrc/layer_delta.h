@@ -32,36 +32,29 @@ struct DeltaArgs : PrefillArgs {
 // every chunk without a count of them; some numbers have no chunk.
 __device__ __forceinline__ int chunk_number(int n, int begin, int at, int C) { return begin / C + n + at / C; }
 
-// ---- T and P as operands: the 16 x 32 pieces on and below the diagonal, in
-// the order in which lanes read them.
+// ---- T and P of a chunk of 32 rows as operands: two pieces of 16 x 32, in the
+// order in which lanes read them.
 //
-// Piece (t, s) holds rows 16 t .. and columns 32 s ..: lane l has row l % 16
-// and, with g = l / 16, columns 4 g .. 4 g + 3 and 16 + 4 g .. (the order in
-// which accumulators of 16 rows each give a summed axis of 32).
-template <typename L, int C>
+// Piece t holds rows 16 t ..: lane l has row l % 16 and, with g = l / 16,
+// columns 4 g .. 4 g + 3 and 16 + 4 g .. (the order in which accumulators of 16
+// rows each give a summed axis of 32).
+template <typename L>
 struct Pieces {
-    static constexpr int TT = C / 16, N = C == 64 ? 6 : 2;
     static constexpr int PARTS = sizeof(L) == 2 ? 3 : 1;
     static constexpr int UNITS = sizeof(L) == 2 ? 1 : 2;   // 16-byte units of a lane's 8 values
-    static constexpr int BYTES = N * PARTS * UNITS * 1024;
-    static __device__ __forceinline__ constexpr int at(int t, int s) { return t < 2 ? t : 2 * t - 2 + s; }
-    // of T^T, whose pieces lie on and above the diagonal
-    static __device__ __forceinline__ constexpr int above(int t, int s)
-    {
-        return C == 32 ? t : t < 2 ? 2 * t + s : 2 + t;
-    }
+    static constexpr int BYTES = 2 * PARTS * UNITS * 1024;
 };
-// The lane's 8 values of part u of piece f in an image at `p`.
-template <typename L, int C>
-__device__ __forceinline__ Frag<L> piece(const char *p, int f, int u, int lane)
+// The lane's 8 values of part u of piece t in an image at `p`.
+template <typename L>
+__device__ __forceinline__ Frag<L> piece(const char *p, int t, int u, int lane)
 {
-    typedef Pieces<L, C> P;
+    typedef Pieces<L> P;
     Frag<L> r;
     char *to = reinterpret_cast<char *>(&r);
 #pragma unroll
     for (int i = 0; i < P::UNITS; ++i)
         *reinterpret_cast<u32x4 *>(to + 16 * i) =
-            *reinterpret_cast<const u32x4 *>(p + (((f * P::PARTS + u) * P::UNITS + i) * 64 + lane) * 16);
+            *reinterpret_cast<const u32x4 *>(p + (((t * P::PARTS + u) * P::UNITS + i) * 64 + lane) * 16);
     return r;
 }
 

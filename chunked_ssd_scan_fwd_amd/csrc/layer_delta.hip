@@ -29,17 +29,19 @@ namespace layer {
 // of 2^-24 and less left out).  In y, the scores P enter as one, S and U as
 // two: with S as one too y was 0.0024 from 64 bits, 0.0025 where little of a
 // row's y is its own chunk's, and its own rounding makes 0.0017.
-template <typename E, int KP, int VT, int C>
+constexpr int C = 32;   // rows of a chunk
+
+template <typename E, int KP, int VT>
 struct DeltaLds {
     typedef typename std::conditional<std::is_same<E, bf16>::value, bf16, float>::type L;
-    typedef Pieces<L, C> PC;
+    typedef Pieces<L> PC;
     static constexpr int PAD = sizeof(L) == 2 ? 16 : 4;
     static constexpr int LK = KP + PAD, LV = VT + PAD;
     static constexpr int PBYTES = PC::BYTES / PC::PARTS;
     L q[2][C * LK], k[2][C * LK], v[2][C * LV];
     alignas(16) char p[PBYTES], t[PC::BYTES];
-    // the next chunk's diagonal blocks of T, and A's tiles below, by lanes
-    alignas(16) f32x4 diag[PC::TT][64], low[PC::TT * (PC::TT - 1) / 2][64];
+    // the next chunk's diagonal blocks of T, and A's tile below, by lanes
+    alignas(16) f32x4 diag[2][64], low[64];
     Decays<C> dec[3];
     alignas(16) float beta[3][C];
 };
@@ -66,10 +68,8 @@ __device__ __forceinline__ float row_of_lanes(float x)
 template <typename E, int KP, int VT>
 struct DeltaPerCu {
     static constexpr int n = VT == 64 && KP <= 128 && std::is_same<E, bf16>::value ? 2 : 1;
-    static constexpr int C = n == 2 || sizeof(E) == 4 || KP > 128 || !std::is_same<E, bf16>::value ? 32 : 64;
-    // waves that hold S, and four more: with 64-row chunks all of them fetch and
-    // have rows of T, with 32-row ones two do either
-    static constexpr int waves = VT / 16, movers = C / 16, solvers = C / 16;
+    // waves that hold S, and four more: two that fetch and two with 16 rows of T each
+    static constexpr int waves = VT / 16, movers = 2;
     static constexpr int threads = 64 * (waves + 4), per_simd = n * threads / 256;
 };
 
@@ -77,15 +77,15 @@ struct DeltaPerCu {
 // the map from the state that enters it to the one that leaves it, S' = M S + B:
 // B as the state that the segment makes from zero, and further blocks for the
 // columns of M, which is what it makes of the identity with v = 0.
-template <typename E, int KP, int VT, int C, bool OUT, bool VEC>
+template <typename E, int KP, int VT, bool OUT, bool VEC>
 __global__ __launch_bounds__((DeltaPerCu<E, KP, VT>::threads))
 __attribute__((amdgpu_waves_per_eu(DeltaPerCu<E, KP, VT>::per_simd, DeltaPerCu<E, KP, VT>::per_simd))) void k_delta_chunks(DeltaArgs a)
 {
-    typedef DeltaLds<E, KP, VT, C> Lds;
+    typedef DeltaLds<E, KP, VT> Lds;
     typedef typename Lds::L L;
-    typedef Pieces<L, C> PC;
+    typedef Pieces<L> PC;
     constexpr int LK = Lds::LK, LV = Lds::LV;
-    constexpr int WAVES = DeltaPerCu<E, KP, VT>::waves, NT = VT / 16 / WAVES, MT = KP / 16, TT = C / 16, KS = KP / 32, TS = C / 32;
+    constexpr int WAVES = DeltaPerCu<E, KP, VT>::waves, MT = KP / 16, KS = KP / 32;
     constexpr int PARTS = PC::PARTS, YU = PARTS == 3 ? 2 : 1;
     constexpr int MOVERS = DeltaPerCu<E, KP, VT>::movers, PT = 64 * MOVERS;   // threads that fetch
     __shared__ __align__(16) Lds lds;
@@ -113,11 +113,11 @@ __attribute__((amdgpu_waves_per_eu(DeltaPerCu<E, KP, VT>::per_simd, DeltaPerCu<E
     const E *v = static_cast<const E *>(a.v) + p.begin * a.st.v_t + h * a.st.v_h + (map ? 0 : c0);
     const float *la = a.la + (a.la_t ? p.begin * a.la_t : 0) + h;
 
-    // half j % 2 of a lane's 8 values of part u of piece (row block, j / 2)
+    // half j of a lane's 8 values of part u of piece `row`
     typedef typename std::conditional<sizeof(L) == 2, bf16x4, f32x4>::type L4;
     const auto put = [&](char *to, int parts, int row, int j, int u, L4 x) {
-        const int f = PC::at(row, j / 2) * parts + u;
-        *reinterpret_cast<L4 *>(to + (f * PC::UNITS * 64 + lane) * 16 + (j & 1) * (PC::UNITS == 2 ? 1024 : 8)) = x;
+        const int f = row * parts + u;
+        *reinterpret_cast<L4 *>(to + (f * PC::UNITS * 64 + lane) * 16 + j * (PC::UNITS == 2 ? 1024 : 8)) = x;
     };
 
     // A tile of P, 16 x 16, on or below the diagonal.  Formed as K Q^T, so that a
@@ -143,9 +143,8 @@ __attribute__((amdgpu_waves_per_eu(DeltaPerCu<E, KP, VT>::per_simd, DeltaPerCu<E
 
     if (wave >= WAVES) {
         // ---- fetches, and T of the next chunk
-        constexpr bool BOTH = MOVERS == 4;   // every wave does both
-        const int w = BOTH ? wave - WAVES : (wave - WAVES) & 1;
-        const bool mover = BOTH || wave < WAVES + MOVERS;
+        const int w = (wave - WAVES) & 1;
+        const bool mover = wave < WAVES + MOVERS;
         Tile<E, C, KP, PT> tq, tk;
         Tile<E, C, VT, PT> tv;
         const auto load = [&](int c) {
@@ -233,95 +232,42 @@ __attribute__((amdgpu_waves_per_eu(DeltaPerCu<E, KP, VT>::per_simd, DeltaPerCu<E
             rows4(ssd::IntC<2>{});
             rows4(ssd::IntC<3>{});
             lds.diag[w][lane] = X;
-#pragma unroll
-            for (int j = 0; j < TT - 1; ++j) {
-                if (j >= w) continue;
+            if (w == 1) {
                 f32x4 x = {};
 #pragma unroll
-                for (int s = 0; s < KS; ++s) x = mma(fk[s], frag8(ks + (16 * j + l16) * LK + 32 * s + 2 * g4), x);
-                scaled(x, j);
-                lds.low[w * (w - 1) / 2 + j][lane] = x;
+                for (int s = 0; s < KS; ++s) x = mma(fk[s], frag8(ks + l16 * LK + 32 * s + 2 * g4), x);
+                scaled(x, 0);
+                lds.low[lane] = x;
             }
         };
-        // Then, from T (I + A) = I, T_ij = -(sum_m T_im A_mj) T_jj, j < m <= i.
-        // Held transposed, so that a sum comes out of the accumulators as the
-        // next product's operand, and T's rows as its pieces hold them; a block
-        // goes into all the sums that take it at once.
-        f32x4 T[TT];
-        const auto solve = [&](int c) {
-            const int lane = anew(threadIdx.x & 63), l16 = lane & 15, g4 = (lane >> 4) * 4;
-            const float *betas = lds.beta[c % 3];
-            f32x4 sum[TT] = {}, own;
-            {
-                const float *x = reinterpret_cast<const float *>(lds.diag[w]) + 64 * (l16 >> 2) + (l16 & 3);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) own[e] = x[4 * (g4 + e)];
-            }
-#pragma unroll
-            for (int m = TT - 1; m >= 0; --m) {
-                if (m > w) continue;
-                T[m] = own;
-                if (m < w) T[m] = times(lds.diag[m][lane], -sum[m], f32x4{});
-                f32x4 f[TT];
-#pragma unroll
-                for (int j = 0; j < m; ++j) f[j] = lds.low[m * (m - 1) / 2 + j][lane];
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-#pragma unroll
-                    for (int j = 0; j < m; ++j)
-                        sum[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(f[j][e], T[m][e], sum[j], 0, 0, 0);
-            }
-            // its columns times beta
-#pragma unroll
-            for (int j = 0; j < TT; ++j) T[j] *= *reinterpret_cast<const f32x4 *>(betas + 16 * j + g4);
-        };
+        // Then T_10 = -T_11 A_10 T_00.  Held transposed, so that T_11 A_10 comes
+        // out of the accumulators as the next product's operand, and T's rows as
+        // its pieces hold them.
         const auto put_t = [&](int row, int j, f32x4 x) {
             L4 parts[PARTS];
             split4(parts, x);
 #pragma unroll
             for (int u = 0; u < PARTS; ++u) put(lds.t, PARTS, row, j, u, parts[u]);
         };
-        const auto write = [&]() {
+        const auto solve = [&](int c) {
+            const int lane = anew(threadIdx.x & 63), l16 = lane & 15, g4 = (lane >> 4) * 4;
+            const float *betas = lds.beta[c % 3];
+            const float *x = reinterpret_cast<const float *>(lds.diag[w]) + 64 * (l16 >> 2) + (l16 & 3);
+            f32x4 T;
 #pragma unroll
-            for (int j = 0; j < TT; ++j)
-                if (j <= w) put_t(w, j, T[j]);
+            for (int e = 0; e < 4; ++e) T[e] = x[4 * (g4 + e)];
+            if (w == 1) {
+                const f32x4 sum = times(lds.low[lane], T, f32x4{});
+                put_t(1, 0, times(lds.diag[0][lane], -sum, f32x4{}) * *reinterpret_cast<const f32x4 *>(betas + g4));
+            }
+            put_t(w, w, T * *reinterpret_cast<const f32x4 *>(betas + 16 * w + g4));
         };
         // what a piece on the diagonal holds above it stays 0
-        if (w % 2 == 0 && (BOTH || !mover)) {
-            put(lds.p, 1, w, w + 1, 0, L4{});
-            put_t(w, w + 1, f32x4{});
+        if (w == 0 && !mover) {
+            put(lds.p, 1, 0, 1, 0, L4{});
+            put_t(0, 1, f32x4{});
         }
-        // Without conditions: a chunk past the last one loads nothing and
-        // leaves zeros in a buffer that is not read.
-        float next = 0.f;
-        const auto first_tiles = [&]() {
-            load(0);
-            store(0);
-            load(1);
-        };
-        const auto first_values = [&]() {
-            row_values(0, row_value(0));
-            next = row_value(1);
-        };
-        if (BOTH) {
-            first_values();
-            first_tiles();
-            block_sync();
-            diagonal(0);
-            row_values(1, next);
-            block_sync();
-            for (int c = 0; c < chunks; ++c) {
-                next = row_value(c + 2);
-                store(c + 1);
-                solve(c);
-                write();
-                block_sync();
-                load(c + 2);
-                diagonal(c + 1);
-                row_values(c + 2, next);
-                block_sync();
-            }
-        } else if (mover) {   // the decays and P are its own too: wave 0 has P's tile (1, 0), wave 1 those on the diagonal
+        if (mover) {   // the decays and P are its own too: wave 0 has P's tile (1, 0), wave 1 those on the diagonal
             f32x4 P0 = {}, P1 = {};
             const auto make_scores = [&](int c) {
                 if (!OUT) return;
@@ -334,8 +280,13 @@ __attribute__((amdgpu_waves_per_eu(DeltaPerCu<E, KP, VT>::per_simd, DeltaPerCu<E
                 put_scores(1, w, P0);
                 if (w == 1) put_scores(0, 0, P1);
             };
-            first_values();
-            first_tiles();
+            // Without conditions: a chunk past the last one loads nothing and
+            // leaves zeros in a buffer that is not read.
+            row_values(0, row_value(0));
+            float next = row_value(1);
+            load(0);
+            store(0);
+            load(1);
             block_sync();
             make_scores(0);
             row_values(1, next);
@@ -356,7 +307,6 @@ __attribute__((amdgpu_waves_per_eu(DeltaPerCu<E, KP, VT>::per_simd, DeltaPerCu<E
             block_sync();
             for (int c = 0; c < chunks; ++c) {
                 solve(c);
-                write();
                 block_sync();
                 diagonal(c + 1);
                 block_sync();
@@ -370,18 +320,15 @@ __attribute__((amdgpu_waves_per_eu(DeltaPerCu<E, KP, VT>::per_simd, DeltaPerCu<E
     const int64_t state = (int64_t)a.dk * width;
     float *pool = p.slot < 0 ? nullptr : a.states + ((int64_t)p.slot * a.H + h) * state;
     float *ends = (map ? a.maps : a.ends) + ((int64_t)id * a.H + h) * state;
-    const int w0 = 16 * NT * wave;   // this wave's columns of the tile
+    const int w0 = 16 * wave;   // this wave's columns of the tile
 
-    // S: value i of accumulator m, n is row 32 (m / 2) + 2 g4 + 4 (m % 2) + i,
-    // column w0 + l16 or, of two column tiles, w0 + 8 (l16 / 4) + 4 n + l16 % 4:
-    // then a lane's values of Y are 8 columns that follow one another.
-    // The registers hold S / scale: the chunks' decays gather in `scale`,
+    // S: value i of accumulator m is row 32 (m / 2) + 2 g4 + 4 (m % 2) + i, column
+    // w0 + l16.  The registers hold S / scale: the chunks' decays gather in `scale`,
     // until it leaves 2^-16 .. 2^16.
-    f32x4 S[MT][NT];
+    f32x4 S[MT];
     float scale = 1.f;
-    const auto column = [&](int n, int l16) { return w0 + (NT == 2 ? 8 * (l16 >> 2) + 4 * n + (l16 & 3) : l16); };
-    const auto state_at = [&](int m, int n, int i, int lane) {
-        const int col = column(n, lane & 15);
+    const auto state_at = [&](int m, int i, int lane) {
+        const int col = w0 + (lane & 15);
         const uint32_t base = col < cols ? (uint32_t)((lane >> 4) * 8 * width + c0 + col) * 4u : kOOB;
         return base + (uint32_t)(32 * (m / 2) + 4 * (m % 2) + i) * (uint32_t)width * 4u;
     };
@@ -391,12 +338,10 @@ __attribute__((amdgpu_waves_per_eu(DeltaPerCu<E, KP, VT>::per_simd, DeltaPerCu<E
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    S[m][n][i] = OUT ? ssd::gload1(r, state_at(m, n, i, lane)) : 0.f;
-                    if (map && 32 * (m / 2) + 2 * g4 + 4 * (m % 2) + i == c0 + column(n, l16)) S[m][n][i] = 1.f;
-                }
+            for (int i = 0; i < 4; ++i) {
+                S[m][i] = OUT ? ssd::gload1(r, state_at(m, i, lane)) : 0.f;
+                if (map && 32 * (m / 2) + 2 * g4 + 4 * (m % 2) + i == c0 + w0 + l16) S[m][i] = 1.f;
+            }
     }
     block_sync();
     block_sync();
@@ -404,146 +349,102 @@ __attribute__((amdgpu_waves_per_eu(DeltaPerCu<E, KP, VT>::per_simd, DeltaPerCu<E
         const int b = c & 1, rows = min(C, p.rows - c * C);
         const Decays<C> &d = lds.dec[c % 3];
         const L *qs = lds.q[b], *ks = lds.k[b], *vs = lds.v[b];
-        // P, dealt to the waves (where no other has the time)
-        constexpr int TILES = OUT && MOVERS == 4 ? TT * (TT + 1) / 2 : 0;
-#pragma unroll
-        for (int u0 = 0; u0 < TILES; u0 += WAVES)
-            if (u0 + wave < TILES) {
-                const int u = u0 + wave, it = (u > 0) + (u > 2) + (u > 5), jt = u - it * (it + 1) / 2;
-                put_scores(it, jt, scores(d, qs, ks, it, jt, lane));
-            }
         // X = K S (rows: the chunk's, columns: of v), Y^T = S^T Q^T
-        f32x4 X[NT][TT], Y[NT][TT];
+        f32x4 X[2], Y[2];
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int t = 0; t < TT; ++t) X[n][t] = Y[n][t] = f32x4{};
+        for (int t = 0; t < 2; ++t) X[t] = Y[t] = f32x4{};
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
-            Frag<L> fs[NT][PARTS];
+            Frag<L> fs[PARTS];
+            split(fs, S[2 * s], S[2 * s + 1]);
+            Frag<L> f[2];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) split(fs[n], S[2 * s][n], S[2 * s + 1][n]);
-            Frag<L> f[TT];
-#pragma unroll
-            for (int t = 0; t < TT; ++t) f[t] = frag8(ks + (16 * t + l16) * LK + 32 * s + 2 * g4);
+            for (int t = 0; t < 2; ++t) f[t] = frag8(ks + (16 * t + l16) * LK + 32 * s + 2 * g4);
 #pragma unroll
             for (int u = PARTS - 1; u >= 0; --u)
 #pragma unroll
-                for (int t = 0; t < TT; ++t)
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) X[n][t] = mma(f[t], fs[n][u], X[n][t]);
+                for (int t = 0; t < 2; ++t) X[t] = mma(f[t], fs[u], X[t]);
             if (!OUT) continue;
 #pragma unroll
-            for (int t = 0; t < TT; ++t) f[t] = frag8(qs + (16 * t + l16) * LK + 32 * s + 2 * g4);
+            for (int t = 0; t < 2; ++t) f[t] = frag8(qs + (16 * t + l16) * LK + 32 * s + 2 * g4);
 #pragma unroll
             for (int u = YU - 1; u >= 0; --u)
 #pragma unroll
-                for (int t = 0; t < TT; ++t)
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) Y[n][t] = mma(fs[n][u], f[t], Y[n][t]);
+                for (int t = 0; t < 2; ++t) Y[t] = mma(fs[u], f[t], Y[t]);
         }
         block_sync();   // P and T are there
         // U = (T diag(beta)) (V - diag(e^b) K S)
-        f32x4 U[NT][TT];
+        f32x4 U[2];
         {
-            Frag<L> fg[TS][NT][PARTS];
+            Frag<L> fg[PARTS];
+            const f32x4 ea = *reinterpret_cast<const f32x4 *>(d.in + g4) * scale;
+            const f32x4 eb = *reinterpret_cast<const f32x4 *>(d.in + 16 + g4) * scale;
+            const Frag<L> fv = frag_col<LV, false>(vs, w0, lane);
+            f32x4 ga, gb;
 #pragma unroll
-            for (int s = 0; s < TS; ++s) {
-                const f32x4 ea = *reinterpret_cast<const f32x4 *>(d.in + 32 * s + g4) * scale;
-                const f32x4 eb = *reinterpret_cast<const f32x4 *>(d.in + 32 * s + 16 + g4) * scale;
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const Frag<L> fv = frag_col<LV, NT == 2>(vs + 32 * s * LV, w0 + 4 * n, lane);
-                    f32x4 ga, gb;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        ga[i] = (float)fv.x[i] - ea[i] * X[n][2 * s][i];
-                        gb[i] = (float)fv.x[4 + i] - eb[i] * X[n][2 * s + 1][i];
-                    }
-                    split(fg[s][n], ga, gb);
-                }
+            for (int i = 0; i < 4; ++i) {
+                ga[i] = (float)fv.x[i] - ea[i] * X[0][i];
+                gb[i] = (float)fv.x[4 + i] - eb[i] * X[1][i];
             }
+            split(fg, ga, gb);
+            U[0] = U[1] = f32x4{};
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+            for (int u = PARTS - 1; u >= 0; --u) {
+                Frag<L> ft[2];
 #pragma unroll
-                for (int t = 0; t < TT; ++t) U[n][t] = f32x4{};
+                for (int t = 0; t < 2; ++t) ft[t] = piece<L>(lds.t, t, u, lane);
 #pragma unroll
-            for (int s = 0; s < TS; ++s)
+                for (int o = PARTS - 1 - u; o >= 0; --o)
 #pragma unroll
-                for (int u = PARTS - 1; u >= 0; --u) {
-                    Frag<L> ft[TT];
-#pragma unroll
-                    for (int t = 2 * s; t < TT; ++t) ft[t] = piece<L, C>(lds.t, PC::at(t, s), u, lane);
-#pragma unroll
-                    for (int o = PARTS - 1 - u; o >= 0; --o)
-#pragma unroll
-                        for (int t = 2 * s; t < TT; ++t)
-#pragma unroll
-                            for (int n = 0; n < NT; ++n) U[n][t] = mma(ft[t], fg[s][n][o], U[n][t]);
-                }
+                    for (int t = 0; t < 2; ++t) U[t] = mma(ft[t], fg[o], U[t]);
+            }
         }
         // An infinity or a NaN in k, v, beta, a decay or the state shows in U.
         float zero = 0.f;
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int t = 0; t < 2; ++t)
 #pragma unroll
-            for (int t = 0; t < TT; ++t)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) zero = __builtin_fmaf(U[n][t][i], 0.f, zero);
+            for (int i = 0; i < 4; ++i) zero = __builtin_fmaf(U[t][i], 0.f, zero);
         const bool odd = __ballot(!(zero == 0.f)) != 0;
         E *yc = OUT ? y + c * C * a.st.y_t : nullptr;
         if (__builtin_expect(odd, 0)) {
             // The products above would carry it to rows before its own, where T
             // and P are 0: the recurrence itself, row by row.
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int n = 0; n < NT; ++n) S[m][n] *= scale;
+            for (int m = 0; m < MT; ++m) S[m] *= scale;
             scale = 1.f;
             const int ln = anew(lane), l16 = ln & 15, g4 = (ln >> 4) * 4;
 #pragma unroll 1
             for (int j = 0; j < rows; ++j) {
                 const float dec = __expf(clamp_decay(la[(c * C + j) * a.la_t]));
                 const float beta = a.beta[(int64_t)(p.begin + c * C + j) * a.beta_t + h];
-                float dot[NT], out[NT];
-#pragma unroll
-                for (int n = 0; n < NT; ++n) dot[n] = out[n] = 0.f;
+                float dot = 0.f, out = 0.f;
 #pragma unroll
                 for (int s = 0; s < KS; ++s) {
                     const Frag<L> fk = frag8(ks + j * LK + 32 * s + 2 * g4);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            float &x = reinterpret_cast<float *>(&S[2 * s + i / 4][n])[i % 4];
-                            x *= dec;
-                            dot[n] += (float)fk.x[i] * x;
-                        }
+                    for (int i = 0; i < 8; ++i) {
+                        float &x = reinterpret_cast<float *>(&S[2 * s + i / 4])[i % 4];
+                        x *= dec;
+                        dot += (float)fk.x[i] * x;
+                    }
                 }
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    dot[n] += __shfl_xor(dot[n], 16);
-                    dot[n] += __shfl_xor(dot[n], 32);
-                    dot[n] = beta * (to_f(vs[j * LV + column(n, l16)]) - dot[n]);
-                }
+                dot += __shfl_xor(dot, 16);
+                dot += __shfl_xor(dot, 32);
+                dot = beta * (to_f(vs[j * LV + w0 + l16]) - dot);
 #pragma unroll
                 for (int s = 0; s < KS; ++s) {
                     const Frag<L> fk = frag8(ks + j * LK + 32 * s + 2 * g4), fq = frag8(qs + j * LK + 32 * s + 2 * g4);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            float &x = reinterpret_cast<float *>(&S[2 * s + i / 4][n])[i % 4];
-                            x += (float)fk.x[i] * dot[n];
-                            out[n] += (float)fq.x[i] * x;
-                        }
+                    for (int i = 0; i < 8; ++i) {
+                        float &x = reinterpret_cast<float *>(&S[2 * s + i / 4])[i % 4];
+                        x += (float)fk.x[i] * dot;
+                        out += (float)fq.x[i] * x;
+                    }
                 }
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    out[n] += __shfl_xor(out[n], 16);
-                    out[n] += __shfl_xor(out[n], 32);
-                    if (OUT && ln < 16 && column(n, l16) < cols) yc[j * a.st.y_t + column(n, l16)] = from_f<E>(out[n]);
-                }
+                out += __shfl_xor(out, 16);
+                out += __shfl_xor(out, 32);
+                if (OUT && ln < 16 && w0 + l16 < cols) yc[j * a.st.y_t + w0 + l16] = from_f<E>(out);
             }
             block_sync();
             continue;
@@ -552,74 +453,56 @@ __attribute__((amdgpu_waves_per_eu(DeltaPerCu<E, KP, VT>::per_simd, DeltaPerCu<E
         scale = __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(scale * d.all)));
         if (!(scale > 0x1p-16f && scale < 0x1p16f)) {   // and where it is NaN
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int n = 0; n < NT; ++n) S[m][n] *= scale;
+            for (int m = 0; m < MT; ++m) S[m] *= scale;
             scale = 1.f;
         }
         const float unscale = 1.f / scale;
 #pragma unroll
-        for (int t = 0; t < TT; ++t) {
-            const float e = d.in[16 * t + l16] * entered;
+        for (int t = 0; t < 2; ++t) Y[t] *= d.in[16 * t + l16] * entered;
+        if constexpr (OUT) {
+            Frag<L> fu[YU], fp[2];
+            split(fu, U[0], U[1]);
 #pragma unroll
-            for (int n = 0; n < NT; ++n) Y[n][t] *= e;
-        }
-#pragma unroll
-        for (int s = 0; s < TS; ++s) {
-            Frag<L> fu[NT][YU], fw[NT][PARTS];
-            const f32x4 wa = *reinterpret_cast<const f32x4 *>(d.out + 32 * s + g4) * unscale;
-            const f32x4 wb = *reinterpret_cast<const f32x4 *>(d.out + 32 * s + 16 + g4) * unscale;
-            if constexpr (OUT) {
-#pragma unroll
-                for (int n = 0; n < NT; ++n) split(fu[n], U[n][2 * s], U[n][2 * s + 1]);
-            Frag<L> fp[TT];
-#pragma unroll
-            for (int t = 2 * s; t < TT; ++t) {
+            for (int t = 0; t < 2; ++t) {
                 char *to = reinterpret_cast<char *>(&fp[t]);
 #pragma unroll
                 for (int i = 0; i < PC::UNITS; ++i)
-                    *reinterpret_cast<u32x4 *>(to + 16 * i) = *reinterpret_cast<const u32x4 *>(
-                        lds.p + ((PC::at(t, s) * PC::UNITS + i) * 64 + lane) * 16);
+                    *reinterpret_cast<u32x4 *>(to + 16 * i) =
+                        *reinterpret_cast<const u32x4 *>(lds.p + ((t * PC::UNITS + i) * 64 + lane) * 16);
             }
 #pragma unroll
             for (int u = YU - 1; u >= 0; --u)
 #pragma unroll
-                for (int t = 2 * s; t < TT; ++t)
+                for (int t = 0; t < 2; ++t) Y[t] = mma(fu[u], fp[t], Y[t]);
+        }
+        Frag<L> fw[PARTS];
+        split(fw, U[0] * (*reinterpret_cast<const f32x4 *>(d.out + g4) * unscale),
+              U[1] * (*reinterpret_cast<const f32x4 *>(d.out + 16 + g4) * unscale));
+        // four accumulators' rows at a time: as many products that do not wait for each other
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) Y[n][t] = mma(fu[n][u], fp[t], Y[n][t]);
-            }
+        for (int m0 = 0; m0 < MT; m0 += 4) {
+            Frag<L> fk[4];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) split(fw[n], U[n][2 * s] * wa, U[n][2 * s + 1] * wb);
-            // four accumulators' rows at a time: as many products that do not wait for each other
+            for (int m = 0; m < 4; ++m) fk[m] = frag_col<LK, true>(ks, 32 * ((m0 + m) / 2) + 4 * (m % 2), lane);
 #pragma unroll
-            for (int m0 = 0; m0 < MT; m0 += 4) {
-                Frag<L> fk[4];
+            for (int u = PARTS - 1; u >= 0; --u)
 #pragma unroll
-                for (int m = 0; m < 4; ++m)
-                    fk[m] = frag_col<LK, true>(ks + 32 * s * LK, 32 * ((m0 + m) / 2) + 4 * (m % 2), lane);
-#pragma unroll
-                for (int u = PARTS - 1; u >= 0; --u)
-#pragma unroll
-                    for (int m = 0; m < 4; ++m)
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) S[m0 + m][n] = mma(fk[m], fw[n][u], S[m0 + m][n]);
-            }
+                for (int m = 0; m < 4; ++m) S[m0 + m] = mma(fk[m], fw[u], S[m0 + m]);
         }
         if constexpr (OUT) {
             const rsrc_t r = make_rsrc(yc, ((rows - 1) * a.st.y_t + cols) * (int64_t)sizeof(E));
-            const int col = w0 + NT * g4;   // 4 NT columns from here on
-            constexpr int W = 4 * NT, PIECE = 16 / (int)sizeof(E) < W ? 16 / (int)sizeof(E) : W;
+            const int col = w0 + g4;   // 4 columns from here on
 #pragma unroll
-            for (int t = 0; t < TT; ++t) {
+            for (int t = 0; t < 2; ++t) {
                 const int row = 16 * t + l16;
                 const uint32_t off = (uint32_t)(row * (int)a.st.y_t + col) * (uint32_t)sizeof(E);
-                E out[W];
+                E out[4];
 #pragma unroll
-                for (int e = 0; e < W; ++e) out[e] = from_f<E>(Y[e / 4][t][e % 4]);
+                for (int e = 0; e < 4; ++e) out[e] = from_f<E>(Y[t][e]);
 #pragma unroll
-                for (int e = 0; e < W; e += VEC ? PIECE : 1) {
+                for (int e = 0; e < 4; e += VEC ? 4 : 1) {
                     const uint32_t o = row < rows && col + e < cols ? off + e * (uint32_t)sizeof(E) : kOOB;
-                    if constexpr (VEC && PIECE * sizeof(E) == 16) {
+                    if constexpr (VEC && sizeof(E) == 4) {
                         ssd::v4u x;
                         __builtin_memcpy(&x, out + e, 16);
                         __builtin_amdgcn_raw_buffer_store_b128(x, r, o, 0, 0);
@@ -644,9 +527,7 @@ __attribute__((amdgpu_waves_per_eu(DeltaPerCu<E, KP, VT>::per_simd, DeltaPerCu<E
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) ssd::gstore1(r, state_at(m, n, i, at), S[m][n][i] * scale);
+        for (int i = 0; i < 4; ++i) ssd::gstore1(r, state_at(m, i, at), S[m][i] * scale);
 }
 
 // The states that enter the segments of a sequence that was cut, in place of
@@ -758,7 +639,20 @@ __global__ __launch_bounds__(64 * CarryWaves<KP>::n) void k_delta_carry(DeltaArg
 
 // ---- host side
 
-static int col_tile(int64_t dk, int64_t dv) { return dk > 128 || dv <= 64 ? 64 : 128; }
+// Columns of a block: 64 where that leaves a block a CU of its own, whose chain
+// of chunks is then shorter (512 rows, 8 heads of 128: bfloat16 43 us, 128
+// columns 56; float32 104 and 154), and with bfloat16's and dk <= 64's few
+// registers and LDS, where two of them share one (8 prompts of 8192 rows, 16
+// heads of 64 x 128: 548 and 668).  Else 128, for T and P are then made half as
+// often (16 x 8192 rows, 16 heads of 128: 946 and 1088; float32, 2 x 8192: 780
+// and 1017).  Long sequences count as the pieces that they can be cut into.
+static int col_tile(const lin_shape &s, int dtype, int cus)
+{
+    if (s.dk > 128 || s.dv <= 64) return 64;
+    const int64_t pieces = s.T / 256 > s.N ? s.T / 256 : s.N;
+    if (pieces * s.H * ((s.dv + 63) / 64) <= cus) return 64;
+    return s.dk <= 64 && dtype == LAYER_BF16 ? 64 : 128;
+}
 
 struct DeltaPlan {
     int seg = 0, ids = 0, map_cols = 0, map_tiles = 0;
@@ -777,7 +671,7 @@ static DeltaPlan plan_delta(const lin_shape &s, int dtype, int64_t max_seqlen, i
 {
     DeltaPlan P;
     const int64_t longest = max_seqlen > 0 && max_seqlen < s.T ? max_seqlen : s.T;
-    const int64_t vt = col_tile(s.dk, s.dv), tiles = (s.dv + vt - 1) / vt, map_tiles = (s.dk + vt - 1) / vt;
+    const int64_t vt = col_tile(s, dtype, cus), tiles = (s.dv + vt - 1) / vt, map_tiles = (s.dk + vt - 1) / vt;
     const int64_t places = (vt == 64 && s.dk <= 128 && dtype == LAYER_BF16 ? 2 : 1) * (int64_t)cus;
     P.ids = (int)s.N;
     P.map_cols = (int)((s.dk + 3) / 4 * 4);
@@ -813,22 +707,21 @@ static size_t delta_workspace(const lin_shape &s, int64_t max_seqlen, int cus)
 template <typename E, int KP, int VT, bool VEC>
 static int run_delta(DeltaArgs &a, hipStream_t st)
 {
-    constexpr int C = DeltaPerCu<E, KP, VT>::C, threads = DeltaPerCu<E, KP, VT>::threads;
+    constexpr int threads = DeltaPerCu<E, KP, VT>::threads;
     if (a.seg > 0) {
         const int64_t grid = (int64_t)a.ids * a.H * (a.tiles + a.map_tiles);
-        k_delta_chunks<E, KP, VT, C, false, VEC><<<dim3((unsigned)grid), dim3(threads), 0, st>>>(a);
+        k_delta_chunks<E, KP, VT, false, VEC><<<dim3((unsigned)grid), dim3(threads), 0, st>>>(a);
         const dim3 carry((unsigned)(a.N * a.H), (unsigned)((a.dv + 15) / 16));
         k_delta_carry<KP><<<carry, dim3(64 * CarryWaves<KP>::n), 0, st>>>(a);
     }
     const int64_t grid = (int64_t)a.ids * a.H * a.tiles;
-    k_delta_chunks<E, KP, VT, C, true, VEC><<<dim3((unsigned)grid), dim3(threads), 0, st>>>(a);
+    k_delta_chunks<E, KP, VT, true, VEC><<<dim3((unsigned)grid), dim3(threads), 0, st>>>(a);
     return launch_status();
 }
 
 template <typename E, bool VEC>
-static int dispatch_delta(DeltaArgs &a, hipStream_t st)
+static int dispatch_delta(DeltaArgs &a, bool wide, hipStream_t st)
 {
-    const bool wide = col_tile(a.dk, a.dv) == 128;
     if (a.dk > 128) return run_delta<E, 256, 64, VEC>(a, st);
     if (a.dk > 64) return wide ? run_delta<E, 128, 128, VEC>(a, st) : run_delta<E, 128, 64, VEC>(a, st);
     return wide ? run_delta<E, 64, 128, VEC>(a, st) : run_delta<E, 64, 64, VEC>(a, st);
@@ -898,7 +791,7 @@ extern "C" int delta_prefill(const lin_shape *shape, int dtype, const lin_stride
     a.dk = (int)s.dk;
     a.dv = (int)s.dv;
     a.nslots = (int)s.slots;
-    const int vt = col_tile(s.dk, s.dv);
+    const int vt = col_tile(s, dtype, cus);
     a.tiles = (a.dv + vt - 1) / vt;
     a.seg = P.seg;
     a.ids = P.ids;
@@ -908,8 +801,9 @@ extern "C" int delta_prefill(const lin_shape *shape, int dtype, const lin_stride
     };
     const bool vec = rows16(q, a.st.q_t, a.st.q_g, s.dk) && rows16(k, a.st.k_t, a.st.k_g, s.dk) &&
                      rows16(v, a.st.v_t, a.st.v_h, s.dv) && rows16(y, a.st.y_t, a.st.y_h, s.dv);
+    const bool wide = vt == 128;
     hipStream_t st = static_cast<hipStream_t>(stream);
-    if (dtype == LAYER_BF16) return vec ? dispatch_delta<bf16, true>(a, st) : dispatch_delta<bf16, false>(a, st);
-    if (dtype == LAYER_F16) return vec ? dispatch_delta<f16, true>(a, st) : dispatch_delta<f16, false>(a, st);
-    return vec ? dispatch_delta<float, true>(a, st) : dispatch_delta<float, false>(a, st);
+    if (dtype == LAYER_BF16) return vec ? dispatch_delta<bf16, true>(a, wide, st) : dispatch_delta<bf16, false>(a, wide, st);
+    if (dtype == LAYER_F16) return vec ? dispatch_delta<f16, true>(a, wide, st) : dispatch_delta<f16, false>(a, wide, st);
+    return vec ? dispatch_delta<float, true>(a, wide, st) : dispatch_delta<float, false>(a, wide, st);
 }

@@ -45,7 +45,7 @@ template <typename E, int KP, bool VEC>
 __global__ __launch_bounds__(256) void k_delta_back_inverse(DeltaBackArgs a)
 {
     typedef typename std::conditional<std::is_same<E, bf16>::value, bf16, float>::type L;
-    typedef Pieces<L, CW> PC;
+    typedef Pieces<L> PC;
     constexpr int PT = 256, KS = KP / 32;
     constexpr int LK = KP + (sizeof(L) == 2 ? 16 : 4), LA = CW + 4;
     __shared__ __align__(16) L ks[CW * LK], qs[CW * LK];
@@ -196,7 +196,7 @@ __device__ __forceinline__ void walk(const DeltaBackArgs &a, WalkLds<E, KP> &lds
 {
     typedef WalkLds<E, KP> Lds;
     typedef typename Lds::L L;
-    typedef Pieces<L, CW> PC;
+    typedef Pieces<L> PC;
     constexpr int LK = Lds::LK, LV = Lds::LV, VT = Lds::VT, C = CW;
     constexpr int MT = KP / 16, KS = KP / 32, PARTS = PC::PARTS, PT = 256;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -283,8 +283,8 @@ __device__ __forceinline__ void walk(const DeltaBackArgs &a, WalkLds<E, KP> &lds
         for (int f = 0; f < 2; ++f)
 #pragma unroll
             for (int u = 0; u < PARTS; ++u) {
-                if (BACK) fp[f][u] = piece<L, C>(image + 2 * PC::BYTES, f, u, lane);
-                ft[f][u] = piece<L, C>(image + (BACK ? PC::BYTES : 0), f, u, lane);
+                if (BACK) fp[f][u] = piece<L>(image + 2 * PC::BYTES, f, u, lane);
+                ft[f][u] = piece<L>(image + (BACK ? PC::BYTES : 0), f, u, lane);
             }
     };
     if (chunks > 0) load_pieces(0);
@@ -1162,7 +1162,7 @@ static DeltaBackPlan plan_back(const lin_shape &s, int dtype, bool by_row)
         o += (bytes + 255) / 256 * 256;
         return at;
     };
-    const size_t image = dtype == LAYER_BF16 ? Pieces<bf16, CW>::BYTES : Pieces<float, CW>::BYTES;
+    const size_t image = dtype == LAYER_BF16 ? Pieces<bf16>::BYTES : Pieces<float>::BYTES;
     const size_t rows = (size_t)(P.walk_ids * s.H * CW * P.dvp) * 4, state = (size_t)(P.ids * s.H * s.dk * P.dvp) * 4;
     P.inv = take((size_t)(P.walk_ids * s.H) * 3 * image);
     P.zrec = take(rows);

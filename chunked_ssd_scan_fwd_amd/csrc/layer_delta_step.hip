@@ -8,8 +8,11 @@
 // of it can be written, so a block keeps its columns in registers, and y is
 // taken from the same pass over them: S'^T q = a S^T q + (k . q) u.
 //
-// 256 rows of 16 heads of 128 x 128 (537 MB): 110 us, 4.9 TB/s; one row of 8
-// heads 5.1 us.
+// The states go past the caches: by a next step the other layers' have taken
+// their place.  Over 3 GB of layers, each with 16 rows of 16 heads of 128 x 128,
+// 7.9 us a call, and through the caches 10.7; with 128 rows 50 and 60.
+//
+// 256 rows (537 MB): 96 us, 5.6 TB/s; one row of 8 heads 3.8 us.
 #include "layer_device.h"
 #include "ssd_internal.h"
 
@@ -30,7 +33,7 @@ struct DeltaStepArgs {
 
 // One block takes TV = CL * VEC columns of one head's state for one row: CL
 // threads across a row of the state, DT / CL rows at a time, NR times.
-template <typename T, int VEC, int CL, int NR, bool STREAM>
+template <typename T, int VEC, int CL, int NR>
 __global__ __launch_bounds__(DT) void k_delta_step(DeltaStepArgs a)
 {
     constexpr int TV = CL * VEC, R = DT / CL, W = DT / 64;
@@ -56,7 +59,7 @@ __global__ __launch_bounds__(DT) void k_delta_step(DeltaStepArgs a)
     for (int u = 0; u < NR; ++u) {
         const int r = r0 + u * R;
         x[u] = V{};
-        if (on && r < a.dk) x[u] = load_state<VEC, STREAM>(S + (int64_t)r * a.dv);
+        if (on && r < a.dk) x[u] = load_state<VEC, true>(S + (int64_t)r * a.dv);
     }
     bool before = false;
     int next = a.N;
@@ -129,35 +132,33 @@ __global__ __launch_bounds__(DT) void k_delta_step(DeltaStepArgs a)
 #pragma unroll
     for (int u = 0; u < NR; ++u) {
         const int r = r0 + u * R;
-        if (on && r < a.dk) store_state<VEC, STREAM>(S + (int64_t)r * a.dv, x[u]);
+        if (on && r < a.dk) store_state<VEC, true>(S + (int64_t)r * a.dv, x[u]);
     }
 }
 
-template <typename T, int VEC, int CL, bool STREAM>
+template <typename T, int VEC, int CL>
 static void launch_rows(DeltaStepArgs &a, hipStream_t st)
 {
     constexpr int R = DT / CL;
     a.tiles = (a.dv + CL * VEC - 1) / (CL * VEC);
     const dim3 grid((unsigned)((int64_t)a.N * a.H * a.tiles));
     if (a.dk <= 64)
-        k_delta_step<T, VEC, CL, 64 / R, STREAM><<<grid, dim3(DT), 0, st>>>(a);
+        k_delta_step<T, VEC, CL, 64 / R><<<grid, dim3(DT), 0, st>>>(a);
     else if (a.dk <= 128)
-        k_delta_step<T, VEC, CL, 128 / R, STREAM><<<grid, dim3(DT), 0, st>>>(a);
+        k_delta_step<T, VEC, CL, 128 / R><<<grid, dim3(DT), 0, st>>>(a);
     else
-        k_delta_step<T, VEC, CL, 256 / R, STREAM><<<grid, dim3(DT), 0, st>>>(a);
+        k_delta_step<T, VEC, CL, 256 / R><<<grid, dim3(DT), 0, st>>>(a);
 }
 
-// Columns of a block as for lin_step: 64 where that makes a block for every
-// CU, else 32; states of more than 128 MiB in a call go past the caches.
+// Columns of a block: 64 where that makes a block for every CU, else 32.  (16
+// heads of 128 x 128: 64 rows 25.7 us with 64, 26.9 with 32, 256 rows 95 and
+// 102; one row of 8 heads 4.7 and 4.4.)
 template <typename T>
 static void launch_delta_step(DeltaStepArgs &a, int cus, hipStream_t st)
 {
-    if (a.dv % 4 != 0 || misaligned(a.states, 16)) return launch_rows<T, 1, 32, false>(a, st);
-    const auto blocks = [&](int tv) { return (int64_t)a.N * a.H * ((a.dv + tv - 1) / tv); };
-    const bool stream = (int64_t)a.N * a.H * a.dk * a.dv * 4 > (int64_t(128) << 20);
-    if (a.dv > 32 && blocks(64) >= cus)
-        return stream ? launch_rows<T, 4, 16, true>(a, st) : launch_rows<T, 4, 16, false>(a, st);
-    return stream ? launch_rows<T, 4, 8, true>(a, st) : launch_rows<T, 4, 8, false>(a, st);
+    if (a.dv % 4 != 0 || misaligned(a.states, 16)) return launch_rows<T, 1, 32>(a, st);
+    if (a.dv > 32 && (int64_t)a.N * a.H * ((a.dv + 63) / 64) >= cus) return launch_rows<T, 4, 16>(a, st);
+    return launch_rows<T, 4, 8>(a, st);
 }
 
 }  // namespace layer
