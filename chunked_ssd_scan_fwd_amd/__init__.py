@@ -11,7 +11,8 @@ Layouts (float32, contiguous):
     q, k [B,G,T,dk]   v, dy [B,H,T,dv]   log_alpha [B,H,T]   h0 [B,H,dk,dv]
 
 The operators of a linear-attention layer (packed prefill, one-token step,
-group norm, 8-bit state cache) are in ``layer``; they too take float32 states
+group norm, 8-bit state cache; the gated delta rule's prefill, step and
+gradients; beam search's selection and reordering of states) are in ``layer``; they too take float32 states
 and log decays, and their activations may be bfloat16 or float16.
 """
 from __future__ import annotations

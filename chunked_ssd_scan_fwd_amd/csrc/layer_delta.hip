@@ -8,20 +8,23 @@ namespace layer {
 // nor U crosses waves: K S comes out of the accumulators as the operand that T
 // takes, and U as the one that P and K^T take.
 //
-// Four more waves fetch the next chunk and make its T and its decays, in two
-// steps with a barrier between them, while the first ones work on this chunk:
-//   K S and Q S, P        | T's blocks joined (solve), the next tiles to LDS
-//   U, P U, S             | A's tiles and the diagonal blocks' inverses (diagonal), loads
+// Four more waves make what the next chunk needs, in two steps with a barrier
+// between them, while the first ones work on this chunk: two have 16 rows of T
+// each, two fetch and make the decays and P.
+//   K S and Q S  | T's blocks joined (solve)                   | P to LDS, the tiles, loads
+//   U, P U, S    | A's tiles, inverses of the diagonal's blocks | P, decays
 // T in a kernel of its own beforehand cost 460 us beside the large batch's 721
 // (16 prompts of 8192 rows, 16 heads of 128), and 18 KB of memory a chunk and
-// head; so the batch takes 890 to 945 us.  There a chunk of 64 rows takes 13500
-// cycles: the waves that hold S work 5800 in either step, the others 6600 and
-// 6900, and matrix and vector instructions fill 0.5 and 0.4 of a SIMD's time.
+// head; so the batch takes 890 to 946 us.  There a chunk takes a CU 7300 cycles,
+// of which a SIMD has vector instructions under way in 0.52 (S in parts most of
+// all, which is anew for every chunk) and matrix ones in 0.37.
 //
-// Eight waves of 16 columns and four others, three waves to a SIMD, took 721 us
-// (T beforehand) where four of 32 columns and four took 808: one wave's matrix
-// products run beside another's vector instructions.  Sixteen waves spilled
-// registers (1015 to 1065 us, T beside).
+// Chunks of 64 rows, whose S is split half as often, took as long (935): P and
+// T have twice the products for a row then, and four waves that both fetch and
+// have rows of T.  They made a prompt of 77 rows 20 us for 17.  Eight waves of 16
+// columns beside four others took 721 us (64 rows, T beforehand) where four of
+// 32 columns and four took 808: one wave's matrix products run beside another's
+// vector instructions.
 //
 // For bfloat16 inputs everything that reaches the state keeps float32's
 // accuracy: S, T, the residual V - diag(e^b) K S and U enter their products as
@@ -666,7 +669,8 @@ struct DeltaPlan {
 // each, those of the blocks for B and M, with 1.2 us for each segment that the
 // carry pass joins and 15 us for two launches more.  (One prompt of 32768 rows,
 // 8 heads of 128: 3123 us whole; cut into 32 the maps take 195, the carry pass
-// 73 and the outputs 121.)
+// 73 and the outputs 121.  20 prompts, 3000 rows the longest, 24 heads of 128 x
+// 64: 216 us whole, 177 cut.  8 prompts of 8192, 32 heads of 64: 562 and 930.)
 static DeltaPlan plan_delta(const lin_shape &s, int dtype, int64_t max_seqlen, int cus)
 {
     DeltaPlan P;
