@@ -88,6 +88,38 @@ def test_prefill_cut_at_other_heads(heads, dtype):
     check_prefill("cut", heads, dtype, [1500, 1700], carry=[0, 1], slots=[2, 0], npool=3, tail=2, seed=13, mu=-6.0)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF, F16])
+@pytest.mark.parametrize("heads", [(2, 144, 128, 128), (1, 150, 33, 97), (4, 144, 64, 128), (1, 90, 100, 200), (2, 80, 77, 256)])
+def test_prefill_many_heads(heads, dtype):
+    """Blocks of 128 columns, which batches of few blocks do not get."""
+    check_prefill("many heads", heads, dtype, [1, 40, 130, 65], carry=[1, 0, 1, 1], slots=[4, 2, 0, 1], npool=5, tail=3,
+                  seed=heads[2], strided=heads[2] == 77)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF, F16])
+@pytest.mark.parametrize("heads", [(1, 8, 128, 128), (2, 8, 100, 97), (1, 8, 128, 256)])
+def test_prefill_many_heads_cut(heads, dtype):
+    assert ssd.layer.delta_prefill_workspace_size(5100, 3, *heads, 3) > 0
+    check_prefill("many heads, cut", heads, dtype, [4500, 0, 600], carry=[1, 0, 0], seed=6, mu=-6.0)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("bad", [NAN, INF])
+def test_prefill_many_heads_infinities_and_nan(bad, dtype):
+    G, H, dk, dv = 1, 144, 128, 128
+    q, k, v, ld, beta, S = (dev(t) for t in ref.inputs(200, G, H, dk, dv, dtype, True, 9, 2))
+    clean = S.clone()
+    want = ssd.delta_prefill(q, k, v, ld, beta, ids([0, 90, 200]), clean)
+    v[131, 140, 70] = bad
+    say(f"delta_prefill many heads v {bad} {dtype}")
+    y = ssd.delta_prefill(q, k, v, ld, beta, ids([0, 90, 200]), S)
+    assert torch.equal(y[:90], want[:90]) and torch.equal(y[:, :140], want[:, :140]) and torch.equal(S[0], clean[0])
+    assert bool(torch.isfinite(y[:131]).all()) and not bool(torch.isfinite(y[131:, 140, 70]).any())
+    y[131:, 140, 70] = want[131:, 140, 70]
+    assert float((y.double() - want.double()).abs().max()) < 0.05
+    assert not bool(torch.isfinite(S[1, 140, :, 70]).all())
+
+
 def test_prefill_long_runs_are_cut():
     """The shapes above do run cut: they ask for a workspace."""
     for shape in ((4500, 1, 1, 1, 128, 128, 1), (4417, 4, 1, 2, 64, 48, 4), (3202, 2, 1, 1, 256, 130, 3),
