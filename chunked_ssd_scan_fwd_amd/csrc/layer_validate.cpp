@@ -81,12 +81,16 @@ int check_cache(const state_cache_shape *s)
     return SSD_OK;
 }
 
+// A place among a request's candidates, and the end of the 8 tiles of 2048 that
+// may follow it, fit 31 bits.
+constexpr int64_t kMaxCandidates = (int64_t(1) << 31) - (1 << 14) - 1;
+
 int check_beam(const beam_shape *s)
 {
     if (!s) return SSD_ERR_NULL;
     if (s->requests < 0 || s->beams < 1 || s->vocabulary < 1 || s->n < 1) return SSD_ERR_SHAPE;
     if (s->beams > BEAM_MAX || s->n > BEAM_MAX) return SSD_ERR_UNSUPPORTED;
-    if (s->requests >= kMaxCount || s->vocabulary > ((int64_t(1) << 31) - 1) / s->beams) return SSD_ERR_SHAPE;
+    if (s->requests >= kMaxCount || s->vocabulary > kMaxCandidates / s->beams) return SSD_ERR_SHAPE;
     // a wave for 2048 logits or more
     const int64_t pieces = (s->vocabulary + 2047) / 2048;
     return s->requests * s->beams > max_blocks(256) / pieces ? SSD_ERR_SHAPE : SSD_OK;

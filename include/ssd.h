@@ -578,7 +578,7 @@ int state_unpack(const state_cache_shape *shape, const uint8_t *cache, const uin
  * candidates of the greatest
  *     score(k, v) = scores[k] + logits[k][v] - log sum_u exp(logits[k][u]),
  * in falling order, of equal ones the lowest k vocabulary + v first.  Sums of
- * exponentials are float32 within 2048 logits of a lane's part and 64 bits
+ * exponentials are float32 within pieces of 2048 to 16384 logits and 64 bits
  * beyond; scores are compared in 64 bits and rounded once.
  *   logits    of type `dtype`, a row of `vocabulary` for each beam, ld_beam
  *             elements apart, ld_request between requests
@@ -592,7 +592,7 @@ int state_unpack(const state_cache_shape *shape, const uint8_t *cache, const uin
  * A logit of -infinity is never taken.  A beam whose logits hold a NaN or
  * +infinity, or nothing but -infinity, offers nothing.  Rows of beams that
  * offer nothing by their score, or have ended, are not read.
- * 1 <= n, beams <= BEAM_MAX, beams vocabulary < 2^31, requests < 2^24 and
+ * 1 <= n, beams <= BEAM_MAX, beams vocabulary < 2^31 - 2^14, requests < 2^24 and
  * requests beams ceil(vocabulary / 2048) < 2^24. */
 #define BEAM_MAX 64
 typedef struct beam_shape {

@@ -50,6 +50,15 @@ def test_select_refuses():
         ssd.beam_select(torch.zeros(1, 2, 8, dtype=torch.float64), torch.zeros(1, 2), 2)
 
 
+def test_select_refuses_places_past_31_bits():
+    """The last tiles of a row end within 31 bits too."""
+    for beams in (1, 2, 64):
+        most = ((1 << 31) - (1 << 14) - 1) // beams
+        assert ssd.layer.beam_select_workspace_size(1, beams, most, 4) > 0
+        for V in (most + 1, ((1 << 31) - 1) // beams):
+            assert select(BeamShapeArg(1, beams, V, 4)) == SHAPE
+
+
 def reorder(shape, parents=P, slots=P, states=P):
     return ssd.library().state_reorder(ctypes.byref(shape), parents, slots, states, None)
 
