@@ -39,6 +39,8 @@ int check_delta_bwd(const lin_shape *s)
     // both walks of a sequence in one launch, and four columns of a row's q to a thread
     const int64_t tiles = (s->dv + 63) / 64;
     if (s->N > max_blocks(512) / (2 * s->H * tiles)) return SSD_ERR_SHAPE;
+    // a block of 512 threads for each chunk of the products and head
+    if (s->T / (s->dk > 128 ? 32 : 64) + s->N > max_blocks(512) / s->H) return SSD_ERR_SHAPE;
     return s->G != s->H && s->T > max_blocks(256) * 256 / (s->G * s->dk) ? SSD_ERR_SHAPE : SSD_OK;
 }
 

@@ -490,8 +490,8 @@ int delta_step(const lin_shape *shape, int dtype, const lin_strides *strides,
  * An infinity or a NaN reaches gradients of its sequence in the heads of its
  * group, and dlog_decay of those heads where that is a sum, no others; where
  * the formulas give an infinity, NaN may stand.
- * Limits as for delta_prefill, 2 N H ceil(dv / 64) < 2^23, and T G dk < 2^32
- * where heads share q and k. */
+ * Limits as for delta_prefill, 2 N H ceil(dv / 64) < 2^23, (T / 64 + N) H < 2^23
+ * (T / 32 for dk over 128), and T G dk < 2^32 where heads share q and k. */
 size_t delta_bwd_workspace_size(const lin_shape *shape);
 int delta_bwd(const lin_shape *shape, int dtype, const lin_strides *strides,
               const void *q, const void *k, const void *v,

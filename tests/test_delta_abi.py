@@ -58,6 +58,16 @@ def test_shapes_refused(which, shape, code):
     assert call(LinShapeArg(*shape), which) == code
 
 
+@pytest.mark.parametrize("dk,rows", [(256, 32), (8, 64)])
+def test_bwd_refuses_more_chunks_than_a_grid_holds(dk, rows):
+    size = ssd.layer.delta_bwd_workspace_size
+    most = (1 << 23) - 1   # chunks, one of them for the sequence's remainder
+    assert size((most - 1) * rows, 1, 1, 1, dk, 1) > 0
+    with pytest.raises(ValueError):
+        size(most * rows, 1, 1, 1, dk, 1)
+    assert call(LinShapeArg(most * rows, 1, 1, 1, dk, 1, 1), "bwd") == SHAPE
+
+
 @pytest.mark.parametrize("which", ["prefill", "step", "bwd"])
 def test_arguments_refused(which):
     s = LinShapeArg(5, 2, 1, 4, 8, 8, 4)
