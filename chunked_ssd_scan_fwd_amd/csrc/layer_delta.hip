@@ -41,7 +41,10 @@ struct DeltaLds {
     static constexpr int PAD = sizeof(L) == 2 ? 16 : 4;
     static constexpr int LK = KP + PAD, LV = VT + PAD;
     static constexpr int PBYTES = PC::BYTES / PC::PARTS;
-    L q[2][C * LK], k[2][C * LK], v[2][C * LV];
+    // k a step earlier than q and v, where a third tile of it fits
+    static constexpr bool EARLY = KP <= 128 || sizeof(L) == 2;
+    static constexpr int KB = EARLY ? 3 : 2;
+    L q[2][C * LK], k[KB][C * LK], v[2][C * LV];
     alignas(16) char p[PBYTES], t[PC::BYTES];
     // the next chunk's diagonal blocks of T, and A's tile below, by lanes
     alignas(16) f32x4 diag[2][64], low[64];
@@ -87,7 +90,8 @@ __attribute__((amdgpu_waves_per_eu(DeltaPerCu<E, KP, VT>::per_simd, DeltaPerCu<E
     typedef DeltaLds<E, KP, VT> Lds;
     typedef typename Lds::L L;
     typedef Pieces<L> PC;
-    constexpr int LK = Lds::LK, LV = Lds::LV;
+    constexpr int LK = Lds::LK, LV = Lds::LV, KB = Lds::KB;
+    constexpr bool EARLY = Lds::EARLY;
     constexpr int WAVES = DeltaPerCu<E, KP, VT>::waves, MT = KP / 16, KS = KP / 32;
     constexpr int PARTS = PC::PARTS, YU = PARTS == 3 ? 2 : 1;
     constexpr int MOVERS = DeltaPerCu<E, KP, VT>::movers, PT = 64 * MOVERS;   // threads that fetch
@@ -150,16 +154,24 @@ __attribute__((amdgpu_waves_per_eu(DeltaPerCu<E, KP, VT>::per_simd, DeltaPerCu<E
         const bool mover = wave < WAVES + MOVERS;
         Tile<E, C, KP, PT> tq, tk;
         Tile<E, C, VT, PT> tv;
+        // Of a chunk past the last one nothing is loaded, and the zeros that it
+        // leaves are not read.
+        const auto load_k = [&](int c) {
+            const int t0 = c * C, rows = p.rows - t0, tid = anew(threadIdx.x - 64 * WAVES);
+            tk.template fetch<VEC>(k + t0 * a.st.k_t, a.st.k_t, min(C, rows), a.dk, tid);
+        };
+        const auto store_k = [&](int c) {
+            const int tid = anew(threadIdx.x - 64 * WAVES);
+            tk.template place<VEC, LK>(lds.k[c % KB], k + c * C * a.st.k_t, a.st.k_t, a.dk, tid);
+        };
         const auto load = [&](int c) {
             const int t0 = c * C, rows = p.rows - t0, tid = anew(threadIdx.x - 64 * WAVES);
             if (OUT) tq.template fetch<VEC>(q + t0 * a.st.q_t, a.st.q_t, min(C, rows), a.dk, tid);
-            tk.template fetch<VEC>(k + t0 * a.st.k_t, a.st.k_t, min(C, rows), a.dk, tid);
             tv.template fetch<VEC>(v + t0 * a.st.v_t, a.st.v_t, map ? 0 : min(C, rows), cols, tid);
         };
         const auto store = [&](int c) {
             const int b = c & 1, tid = anew(threadIdx.x - 64 * WAVES);
             if (OUT) tq.template place<VEC, LK>(lds.q[b], q + c * C * a.st.q_t, a.st.q_t, a.dk, tid);
-            tk.template place<VEC, LK>(lds.k[b], k + c * C * a.st.k_t, a.st.k_t, a.dk, tid);
             tv.template place<VEC, LV>(lds.v[b], v + c * C * a.st.v_t, a.st.v_t, cols, tid);
         };
         const float *beta = a.beta + p.begin * a.beta_t + h;
@@ -173,14 +185,12 @@ __attribute__((amdgpu_waves_per_eu(DeltaPerCu<E, KP, VT>::per_simd, DeltaPerCu<E
             if (w == 0) make_decays(lds.dec[c % 3], x, lane);
             if (w == 1 && lane < C) lds.beta[c % 3][lane] = x;
         };
-        // T in two steps, a row block of 16 to a wave.  First the tiles of
-        // A = diag(beta) M left of the diagonal, and the diagonal block's
-        // inverse X by substitution: a lane holds rows 4 g .. 4 g + 3 of column
-        // l % 16, so four rows at a time, which the lanes of the others then
-        // take off theirs.
-        const auto diagonal = [&](int c) {
+        // T in three steps, a row block of 16 to a wave.  First the diagonal
+        // block of A = diag(beta) M, and the tile left of it.
+        f32x4 m;
+        const auto products = [&](int c) {
             const int lane = anew(threadIdx.x & 63), l16 = lane & 15, g4 = (lane >> 4) * 4;
-            const L *ks = lds.k[c & 1];
+            const L *ks = lds.k[c % KB];
             const Decays<C> &d = lds.dec[c % 3];
             const float *betas = lds.beta[c % 3];
             Frag<L> fk[KS];
@@ -189,7 +199,7 @@ __attribute__((amdgpu_waves_per_eu(DeltaPerCu<E, KP, VT>::per_simd, DeltaPerCu<E
             const f32x4 ih = *reinterpret_cast<const f32x4 *>(d.hi + 16 * w + g4);
             const f32x4 il = *reinterpret_cast<const f32x4 *>(d.lo + 16 * w + g4);
             const f32x4 bt = *reinterpret_cast<const f32x4 *>(betas + 16 * w + g4);
-            f32x4 m = {};
+            m = f32x4{};
 #pragma unroll
             for (int s = 0; s < KS; ++s) m = mma(fk[s], fk[s], m);
             const auto scaled = [&](f32x4 &x, int j) {
@@ -198,43 +208,9 @@ __attribute__((amdgpu_waves_per_eu(DeltaPerCu<E, KP, VT>::per_simd, DeltaPerCu<E
                 for (int e = 0; e < 4; ++e) x[e] *= bt[e] * __expf((ih[e] - jh) + (il[e] - jl));
             };
             scaled(m, w);
-            f32x4 X;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
+            for (int e = 0; e < 4; ++e)
                 if (l16 >= g4 + e) m[e] = 0.f;
-                X[e] = l16 == g4 + e ? 1.f : 0.f;
-            }
-            // the four rows' own block of A
-            const int own = 5 * g4;
-            const float a10 = __shfl(m[1], own), a20 = __shfl(m[2], own), a21 = __shfl(m[2], own + 1);
-            const float a30 = __shfl(m[3], own), a31 = __shfl(m[3], own + 1), a32 = __shfl(m[3], own + 2);
-            const auto rows4 = [&](auto which) {
-                constexpr int n = decltype(which)::value;
-                f32x4 y = X;
-                y[1] -= a10 * y[0];
-                y[2] -= a20 * y[0] + a21 * y[1];
-                y[3] -= a30 * y[0] + a31 * y[1] + a32 * y[2];
-                if (g4 == 4 * n) X = y;
-                if constexpr (n < 3) {
-                    const auto column = [&](int e, auto j) {   // A(g4 + e, 4 n + j)
-                        constexpr int ctrl = 0x150 + 4 * n + decltype(j)::value;   // row_newbcast
-                        return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(m[e]), ctrl, 0xf, 0xf, true));
-                    };
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) y[e] = row_of_lanes<n>(y[e]);
-                    f32x4 x = X;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        x[e] -= (column(e, ssd::IntC<0>{}) * y[0] + column(e, ssd::IntC<1>{}) * y[1]) +
-                                (column(e, ssd::IntC<2>{}) * y[2] + column(e, ssd::IntC<3>{}) * y[3]);
-                    if (g4 > 4 * n) X = x;
-                }
-            };
-            rows4(ssd::IntC<0>{});
-            rows4(ssd::IntC<1>{});
-            rows4(ssd::IntC<2>{});
-            rows4(ssd::IntC<3>{});
-            lds.diag[w][lane] = X;
             if (w == 1) {
                 f32x4 x = {};
 #pragma unroll
@@ -243,7 +219,54 @@ __attribute__((amdgpu_waves_per_eu(DeltaPerCu<E, KP, VT>::per_simd, DeltaPerCu<E
                 lds.low[lane] = x;
             }
         };
-        // Then T_10 = -T_11 A_10 T_00.  Held transposed, so that T_11 A_10 comes
+        // Then the diagonal block's inverse X by substitution: a lane holds rows
+        // 4 g .. 4 g + 3 of column l % 16, so four rows at a time, which the
+        // lanes of the others then take off theirs.
+        const auto inverse = [&]() {
+            const int lane = anew(threadIdx.x & 63), l16 = lane & 15, g4 = (lane >> 4) * 4;
+            f32x4 X;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) X[e] = l16 == g4 + e ? 1.f : 0.f;
+            const auto rows4 = [&](auto which) {
+                constexpr int n = decltype(which)::value;
+                const auto column = [&](int e, auto j) {   // A(g4 + e, 4 n + j)
+                    constexpr int ctrl = 0x150 + 4 * n + decltype(j)::value;   // row_newbcast
+                    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(m[e]), ctrl, 0xf, 0xf, true));
+                };
+                const ssd::IntC<0> j0;
+                const ssd::IntC<1> j1;
+                const ssd::IntC<2> j2;
+                const ssd::IntC<3> j3;
+                f32x4 y = X;
+                y[1] -= column(1, j0) * y[0];
+                y[2] -= column(2, j0) * y[0];
+                y[3] -= column(3, j0) * y[0];
+                y[2] -= column(2, j1) * y[1];
+                y[3] -= column(3, j1) * y[1];
+                y[3] -= column(3, j2) * y[2];
+                if (g4 == 4 * n) X = y;
+                if constexpr (n < 3) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) y[e] = row_of_lanes<n>(y[e]);
+                    f32x4 x = X;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[e] -= column(e, j0) * y[0];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[e] -= column(e, j1) * y[1];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[e] -= column(e, j2) * y[2];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[e] -= column(e, j3) * y[3];
+                    if (g4 > 4 * n) X = x;
+                }
+            };
+            rows4(ssd::IntC<0>{});
+            rows4(ssd::IntC<1>{});
+            rows4(ssd::IntC<2>{});
+            rows4(ssd::IntC<3>{});
+            lds.diag[w][lane] = X;
+        };
+        // At last T_10 = -T_11 A_10 T_00.  Held transposed, so that T_11 A_10 comes
         // out of the accumulators as the next product's operand, and T's rows as
         // its pieces hold them.
         const auto put_t = [&](int row, int j, f32x4 x) {
@@ -275,43 +298,59 @@ __attribute__((amdgpu_waves_per_eu(DeltaPerCu<E, KP, VT>::per_simd, DeltaPerCu<E
             const auto make_scores = [&](int c) {
                 if (!OUT) return;
                 const int lane = anew(threadIdx.x & 63), b = c & 1;
-                P0 = scores(lds.dec[c % 3], lds.q[b], lds.k[b], 1, w, lane);
-                if (w == 1) P1 = scores(lds.dec[c % 3], lds.q[b], lds.k[b], 0, 0, lane);
+                P0 = scores(lds.dec[c % 3], lds.q[b], lds.k[c % KB], 1, w, lane);
+                if (w == 1) P1 = scores(lds.dec[c % 3], lds.q[b], lds.k[c % KB], 0, 0, lane);
             };
             const auto write_scores = [&]() {
                 if (!OUT) return;
                 put_scores(1, w, P0);
                 if (w == 1) put_scores(0, 0, P1);
             };
-            // Without conditions: a chunk past the last one loads nothing and
-            // leaves zeros in a buffer that is not read.
             row_values(0, row_value(0));
             float next = row_value(1);
+            load_k(0);
             load(0);
+            store_k(0);
             store(0);
+            load_k(1);
             load(1);
             block_sync();
             make_scores(0);
             row_values(1, next);
+            if (EARLY) {
+                store_k(1);
+                load_k(2);
+            }
             block_sync();
             for (int c = 0; c < chunks; ++c) {
                 next = row_value(c + 2);
                 write_scores();
+                if (!EARLY) {
+                    store_k(c + 1);
+                    load_k(c + 2);
+                }
                 store(c + 1);
                 load(c + 2);
                 block_sync();
                 make_scores(c + 1);
                 row_values(c + 2, next);
+                if (EARLY) {
+                    store_k(c + 2);
+                    load_k(c + 3);
+                }
                 block_sync();
             }
         } else {
             block_sync();
-            diagonal(0);
+            products(0);
+            inverse();
             block_sync();
             for (int c = 0; c < chunks; ++c) {
                 solve(c);
+                if (EARLY) products(c + 1);
                 block_sync();
-                diagonal(c + 1);
+                if (!EARLY) products(c + 1);
+                inverse();
                 block_sync();
             }
         }
@@ -351,7 +390,7 @@ __attribute__((amdgpu_waves_per_eu(DeltaPerCu<E, KP, VT>::per_simd, DeltaPerCu<E
     for (int c = 0; c < chunks; ++c) {
         const int b = c & 1, rows = min(C, p.rows - c * C);
         const Decays<C> &d = lds.dec[c % 3];
-        const L *qs = lds.q[b], *ks = lds.k[b], *vs = lds.v[b];
+        const L *qs = lds.q[b], *ks = lds.k[c % KB], *vs = lds.v[b];
         // X = K S (rows: the chunk's, columns: of v), Y^T = S^T Q^T
         f32x4 X[2], Y[2];
 #pragma unroll
