@@ -47,7 +47,7 @@ struct DeltaLds {
     L q[2][C * LK], k[KB][C * LK], v[2][C * LV];
     alignas(16) char p[PBYTES], t[PC::BYTES];
     // the next chunk's diagonal blocks of T, and A's tile below, by lanes
-    alignas(16) f32x4 diag[2][64], low[64];
+    alignas(16) f32x4 diag[2][64], low[EARLY ? 2 : 1][64];
     Decays<C> dec[3];
     alignas(16) float beta[3][C];
 };
@@ -186,7 +186,7 @@ __attribute__((amdgpu_waves_per_eu(DeltaPerCu<E, KP, VT>::per_simd, DeltaPerCu<E
             if (w == 1 && lane < C) lds.beta[c % 3][lane] = x;
         };
         // T in three steps, a row block of 16 to a wave.  First the diagonal
-        // block of A = diag(beta) M, and the tile left of it.
+        // blocks of A = diag(beta) M, and the tile left of the second.
         f32x4 m;
         const auto products = [&](int c) {
             const int lane = anew(threadIdx.x & 63), l16 = lane & 15, g4 = (lane >> 4) * 4;
@@ -196,27 +196,28 @@ __attribute__((amdgpu_waves_per_eu(DeltaPerCu<E, KP, VT>::per_simd, DeltaPerCu<E
             Frag<L> fk[KS];
 #pragma unroll
             for (int s = 0; s < KS; ++s) fk[s] = frag8(ks + (16 * w + l16) * LK + 32 * s + 2 * g4);
-            const f32x4 ih = *reinterpret_cast<const f32x4 *>(d.hi + 16 * w + g4);
-            const f32x4 il = *reinterpret_cast<const f32x4 *>(d.lo + 16 * w + g4);
-            const f32x4 bt = *reinterpret_cast<const f32x4 *>(betas + 16 * w + g4);
-            m = f32x4{};
-#pragma unroll
-            for (int s = 0; s < KS; ++s) m = mma(fk[s], fk[s], m);
-            const auto scaled = [&](f32x4 &x, int j) {
+            // times beta and the decays: rows of block i, columns of block j
+            const auto scaled = [&](f32x4 x, int i, int j) {
+                const f32x4 ih = *reinterpret_cast<const f32x4 *>(d.hi + 16 * i + g4);
+                const f32x4 il = *reinterpret_cast<const f32x4 *>(d.lo + 16 * i + g4);
+                const f32x4 bt = *reinterpret_cast<const f32x4 *>(betas + 16 * i + g4);
                 const float jh = d.hi[16 * j + l16], jl = d.lo[16 * j + l16];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) x[e] *= bt[e] * __expf((ih[e] - jh) + (il[e] - jl));
+                return x;
             };
-            scaled(m, w);
+            m = f32x4{};
+#pragma unroll
+            for (int s = 0; s < KS; ++s) m = mma(fk[s], fk[s], m);
+            m = scaled(m, w, w);
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 if (l16 >= g4 + e) m[e] = 0.f;
-            if (w == 1) {
+            if (w == 0) {   // the other wave's part of `solve` is the longer
                 f32x4 x = {};
 #pragma unroll
-                for (int s = 0; s < KS; ++s) x = mma(fk[s], frag8(ks + l16 * LK + 32 * s + 2 * g4), x);
-                scaled(x, 0);
-                lds.low[lane] = x;
+                for (int s = 0; s < KS; ++s) x = mma(frag8(ks + (16 + l16) * LK + 32 * s + 2 * g4), fk[s], x);
+                lds.low[EARLY ? c & 1 : 0][lane] = scaled(x, 1, 0);
             }
         };
         // Then the diagonal block's inverse X by substitution: a lane holds rows
@@ -283,7 +284,7 @@ __attribute__((amdgpu_waves_per_eu(DeltaPerCu<E, KP, VT>::per_simd, DeltaPerCu<E
 #pragma unroll
             for (int e = 0; e < 4; ++e) T[e] = x[4 * (g4 + e)];
             if (w == 1) {
-                const f32x4 sum = times(lds.low[lane], T, f32x4{});
+                const f32x4 sum = times(lds.low[EARLY ? c & 1 : 0][lane], T, f32x4{});
                 put_t(1, 0, times(lds.diag[0][lane], -sum, f32x4{}) * *reinterpret_cast<const f32x4 *>(betas + g4));
             }
             put_t(w, w, T * *reinterpret_cast<const f32x4 *>(betas + 16 * w + g4));
@@ -358,7 +359,6 @@ __attribute__((amdgpu_waves_per_eu(DeltaPerCu<E, KP, VT>::per_simd, DeltaPerCu<E
     }
 
     // ---- states and outputs
-    __builtin_amdgcn_s_setprio(1);
     const int64_t state = (int64_t)a.dk * width;
     float *pool = p.slot < 0 ? nullptr : a.states + ((int64_t)p.slot * a.H + h) * state;
     float *ends = (map ? a.maps : a.ends) + ((int64_t)id * a.H + h) * state;
