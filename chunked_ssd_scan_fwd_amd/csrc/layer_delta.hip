@@ -11,13 +11,16 @@ namespace layer {
 // Four more waves make what the next chunk needs, in two steps with a barrier
 // between them, while the first ones work on this chunk: two have 16 rows of T
 // each, two fetch and make the decays and P.
-//   K S and Q S  | T's blocks joined (solve)                   | P to LDS, the tiles, loads
-//   U, P U, S    | A's tiles, inverses of the diagonal's blocks | P, decays
+//   K S and Q S  | T's blocks joined (solve), the next A (products) | P to LDS, q and v, loads
+//   U, P U, S    | inverses of the diagonal's blocks (inverse)     | P, decays, k
+// k comes a step earlier than q and v where LDS holds three tiles of it, for in
+// the second step A's products made T's waves the last by 1300 cycles of 5800
+// (512 rows, 8 heads: 43 us so, and 39.5).
 // T in a kernel of its own beforehand cost 460 us beside the large batch's 721
 // (16 prompts of 8192 rows, 16 heads of 128), and 18 KB of memory a chunk and
-// head; so the batch takes 890 to 946 us.  There a chunk takes a CU 7300 cycles,
-// of which a SIMD has vector instructions under way in 0.52 (S in parts most of
-// all, which is anew for every chunk) and matrix ones in 0.37.
+// head; so the batch takes 904 to 931 us.  There a chunk takes a CU 6900 cycles,
+// of which a SIMD has vector instructions under way in 0.55 (S in parts is anew
+// for every chunk) and matrix ones in 0.39: little is left to fill.
 //
 // Chunks of 64 rows, whose S is split half as often, took as long (935): P and
 // T have twice the products for a row then, and four waves that both fetch and
@@ -682,8 +685,8 @@ __global__ __launch_bounds__(64 * CarryWaves<KP>::n) void k_delta_carry(DeltaArg
 // ---- host side
 
 // Columns of a block: 64 where that leaves a block a CU of its own, whose chain
-// of chunks is then shorter (512 rows, 8 heads of 128: bfloat16 43 us, 128
-// columns 56; float32 104 and 154), and with bfloat16's and dk <= 64's few
+// of chunks is then shorter (512 rows, 8 heads of 128: bfloat16 43 us where 128
+// columns take 56; float32 104 and 154), and with bfloat16's and dk <= 64's few
 // registers and LDS, where two of them share one (8 prompts of 8192 rows, 16
 // heads of 64 x 128: 548 and 668).  Else 128, for T and P are then made half as
 // often (16 x 8192 rows, 16 heads of 128: 946 and 1088; float32, 2 x 8192: 780
@@ -707,8 +710,8 @@ struct DeltaPlan {
 // rows over the places; cut, the output pass's rows and, for 0.7 of its time
 // each, those of the blocks for B and M, with 1.2 us for each segment that the
 // carry pass joins and 15 us for two launches more.  (One prompt of 32768 rows,
-// 8 heads of 128: 3123 us whole; cut into 32 the maps take 195, the carry pass
-// 73 and the outputs 121.  20 prompts, 3000 rows the longest, 24 heads of 128 x
+// 8 heads of 128: 3024 us whole; cut into 32 the maps take 194, the carry pass
+// 73 and the outputs 118.  20 prompts, 3000 rows the longest, 24 heads of 128 x
 // 64: 216 us whole, 177 cut.  8 prompts of 8192, 32 heads of 64: 562 and 930.)
 static DeltaPlan plan_delta(const lin_shape &s, int dtype, int64_t max_seqlen, int cus)
 {
