@@ -247,19 +247,25 @@ __device__ __forceinline__ float add_zero_times(unsigned bits, float sum)
 template <typename E, int ROWS, int COLS, int PT>
 struct Tile {
     static constexpr int VE = 16 / (int)sizeof(E), PIECES = ROWS * COLS / VE, PER = (PIECES + PT - 1) / PT;
+    // Rows that one resource covers, so that its offsets stay below 2^31 and
+    // kOOB past its end: 64 of 2-byte elements, 32 of 4-byte ones.
+    static constexpr int SPAN = 128 / (int)sizeof(E);
+    static_assert((int64_t)(SPAN - 1) * (kMaxCount - 1) * sizeof(E) + COLS * sizeof(E) <= kOOB, "offsets below 2^31");
+    // rows between a thread's pieces
+    static constexpr int STEP = PT * VE / COLS;
     u32x4 buf[PER];
 
     // Whether piece u of a thread exists.
     static __device__ __forceinline__ bool has(int u, int tid) { return PIECES % PT == 0 || u * PT + tid < PIECES; }
 
     // Rows 0 .. rows-1 and columns 0 .. cols-1 of the matrix at `base`, whose
-    // rows are `ld` elements apart; 0 elsewhere.  At most 64 rows of strides
-    // below 2^24 elements (32 of 4-byte ones): offsets stay below 2^31.
+    // rows are `ld` elements apart (less than 2^24); 0 elsewhere.
     // VEC (ld >= cols, and all on 16 bytes): rows past the last lie past the
     // resource's end, so the offsets are the same for every tile.
     template <bool VEC>
     __device__ __forceinline__ void load(const E *base, int64_t ld, int rows, int cols, int tid)
     {
+        if constexpr (ROWS > SPAN) return load_spans<VEC>(base, ld, rows, cols, tid);
         const int64_t bytes = rows > 0 ? ((rows - 1) * ld + cols) * (int64_t)sizeof(E) : 0;
         if constexpr (VEC) {
             const rsrc_t r = make_rsrc(base, bytes);
@@ -294,6 +300,31 @@ struct Tile {
         }
     }
 
+    // The same for more rows than one resource covers.
+    template <bool VEC>
+    __device__ __forceinline__ void load_spans(const E *base, int64_t ld, int rows, int cols, int tid)
+    {
+        static_assert(sizeof(E) == 4 && 64 * VE <= SPAN * COLS && (STEP % SPAN == 0 || SPAN % STEP == 0),
+                      "a wave's pieces in one span");
+#pragma unroll
+        for (int u = 0; u < PER; ++u) {
+            const int row = u * STEP + tid * VE / COLS, col = tid * VE % COLS;
+            const int span = STEP <= SPAN ? u * STEP / SPAN : __builtin_amdgcn_readfirstlane(row / SPAN);
+            const int at = row - span * SPAN, left = min(rows - span * SPAN, SPAN);
+            const rsrc_t r = make_rsrc(base + span * SPAN * ld, left > 0 ? ((left - 1) * ld + cols) * (int64_t)sizeof(E) : 0);
+            const uint32_t off = (uint32_t)(at * (int)ld + col) * (uint32_t)sizeof(E);
+            const bool on = has(u, tid) && at < left;
+            if constexpr (VEC) {
+                buf[u] = __builtin_bit_cast(u32x4,
+                                            __builtin_amdgcn_raw_buffer_load_b128(r, on && col < cols ? off : kOOB, 0, 0));
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    buf[u][i] = __builtin_amdgcn_raw_buffer_load_b32(r, on && col + i < cols ? off + i * 4u : kOOB, 0, 0);
+            }
+        }
+    }
+
     // The same tile for rows on any alignment, kept as the words that hold it
     // until `place` writes it: an element of 2 bytes may begin in the middle of
     // one, so a piece is five words.  The first and the last of a tile may hold
@@ -307,6 +338,7 @@ struct Tile {
         if constexpr (VEC || sizeof(E) != 2) {
             load<VEC>(base, ld, rows, cols, tid);
         } else {
+            static_assert(ROWS <= SPAN, "one resource");
             const uintptr_t at = reinterpret_cast<uintptr_t>(base);
             const uint32_t skip = (uint32_t)(at & 2);
             const int64_t bytes = rows > 0 ? (((rows - 1) * ld + cols) * 2 + skip + 3) / 4 * 4 : 0;

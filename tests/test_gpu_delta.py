@@ -664,3 +664,34 @@ def test_another_streams_and_devices_tensors_are_refused_or_served():
         ssd.state_reorder(S, ids([[0, 1, 2]]).flatten())
     with pytest.raises(ssd.SsdError):
         ssd.state_reorder(S, ids([[0, 1, 2]]))   # more beams than slots
+
+
+@pytest.mark.parametrize("dtype", [F32, BF, F16])
+@pytest.mark.parametrize("heads,stride", [((1, 1, 33, 20), (1 << 24) - 1), ((1, 2, 40, 24), (1 << 24) - 8),
+                                          ((1, 1, 100, 72), (1 << 24) - 8), ((1, 1, 65, 33), 8521761),
+                                          ((1, 1, 200, 40), (1 << 24) - 8)])
+def test_largest_row_strides(heads, stride, dtype):
+    """Rows as far apart as they may be, other values between them, against the same rows side by side."""
+    G, H, dk, dv = heads
+    T, cu = 97, [0, 20, 97]
+    q, k, v, ld, beta, S = ref.inputs(T, G, H, dk, dv, dtype, True, 12, 2)
+    dy = torch.randn(T, H, dv, generator=torch.Generator().manual_seed(2)).to(dtype)
+    say(f"largest strides {heads} {stride} {dtype}")
+    base, at, far = torch.full((T * stride,), 3.0, dtype=dtype, device="cuda"), 0, []
+    near = [dev(x) for x in (q, k, v, dy, torch.zeros_like(dy))]
+    for x in near:
+        far.append(torch.as_strided(base, x.shape, (stride, x.shape[2], 1), at))
+        far[-1].copy_(x)
+        at += (x[0].numel() + 7) // 8 * 8
+    ld, beta, S, cu = dev(ld), dev(beta), dev(S), ids(cu)
+    got = []
+    for q, k, v, dy, out in (near, far):
+        pool = S.clone()
+        y = ssd.delta_prefill(q, k, v, ld, beta, cu, pool, out=out)
+        got.append([y, pool, *ssd.delta_bwd(q, k, v, ld, beta, cu, dy, states=S, dstates=S)])
+    torch.cuda.synchronize()
+    assert len(got[0]) == 8
+    for i, (a, b) in enumerate(zip(*got)):
+        assert bool(torch.isfinite(a).all()) and torch.equal(a, b), i
+    rows = base.view(T, stride)
+    assert bool((rows[:, at:at + 4096] == 3.0).all())   # nothing written between
