@@ -1134,7 +1134,7 @@ __global__ __launch_bounds__(1024) void k_delta_decay_sum(DeltaBackArgs a)
     }
 }
 
-// A head's dlog_decay where there are no rows.
+// A head's dlog_decay where no sequence has a row.
 __global__ __launch_bounds__(256) void k_delta_no_rows(float *dla, int H)
 {
     const int h = blockIdx.x * 256 + threadIdx.x;
@@ -1253,10 +1253,11 @@ extern "C" int delta_bwd(const lin_shape *shape, int dtype, const lin_strides *s
     if (rc != SSD_OK) return rc;
     if (decay_stride < 0 || decay_stride >= kMaxCount || beta_stride < 0 || beta_stride >= kMaxCount)
         return SSD_ERR_SHAPE;
-    if (s.N == 0 && (decay_by_row || s.T > 0)) return SSD_OK;
+    if (s.N == 0 && decay_by_row) return SSD_OK;
     if (s.N > 0 && !cu_seqlens) return SSD_ERR_NULL;
     if (!dlog_decay && !(decay_by_row && s.T == 0)) return SSD_ERR_NULL;
-    if (s.T > 0 && (!q || !k || !v || !log_decay || !beta || !dy || !dq || !dk || !dv || !dbeta)) return SSD_ERR_NULL;
+    if (s.N > 0 && s.T > 0 && (!q || !k || !v || !log_decay || !beta || !dy || !dq || !dk || !dv || !dbeta))
+        return SSD_ERR_NULL;
     const unsigned e = dtype_size(dtype);
     for (const void *x : {q, k, v, dy, (const void *)dq, (const void *)dk, (const void *)dv})
         if (misaligned(x, e)) return SSD_ERR_ALIGN;
@@ -1314,7 +1315,7 @@ extern "C" int delta_bwd(const lin_shape *shape, int dtype, const lin_strides *s
     a.ids = (int)s.N;
     a.shift = -1;
     hipStream_t st = static_cast<hipStream_t>(stream);
-    if (s.N == 0 || s.T == 0) {   // no rows: nothing but zeros and the last states' gradients
+    if (s.N == 0 || s.T == 0) {   // no sequence has a row: zeros, and the last states' gradients
         if (a.dla) k_delta_no_rows<<<dim3((unsigned)((s.H + 255) / 256)), dim3(256), 0, st>>>(a.dla, (int)s.H);
         if (s.N == 0) return launch_status();
         a.dla = nullptr;

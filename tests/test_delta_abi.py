@@ -174,3 +174,12 @@ def test_gradient_reference_against_differences(by_row):
             num = (loss(**{name: t + h * d}) - loss(**{name: t - h * d})) / (2 * h)
             assert abs(num - float((g[name] * d).sum())) <= 1e-6 * (1 + abs(num)), name
         assert bool((e[name] >= 0).all())
+
+
+@pytest.mark.parametrize("T", [0, 5])
+def test_sum_over_no_sequence_is_written(T):
+    """dlog_decay [H] is an output for a batch without sequences too; nothing else is."""
+    s = LinShapeArg(T, 0, 1, 4, 8, 8, 0)
+    assert call(s, "bwd", ptr=None, by_row=0) == NULL
+    assert call(s, "bwd", ptr=None, by_row=0, dla=P + 1) == ALIGN
+    assert call(s, "bwd", ptr=None, by_row=1) == OK

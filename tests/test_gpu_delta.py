@@ -695,3 +695,17 @@ def test_largest_row_strides(heads, stride, dtype):
         assert bool(torch.isfinite(a).all()) and torch.equal(a, b), i
     rows = base.view(T, stride)
     assert bool((rows[:, at:at + 4096] == 3.0).all())   # nothing written between
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("T,N", [(5, 0), (0, 0), (0, 2), (5, 2)])
+def test_bwd_sums_over_no_rows(T, N, dtype):
+    """dlog_decay [H] is the sum over the sequences' rows, of which there are none, whatever was in `out`."""
+    G, H, dk, dv = 1, 300, 8, 8
+    q, k, v, ld, beta, S = (dev(t) for t in ref.inputs(T, G, H, dk, dv, dtype, False, 3, N))
+    out = [torch.full_like(t, 7.0) for t in (q, k, v, ld, beta, S)]
+    say(f"delta_bwd sums over no rows T {T} N {N} {dtype}")
+    ssd.delta_bwd(q, k, v, ld, beta, ids([0] * (N + 1)), torch.ones_like(v), states=S, dstates=S, out=out)
+    assert bool((out[3] == 0).all())
+    assert all(bool((t == 7.0).all()) for t in (*out[:3], out[4]))   # rows of no sequence, as they were
+    assert torch.equal(out[5], S)
