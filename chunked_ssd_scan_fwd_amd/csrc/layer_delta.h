@@ -44,8 +44,8 @@ struct Pieces {
     static constexpr int UNITS = sizeof(L) == 2 ? 1 : 2;   // 16-byte units of a lane's 8 values
     static constexpr int BYTES = 2 * PARTS * UNITS * 1024;
 };
-// The lane's 8 values of part u of piece t in an image at `p`.
-template <typename L>
+// The lane's 8 values of part u of piece t in an image of PARTS parts at `p`.
+template <typename L, int PARTS = Pieces<L>::PARTS>
 __device__ __forceinline__ Frag<L> piece(const char *p, int t, int u, int lane)
 {
     typedef Pieces<L> P;
@@ -54,7 +54,7 @@ __device__ __forceinline__ Frag<L> piece(const char *p, int t, int u, int lane)
 #pragma unroll
     for (int i = 0; i < P::UNITS; ++i)
         *reinterpret_cast<u32x4 *>(to + 16 * i) =
-            *reinterpret_cast<const u32x4 *>(p + (((t * P::PARTS + u) * P::UNITS + i) * 64 + lane) * 16);
+            *reinterpret_cast<const u32x4 *>(p + (((t * PARTS + u) * P::UNITS + i) * 64 + lane) * 16);
     return r;
 }
 

@@ -32,9 +32,12 @@ namespace layer {
 // For bfloat16 inputs everything that reaches the state keeps float32's
 // accuracy: S, T, the residual V - diag(e^b) K S and U enter their products as
 // sums of three bfloat16 numbers (six products for two such operands, the ones
-// of 2^-24 and less left out).  In y, the scores P enter as one, S and U as
-// two: with S as one too y was 0.0024 from 64 bits, 0.0025 where little of a
-// row's y is its own chunk's, and its own rounding makes 0.0017.
+// of 2^-24 and less left out).  In y the scores P, S and U enter as sums of
+// two, 2^-18 of each term off, where y's own rounding is 2^-9 of their sum: 3 in
+// 1000 values of y round to the neighbour.  Three parts left 2 in 10000 and took
+// 6% more time (16 prompts of 8192 rows, 16 heads of 128: 970 us for 909); P as
+// one part made y 0.0018 to 0.0023 from 64 bits, and its rounding alone is
+// 0.00165.
 constexpr int C = 32;   // rows of a chunk
 
 template <typename E, int KP, int VT>
@@ -43,7 +46,8 @@ struct DeltaLds {
     typedef Pieces<L> PC;
     static constexpr int PAD = sizeof(L) == 2 ? 16 : 4;
     static constexpr int LK = KP + PAD, LV = VT + PAD;
-    static constexpr int PBYTES = PC::BYTES / PC::PARTS;
+    static constexpr int YU = PC::PARTS == 3 ? 2 : 1;   // parts of what y is made of: P, S and U
+    static constexpr int PBYTES = PC::BYTES / PC::PARTS * YU;
     // k a step earlier than q and v, where a third tile of it fits
     static constexpr bool EARLY = KP <= 128 || sizeof(L) == 2;
     static constexpr int KB = EARLY ? 3 : 2;
@@ -96,7 +100,7 @@ __attribute__((amdgpu_waves_per_eu(DeltaPerCu<E, KP, VT>::per_simd, DeltaPerCu<E
     constexpr int LK = Lds::LK, LV = Lds::LV, KB = Lds::KB;
     constexpr bool EARLY = Lds::EARLY;
     constexpr int WAVES = DeltaPerCu<E, KP, VT>::waves, MT = KP / 16, KS = KP / 32;
-    constexpr int PARTS = PC::PARTS, YU = PARTS == 3 ? 2 : 1;
+    constexpr int PARTS = PC::PARTS, YU = Lds::YU;
     constexpr int MOVERS = DeltaPerCu<E, KP, VT>::movers, PT = 64 * MOVERS;   // threads that fetch
     __shared__ __align__(16) Lds lds;
 
@@ -149,7 +153,12 @@ __attribute__((amdgpu_waves_per_eu(DeltaPerCu<E, KP, VT>::per_simd, DeltaPerCu<E
         }
         return x;
     };
-    const auto put_scores = [&](int it, int jt, f32x4 x) { put(lds.p, 1, it, jt, 0, __builtin_convertvector(x, L4)); };
+    const auto put_scores = [&](int it, int jt, f32x4 x) {
+        L4 parts[YU];
+        split4(parts, x);
+#pragma unroll
+        for (int u = 0; u < YU; ++u) put(lds.p, YU, it, jt, u, parts[u]);
+    };
 
     if (wave >= WAVES) {
         // ---- fetches, and T of the next chunk
@@ -294,7 +303,7 @@ __attribute__((amdgpu_waves_per_eu(DeltaPerCu<E, KP, VT>::per_simd, DeltaPerCu<E
         };
         // what a piece on the diagonal holds above it stays 0
         if (w == 0 && !mover) {
-            put(lds.p, 1, 0, 1, 0, L4{});
+            put_scores(0, 1, f32x4{});
             put_t(0, 1, f32x4{});
         }
         if (mover) {   // the decays and P are its own too: wave 0 has P's tile (1, 0), wave 1 those on the diagonal
@@ -505,20 +514,18 @@ __attribute__((amdgpu_waves_per_eu(DeltaPerCu<E, KP, VT>::per_simd, DeltaPerCu<E
 #pragma unroll
         for (int t = 0; t < 2; ++t) Y[t] *= d.in[16 * t + l16] * entered;
         if constexpr (OUT) {
-            Frag<L> fu[YU], fp[2];
+            Frag<L> fu[YU], fp[2][YU];
             split(fu, U[0], U[1]);
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                char *to = reinterpret_cast<char *>(&fp[t]);
+            for (int t = 0; t < 2; ++t)
 #pragma unroll
-                for (int i = 0; i < PC::UNITS; ++i)
-                    *reinterpret_cast<u32x4 *>(to + 16 * i) =
-                        *reinterpret_cast<const u32x4 *>(lds.p + ((t * PC::UNITS + i) * 64 + lane) * 16);
-            }
+                for (int u = 0; u < YU; ++u) fp[t][u] = piece<L, YU>(lds.p, t, u, lane);
 #pragma unroll
-            for (int u = YU - 1; u >= 0; --u)
+            for (int o = YU - 1; o >= 0; --o)   // the small products first
 #pragma unroll
-                for (int t = 0; t < 2; ++t) Y[t] = mma(fu[u], fp[t], Y[t]);
+                for (int u = 0; u <= o; ++u)
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) Y[t] = mma(fu[u], fp[t][o - u], Y[t]);
         }
         Frag<L> fw[PARTS];
         split(fw, U[0] * (*reinterpret_cast<const f32x4 *>(d.out + g4) * unscale),

@@ -453,8 +453,8 @@ int lin_step(const lin_shape *shape, int dtype, const lin_strides *strides,
  *                 are the caller's risk.
  * Rounding: q, k and v in float32 are rounded nowhere.  bfloat16 calls hold
  * the state, u and all that they come from to float32's accuracy; in y the
- * masked scores are rounded to bfloat16 too, and the copies of the state and
- * of u that meet q and them are sums of two bfloat16 numbers.
+ * masked scores, and the copies of the state and of u that meet q and them,
+ * are sums of two bfloat16 numbers (2^-18 of each), and y is rounded once.
  * Infinite and NaN values of a row reach, as in the recurrence, only it and
  * the rows after it in its sequence, and one in v no column but its own; a
  * sequence that holds them is slow from there on, where they reached a state

@@ -709,3 +709,19 @@ def test_bwd_sums_over_no_rows(T, N, dtype):
     assert bool((out[3] == 0).all())
     assert all(bool((t == 7.0).all()) for t in (*out[:3], out[4]))   # rows of no sequence, as they were
     assert torch.equal(out[5], S)
+
+
+@pytest.mark.parametrize("heads,lens,mu", [((2, 4, 128, 128), [600, 33], -4.0), ((1, 2, 64, 128), [300], -4.0),
+                                           ((1, 2, 128, 64), [300], 0.0), ((1, 1, 200, 64), [200], -8.0),
+                                           ((2, 4, 33, 40), [130], -2.0), ((1, 1, 128, 128), [2500], -6.0)])
+def test_prefill_in_bfloat16_rounds_y_once(heads, lens, mu):
+    """Scores, states and u in y are sums of two bfloat16 numbers: 2^-18 off, and in a product of two such sums the
+    least parts' product, 2^-18 at most, is left out.  So y is its own rounding and 3 2^-18 < 2^-16 of its magnitudes
+    from the formula, besides what float32 sums leave."""
+    G, H, dk, dv = heads
+    cu = offsets(lens)
+    q, k, v, ld, beta, S = ref.inputs(cu[-1], G, H, dk, dv, BF, True, 5, len(lens), mu=mu)
+    say(f"delta_prefill rounds y once {heads} {lens}")
+    y = ssd.delta_prefill(*(dev(t) for t in (q, k, v, ld, beta)), ids(cu), dev(S))
+    want, _, ye, _, ym = ref.rule(q, k, v, ld, beta, cu, S)
+    assert beyond(y, want, ref.y_bound(BF, want, ye + 2.0 ** -16 * ym, ym, rounded_inside=False)) <= 1
