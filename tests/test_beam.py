@@ -269,3 +269,35 @@ def test_reorder_off_16_bytes():
     parents = torch.tensor([[3, 2, 1, 0], [0, 0, 0, 0]], dtype=torch.int32)
     ssd.state_reorder(pool, parents.to("cuda"))
     assert torch.equal(pool.cpu(), reordered(S, parents, list(range(8))))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_select_into_its_own_scores(dtype):
+    """The scores of a step in the place of those of the step before."""
+    need_gpu()
+    R, K, V = 5, 4, 9001
+    x, s = rows(R, K, V, dtype, 8)
+    ended = torch.zeros(R, K, dtype=torch.uint8, device="cuda")
+    ended[1, 2] = ended[3] = 1
+    x, s = x.to("cuda"), s.to("cuda")
+    want = ssd.beam_select(x, s, K, ended=ended, end_token=7)
+    out = (s, *(torch.empty(R, K, dtype=torch.int32, device="cuda") for _ in range(2)))
+    got = ssd.beam_select(x, s, K, ended=ended, end_token=7, out=out)
+    assert got[0] is s and all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF, F16])
+@pytest.mark.parametrize("n", [1, 8, 64])
+def test_select_of_masked_pieces(n, dtype):
+    """Masks that leave nothing of a row's first pieces, little of them, or one token at its end."""
+    need_gpu()
+    x, s = rows(3, 2, 40007, dtype, 21)
+    x[0, 0, :30000] = -INF
+    x[0, 1, 5:] = -INF
+    x[1, 0, :40006] = -INF
+    x[1, 1, 2000:39990] = -INF
+    x[2, 0, ::2] = -INF
+    x[2, 1, torch.arange(40007) % 701 != 3] = -INF
+    check_select("masked pieces", x, s, n)

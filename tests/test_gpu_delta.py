@@ -725,3 +725,121 @@ def test_prefill_in_bfloat16_rounds_y_once(heads, lens, mu):
     y = ssd.delta_prefill(*(dev(t) for t in (q, k, v, ld, beta)), ids(cu), dev(S))
     want, _, ye, _, ym = ref.rule(q, k, v, ld, beta, cu, S)
     assert beyond(y, want, ref.y_bound(BF, want, ye + 2.0 ** -16 * ym, ym, rounded_inside=False)) <= 1
+
+
+WHERE = ["q", "k", "v", "beta", "dy", "state", "dstate"]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF, F16])
+@pytest.mark.parametrize("where,bad,by_row", [(w, *c) for w in WHERE for c in ((INF, True), (-INF, True), (INF, False),
+                                                                             (NAN, False))] + [("decay", INF, True)])
+def test_bwd_infinities_stay_in_their_sequence(where, bad, by_row, dtype):
+    """An infinity or a NaN reaches its own sequence's gradients in the heads of its group, and those heads' sums."""
+    G, H, dk, dv = 2, 4, 40, 72
+    cu = [0, 90, 200, 260]
+    q, k, v, ld, beta, S = ref.inputs(260, G, H, dk, dv, dtype, by_row, 9, 3)
+    g = torch.Generator().manual_seed(4)
+    dy, dS = torch.randn(260, H, dv, generator=g).to(dtype), torch.randn(3, H, dk, dv, generator=g)
+    x = {"q": q, "k": k, "v": v, "beta": beta, "decay": ld, "dy": dy, "state": S, "dstate": dS}
+    say(f"delta_bwd {where} {bad} {by_row} {dtype}")
+    run = lambda: [t.cpu() for t in ssd.delta_bwd(dev(q), dev(k), dev(v), dev(ld), dev(beta), ids(cu), dev(dy),   # noqa: E731
+                                                  states=dev(S), dstates=dev(dS))]
+    want = run()
+    t = x[where]
+    if where in ("state", "dstate"):
+        t[1, 1, 3, 5] = bad
+    else:
+        t[131, 0 if where == "q" or where == "k" else 1] = bad
+    got = run()
+    finite = [torch.isfinite(a) for a in got]
+    for i, (a, b, f) in enumerate(zip(got, want, finite)):
+        if i == 5:
+            assert torch.equal(a[[0, 2]], b[[0, 2]]) and torch.equal(a[1, 2:], b[1, 2:])
+        elif i == 3 and not by_row:
+            assert torch.equal(a[2:], b[2:])
+        else:
+            assert torch.equal(a[:90], b[:90]) and torch.equal(a[200:], b[200:])
+            n = a.shape[1] // G   # the other group
+            assert torch.equal(a[:, n:], b[:, n:])
+    assert not all(bool(f.all()) for f in finite)
+    if not by_row:
+        assert not bool(finite[3][:2].all())
+
+
+def test_captured_calls_share_a_workspace():
+    """Two graphs whose calls have one workspace between them, replayed in turn on one stream, against eager results."""
+    heads, lens = (1, 2, 128, 64), [1700, 40]
+    (G, H, dk, dv), T = heads, sum(lens)
+    need = max(ssd.layer.delta_prefill_workspace_size(T, 2, G, H, dk, dv, 2), ssd.layer.delta_bwd_workspace_size(T, 2, G, H, dk, dv),
+               ssd.layer.beam_select_workspace_size(2, 3, 3000, 4))
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+
+    def run(x, ws):
+        q, k, v, ld, beta, cu, S, dy, pool, logits, scores = x
+        pool.copy_(S)
+        y = ssd.delta_prefill(q, k, v, ld, beta, cu, pool, workspace=ws)
+        sel = ssd.beam_select(logits, scores, 4, workspace=ws)
+        return [y, pool, *sel, *ssd.delta_bwd(q, k, v, ld, beta, cu, dy, states=S, dstates=S, workspace=ws)]
+
+    sets = []
+    for s in (1, 2):
+        p = problem(BF, lens, heads, seed=s)
+        g = torch.Generator("cuda").manual_seed(s)
+        sets.append([*p, p[6].clone(), torch.randn(2, 3, 3000, device="cuda", generator=g), torch.zeros(2, 3, device="cuda")])
+    eager = [[t.clone() for t in run(x, None)] for x in sets]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    graphs, outs = [], []
+    with torch.cuda.stream(side):
+        for x in sets:
+            run(x, ws)
+            torch.cuda.synchronize()
+            graphs.append(torch.cuda.CUDAGraph())
+            with torch.cuda.graph(graphs[-1], stream=side):
+                outs.append(run(x, ws))
+    torch.cuda.synchronize()
+    for rep in range(3):
+        ws.fill_(255)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            for out in outs:
+                for t in out:
+                    t.zero_()
+            for i in (0, 1, 1, 0):
+                graphs[i].replay()
+        torch.cuda.synchronize()
+        for i in (0, 1):
+            for j, (a, b) in enumerate(zip(outs[i], eager[i])):
+                assert torch.equal(a, b), (rep, i, j)
+        run(sets[rep % 2], None)   # eager work between
+        torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_calls_follow_the_current_stream(dtype):
+    """Tensors made on the default stream and handed to another one: a call waits for that stream's work alone."""
+    q, k, v, ld, beta, cu, S, dy = problem(dtype, [700, 40], seed=4)
+    x, sc = torch.randn(2, 3, 900, device="cuda").to(dtype), torch.zeros(2, 3, device="cuda")
+
+    def run(v, S, x):
+        pool = S.clone()
+        y = ssd.delta_prefill(q, k, v, ld, beta, cu, pool)
+        z = ssd.delta_step(q[:2], k[:2], v[:2], ld[:2], beta[:2], pool)
+        sel = ssd.beam_select(x, sc, 2)
+        ssd.state_reorder(pool, ids([[1, 0]]))
+        return [y, z, pool, *sel, *ssd.delta_bwd(q, k, v, ld, beta, cu, dy, states=S)]
+
+    want = run(v, S, x)
+    late = [torch.zeros_like(t) for t in (v, S, x)]
+    a = torch.randn(4096, 4096, device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        for _ in range(20):   # what the stream has to do before the inputs are there
+            b = a @ a
+        for t, s in zip(late, (v, S, x)):
+            t.copy_(s)
+        got = run(*late)
+    torch.cuda.synchronize()
+    assert bool(torch.isfinite(b).all())
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
