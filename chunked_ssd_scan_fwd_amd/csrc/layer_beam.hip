@@ -162,13 +162,15 @@ __device__ __forceinline__ bool goes_on(const BeamArgs &a, int row)
 // The largest logit, the sum of exponentials and the n best of a piece of a
 // row, in one pass: a wave to a piece, 2048 logits at a time in registers.
 //
-// Memory bounds it, with about 5 vector instructions a logit beside it, one of
-// them an exponential at a quarter of the rate.  So the candidates have to
-// cost next to nothing: a logit is compared once, with the n-th best so far.
-// For the first 2048 that is the n-th largest of the lanes' own largest ones
-// (at least n logits reach it); the few that reach it go into the list one by
-// one.  256 rows of 131072 bfloat16 logits: 24 us (2.8 TB/s); with each lane's
-// best offered in turn, and sorts through LDS, 33.
+// Vector instructions bound it: 256 rows of 131072 bfloat16 logits take 24 us,
+// where 67 MB are 13.  A SIMD has them under way in 0.7 of that: 15 for 64
+// logits by the counters, one of them an exponential at half the rate.
+// About 11 are every tile's (conversion, largest, the exponential and its sum,
+// the votes), the rest orders and candidates.  So the candidates have to cost
+// little: a logit is compared with the n-th best so far.  For the first 2048
+// that is the n-th largest of the lanes' own largest ones (at least n logits
+// reach it); the few that reach it go into the list one by one.  With each
+// lane's best offered in turn, and sorts through LDS, it took 33.
 template <typename T, bool VEC>
 __global__ __launch_bounds__(BT) void k_beam_rows(BeamArgs a)
 {
@@ -329,8 +331,8 @@ struct ReorderArgs {
 // States of a request's beams, the values of one place (V of them) in a
 // thread for all beams: it has read all before it writes any, so the states
 // can change places with no copy of the pool.  A state that stays is neither
-// read nor written.  Memory bounds it: 64 requests of 4 beams, 1 MB each, 75 us
-// (4.7 TB/s).
+// read nor written.  Memory bounds it: 64 requests of 4 beams, 1 MB each, of
+// which 356 MB move: 74 to 78 us (4.6 to 4.8 TB/s).
 template <int KM, int V>
 __global__ __launch_bounds__(BT) void k_state_reorder(ReorderArgs a)
 {
@@ -386,8 +388,9 @@ struct BeamPlan {
 };
 
 // Tiles of a wave: as many as leave 16 waves for every CU, 8 at most.  (256 rows
-// of 131072 logits: 35 us, one each 46; 4 of 32001: one each 18 us, 8 each 34,
-// for a wave's tiles come one after the other.)
+// of 131072 logits: 4 each 36 us, one 47, 8 35, in float32 44, 50 and 39; 4 rows
+// of 32001: one each 17 us, 8 each 33, for a wave's tiles come one after the
+// other.)
 static BeamPlan plan_beam(const beam_shape &s, int cus)
 {
     BeamPlan P;
@@ -497,9 +500,10 @@ extern "C" int state_reorder(const state_reorder_shape *shape, const int32_t *pa
     a.state = s.H * s.dk * s.dv;
     hipStream_t st = static_cast<hipStream_t>(stream);
     // A place of all beams is in registers: four values of up to 16 beams, or one
-    // of up to 64 (states of 1 MB: 64 requests of 4 beams 43 us, 576 with one
-    // value and room for 64; 16 of 16 beams 55 and 176).  Room for 4 or 8 beams
-    // where that is enough: 43 and 51 us, with 16's 45 and 52.
+    // of up to 64.  States of 1 MB that no cache holds, at random parents: 64
+    // requests of 4 beams (340 MB move) 72 us, 578 with one value and room for 64;
+    // 16 of 16 beams (415 MB) 98 and 178.  Room for 4 or 8 beams where that is
+    // enough: 64 of 4 72 us, with 16's 73; 32 of 8 (397 MB) 88 and 97.
     const bool vec = a.state % 4 == 0 && !misaligned(states, 16);
     if (!vec) {
         if (a.K <= 8) launch_reorder<8, 1>(a, st);

@@ -18,9 +18,9 @@ namespace layer {
 // (512 rows, 8 heads: 43 us so, and 39.5).
 // T in a kernel of its own beforehand cost 460 us beside the large batch's 721
 // (16 prompts of 8192 rows, 16 heads of 128), and 18 KB of memory a chunk and
-// head; so the batch takes 904 to 931 us.  There a chunk takes a CU 6900 cycles,
-// of which a SIMD has vector instructions under way in 0.55 (S in parts is anew
-// for every chunk) and matrix ones in 0.39: little is left to fill.
+// head; so the batch takes 909 us.  There a chunk takes a CU 6930 cycles, of
+// which a SIMD has vector instructions under way in 0.56 (S in parts is anew for
+// every chunk) and matrix ones in 0.40: little is left to fill.
 //
 // Chunks of 64 rows, whose S is split half as often, took as long (935): P and
 // T have twice the products for a row then, and four waves that both fetch and
@@ -78,6 +78,8 @@ __device__ __forceinline__ float row_of_lanes(float x)
     return __uint_as_float(halves[N >> 1]);
 }
 
+// Two blocks of eight waves leave a wave 128 registers; with q's, k's and v's
+// tiles on their way the 64-column kernel for dk over 64 spills 18 of them.
 template <typename E, int KP, int VT>
 struct DeltaPerCu {
     static constexpr int n = VT == 64 && KP <= 128 && std::is_same<E, bf16>::value ? 2 : 1;
@@ -692,12 +694,12 @@ __global__ __launch_bounds__(64 * CarryWaves<KP>::n) void k_delta_carry(DeltaArg
 // ---- host side
 
 // Columns of a block: 64 where that leaves a block a CU of its own, whose chain
-// of chunks is then shorter (512 rows, 8 heads of 128: bfloat16 43 us where 128
-// columns take 56; float32 104 and 154), and with bfloat16's and dk <= 64's few
+// of chunks is then shorter (512 rows, 8 heads of 128: bfloat16 40 us where 128
+// columns take 54; float32 108 and 158), and with bfloat16's and dk <= 64's few
 // registers and LDS, where two of them share one (8 prompts of 8192 rows, 16
-// heads of 64 x 128: 548 and 668).  Else 128, for T and P are then made half as
-// often (16 x 8192 rows, 16 heads of 128: 946 and 1088; float32, 2 x 8192: 780
-// and 1017).  Long sequences count as the pieces that they can be cut into.
+// heads of 64 x 128: 510 and 604).  Else 128, for T and P are then made half as
+// often (16 x 8192 rows, 16 heads of 128: 909 and 1060; float32, 2 x 8192: 746
+// and 964).  Long sequences count as the pieces that they can be cut into.
 static int col_tile(const lin_shape &s, int dtype, int cus)
 {
     if (s.dk > 128 || s.dv <= 64) return 64;
@@ -717,9 +719,10 @@ struct DeltaPlan {
 // rows over the places; cut, the output pass's rows and, for 0.7 of its time
 // each, those of the blocks for B and M, with 1.2 us for each segment that the
 // carry pass joins and 15 us for two launches more.  (One prompt of 32768 rows,
-// 8 heads of 128: 3024 us whole; cut into 32 the maps take 194, the carry pass
-// 73 and the outputs 118.  20 prompts, 3000 rows the longest, 24 heads of 128 x
-// 64: 216 us whole, 177 cut.  8 prompts of 8192, 32 heads of 64: 562 and 930.)
+// 8 heads of 128: 2965 us whole; cut into 32, 355, of which the maps take 195,
+// the carry pass 74 and the outputs 118.  20 prompts, 3000 rows the longest, 24
+// heads of 128 x 64: 210 us whole, 166 cut.  8 prompts of 8192, 32 heads of 64:
+// 470 whole, 900 cut.)
 static DeltaPlan plan_delta(const lin_shape &s, int dtype, int64_t max_seqlen, int cus)
 {
     DeltaPlan P;

@@ -190,7 +190,9 @@ struct WalkLds {
 // in the registers of four waves, 16 columns each, while four others fetch the
 // next chunk.  BACK: from the last chunk to the first.  Its chain of dependent
 // steps bounds it, about 3 us a chunk: a SIMD has matrix instructions under way
-// in 0.2 of that and vector ones in 0.3.
+// in 0.2 of that and vector ones in 0.3.  Sequences are not cut, so one of 32768
+// rows with 8 heads of 128 takes 2.9 ms on 32 CUs.  For dk over 128 it spills 39
+// to 63 registers.
 template <typename E, int KP, bool VEC, bool BACK>
 __device__ __forceinline__ void walk(const DeltaBackArgs &a, WalkLds<E, KP> &lds, int n, int h, int tile)
 {
@@ -734,8 +736,8 @@ __global__ __launch_bounds__(64 * GradsLds<KP>::WAVES) void k_delta_grads(DeltaB
 // the other in one place, and q and k take it over after them, so that two
 // blocks share a CU and fill each other's waits (one block of eight waves with
 // a place for each took 272 us for the training case, this 243; its waves wait
-// in 0.6 of their cycles still, for barriers and loads, and loads further ahead
-// spill registers: 307).
+// in 0.6 of their cycles still, for barriers and loads.  For dk over 64 it
+// spills 37 registers as it is; loads further ahead spill more: 307).
 template <int KP>
 struct GradsBfLds {
     static constexpr int CB = 64, WAVES = 4, SL = 32, TT = 4, TILES = 10;

@@ -10,9 +10,12 @@
 //
 // The states go past the caches: by a next step the other layers' have taken
 // their place.  Over 3 GB of layers, each with 16 rows of 16 heads of 128 x 128,
-// 7.9 us a call, and through the caches 10.7; with 128 rows 50 and 60.
+// 7.8 us a call, and through the caches 10.7; with 128 rows 49 and 59.  A small
+// model, whose states all stay in the last cache, gains too: 117 MB of layers of
+// 16 rows 8.4 and 9.8, 34 MB of layers of one row of 8 heads 3.8 and 4.3.
 //
-// 256 rows (537 MB): 96 us, 5.6 TB/s; one row of 8 heads 3.8 us.
+// Captured calls on such layers, 256 rows (537 MB): 96 us, 5.6 TB/s.  One after
+// the other from Python, with new inputs, 109 us (4.9 TB/s).
 #include "layer_device.h"
 #include "ssd_internal.h"
 
@@ -151,8 +154,8 @@ static void launch_rows(DeltaStepArgs &a, hipStream_t st)
 }
 
 // Columns of a block: 64 where that makes a block for every CU, else 32.  (16
-// heads of 128 x 128: 64 rows 25.7 us with 64, 26.9 with 32, 256 rows 95 and
-// 102; one row of 8 heads 4.7 and 4.4.)
+// heads of 128 x 128, captured: 64 rows 24.6 us with 64, 27.7 with 32, 256 rows
+// 96 and 104; one row of 8 heads 4.1 and 3.8.)
 template <typename T>
 static void launch_delta_step(DeltaStepArgs &a, int cus, hipStream_t st)
 {

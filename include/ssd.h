@@ -478,15 +478,20 @@ int delta_step(const lin_shape *shape, int dtype, const lin_strides *strides,
  * delta_prefill of the same batch, in which sequence n starts from states[n]
  * (NULL: from zero): dq, dk [T][G][dk] (summed over the heads of a group) and
  * dv [T][H][dv], dense, of the type `dtype`; dlog_decay, rows of H where
- * decay_by_row is not 0, else [H], summed over all rows (in 64 bits, in a
- * fixed order); dbeta [T][H]; dstates [N][H][dk][dv], or NULL if not wanted.
- * states and dstates_last are float32 [N][H][dk][dv] or NULL; the strides of
- * y are dy's, and may be 0 here.  shape->slots is not read.  Rows of no
- * sequence are not read; their gradients are left as they were, or, where
- * `clear` is not 0 and there is a sequence, set to zero.
+ * decay_by_row is not 0, else [H], summed over the sequences' rows (in 64 bits,
+ * in a fixed order; 0 where there are none); dbeta [T][H]; dstates
+ * [N][H][dk][dv], or NULL if not wanted.  states and dstates_last are float32
+ * [N][H][dk][dv] or NULL; the strides of y are dy's, and may be 0 here.
+ * shape->slots is not read.  Rows of no sequence are not read; their gradients
+ * are left as they were, or, where `clear` is not 0 and there is a sequence,
+ * set to zero.
  * Every sum and every value between is float32, or three bfloat16 numbers
- * that hold one; nothing of a forward call is needed.  The states of every
- * 64th row (32nd for dk over 128) are kept in the workspace meanwhile, twice.
+ * that hold one, but for bfloat16 calls with dk up to 128: there dP and dM, the
+ * gradients of the chunks' score matrices, meet k and q for dq and dk (and
+ * nothing else) as sums of two bfloat16 numbers, 2^-18 of each term off where
+ * the rounding of dq and dk is 2^-9.  Nothing of a forward call is needed.  The
+ * states of every 64th row (32nd for dk over 128) are kept in the workspace
+ * meanwhile, twice.
  * An infinity or a NaN reaches gradients of its sequence in the heads of its
  * group, and dlog_decay of those heads where that is a sum, no others; where
  * the formulas give an infinity, NaN may stand.
@@ -611,7 +616,8 @@ int beam_select(const beam_shape *shape, int dtype, const void *logits, int64_t 
  * that is negative or does not exist, leaves its state as it was; a parent
  * that does not exist (or whose slot does not) makes it NaN; of beams with one
  * slot the last counts.  A request that has a slot of an earlier request of
- * the call is left as it was.
+ * the call, be it one that does not exist, is left as it was: beams that are
+ * there for the shape's sake take negative slots.
  * 1 <= beams <= BEAM_MAX; 1 <= dk, dv <= 256; requests and slots < 2^24. */
 typedef struct state_reorder_shape {
     int64_t requests, beams, slots, H, dk, dv;
