@@ -301,3 +301,20 @@ def test_select_of_masked_pieces(n, dtype):
     x[2, 0, ::2] = -INF
     x[2, 1, torch.arange(40007) % 701 != 3] = -INF
     check_select("masked pieces", x, s, n)
+
+
+@pytest.mark.gpu
+def test_reorder_with_beams_for_the_shapes_sake():
+    """Negative slots stand for no beam in any number of requests; one that does not exist counts as a slot of both."""
+    need_gpu()
+    S = torch.randn(8, 2, 4, 6, generator=torch.Generator().manual_seed(1))
+    parents = torch.tensor([[1, 0, -1], [1, 0, -1], [1, 0, 2], [1, 0, 2]], dtype=torch.int32)
+    for pad, served in ((-1, (0, 1, 2, 3)), (-7, (0, 1, 2, 3)), (8, (0,)), (1 << 30, (0,))):
+        slots = [x for r in range(4) for x in (2 * r, 2 * r + 1, pad)]
+        want = S.clone()
+        for r in served:
+            want[[2 * r, 2 * r + 1]] = S[[2 * r + 1, 2 * r]]
+        assert torch.equal(reordered(S, parents, slots), want)
+        pool = S.to("cuda")
+        ssd.state_reorder(pool, parents.to("cuda"), slots=torch.tensor(slots, dtype=torch.int32, device="cuda"))
+        assert torch.equal(pool.cpu(), want)
